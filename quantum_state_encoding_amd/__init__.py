@@ -22,7 +22,8 @@ __all__ = ["Plan", "FwtError", "execute", "stream_copy", "library_path", "load_l
            "PATH_AUTO", "PATH_SINGLE_BLOCK", "PATH_MULTIPASS", "PATH_MFMA_ABLATION",
            "FWT_OK", "FWT_EINVAL", "FWT_EALIGN", "FWT_EUNSUPPORTED", "FWT_EHIP",
            "FWT_ENOMEM", "FWT_ESCRATCH", "STATIC_SCRATCH_BYTES", "ablation_execute_static",
-           "EXPORTED_SYMBOLS", "workspace_status"]
+           "EXPORTED_SYMBOLS", "workspace_status", "rotate_quantize", "scaled_matmul",
+           "gated_ffn", "gated_ffn_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfwt.so")
@@ -547,3 +548,6 @@ def stream_copy(dst, src, stream=None):
     if st != FWT_OK:
         raise FwtError(st, "fwt_stream_copy")
     return dst
+
+
+from .ffn import gated_ffn, gated_ffn_backward, rotate_quantize, scaled_matmul  # noqa: E402

@@ -15,9 +15,12 @@ LIB = os.path.join(PKG, "libfwt.so")
 OBJDIR = os.path.join(PKG, "_build")
 SOURCES = [os.path.join(CSRC, f) for f in ("fwt_kernels.hip", "fwt_onepass.hip",
                                            "fwt_ablation.hip", "fwt_ozaki.hip",
-                                           "fwt_static.hip", "fwt_api.cpp")]
+                                           "fwt_static.hip", "fwt_api.cpp",
+                                           "ffn_rotate.hip", "ffn_matmul.hip", "ffn_strip.hip",
+                                           "ffn_api.cpp")]
 HEADERS = [os.path.join(CSRC, "fwt_internal.h"), os.path.join(CSRC, "fwt_device.h"),
-           os.path.join(ROOT, "include", "fwt.h")]
+           os.path.join(CSRC, "ffn_internal.h"), os.path.join(CSRC, "ffn_device.h"),
+           os.path.join(ROOT, "include", "fwt.h"), os.path.join(ROOT, "include", "fwt_ffn.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

@@ -1,0 +1,83 @@
+// Internal interface between the feed-forward entry points (ffn_api.cpp)
+// and their gfx950 kernels (ffn_rotate.hip, ffn_matmul.hip,
+// ffn_strip.hip).  Not installed; not part of the C ABI.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+#include <stdint.h>
+
+namespace qse {
+
+constexpr int kFfnBlock = 128;        // contraction elements that share a scale
+constexpr int kFfnMaxBits = 14;       // log2 of the largest rotation
+constexpr int kFfnMaxBitsT = 7;       // the same, for a transposed input
+
+// Element types, as fwt_ffn_dtype numbers them.
+// kTE4m3Exact: e4m3 operands whose products and sums keep 32 bits.
+enum FfnType : int { kTBf16 = 0, kTF16 = 1, kTF32 = 2, kTE4m3 = 3, kTE4m3Exact = 4 };
+
+// Largest row stride of a product's operand, in bytes: 256 rows of a tile
+// stay within a 32-bit offset of its first one.
+constexpr int64_t kFfnMaxStride = (int64_t)1 << 23;
+
+// What a product's epilogue does with its accumulators.
+enum FfnEpilogue : int {
+    kEpStore = 0,     // C = A B^T
+    kEpGate = 1,      // C = act(A B0^T) * (A B1^T)
+    kEpGateGrad = 2,  // the gradients of A B0^T and A B1^T from that of C
+};
+
+// One product A B^T (A: m x k, B: n x k, both with k contiguous), or two
+// that share A.  Strides of a and b in bytes, of the others in elements.
+struct ProductArgs {
+    const void* a;
+    const void* b0;
+    const void* b1;         // the up projection (kEpGate, kEpGateGrad)
+    int64_t lda, ldb0, ldb1;
+    int64_t m, n;
+    int64_t kbytes;         // bytes of a row that are contracted
+    const float* sa;        // e4m3: scales [k block][m]
+    const float* sb0;       // scales [k block][sb_n]
+    const float* sb1;
+    int64_t sb_n;           // n (one for each row of B) or ceil(n / 128)
+    void* c;                // m x n; kEpGateGrad: m x 2n, dg beside du
+    int64_t ldc;
+    int ctype;
+    const void* dh;         // kEpGateGrad: gradient of C, m x n
+    int64_t lddh;
+    int act;                // 0 silu, 1 gelu
+    int tiles_m, tiles_n;   // set by the launcher
+};
+
+// Enqueue a product.  type: element type of A and B; row_scales: e4m3 with
+// a scale for each row of B.
+hipError_t launch_product(const ProductArgs& p, int type, int epilogue, bool row_scales,
+                          hipStream_t stream);
+// Its form for few rows of A (kEpStore: e4m3 only).
+constexpr int kStripRows = 64;
+hipError_t launch_strip(const ProductArgs& p, int type, int epilogue, bool row_scales,
+                        hipStream_t stream);
+
+// dst (cols x rows, stride ldd) = src (rows x cols, stride lds)^T, 16-bit.
+hipError_t launch_transpose16(const void* src, int64_t lds, void* dst, int64_t ldd, int64_t rows,
+                              int64_t cols, hipStream_t stream);
+
+// Zeros to rows x cols 16-bit elements.
+hipError_t launch_zero16(void* dst, int64_t ld, int64_t rows, int64_t cols, hipStream_t stream);
+
+struct RotateArgs {
+    const void* x;          // m x k, or k x m when transposed
+    int64_t ldx;            // elements
+    int64_t m, k;
+    int bits;
+    uint8_t* q;             // m x k codes
+    int64_t ldq;            // bytes
+    float* s;               // scales
+    float* amax;            // tile scales of long rotations: workspace [k block][m]
+};
+hipError_t launch_rotate(const RotateArgs& p, int type, bool tile, bool transpose,
+                         hipStream_t stream);
+// Bytes of RotateArgs::amax that the call needs.
+size_t rotate_workspace(int64_t m, int64_t k, int bits, bool tile, bool transpose);
+
+}  // namespace qse

@@ -1,0 +1,221 @@
+// Products of few rows: A B^T (and the gated block) for m up to 64.
+//
+// The rows of B are read once and bound the time, so a workgroup takes 16 of
+// them (16 of each projection) and all of A, its waves take the 128-byte
+// steps of k in turn, straight from memory into the matrix instructions'
+// registers, and one sum over the waves in LDS, in a fixed order, joins them.
+#include <hip/hip_runtime.h>
+
+#include "ffn_device.h"
+
+namespace qse {
+namespace {
+
+constexpr int kStep = 128;   // bytes of k per step
+
+// Sixteen bytes at any address.
+__device__ __forceinline__ v4i load16(const char* p)
+{
+    struct __attribute__((packed)) Any {
+        v4i v;
+    };
+    return ((const Any*)p)->v;
+}
+
+// The same, of a row that ends `left` bytes on: 0 from there.
+__device__ __forceinline__ v4i load16_tail(const char* p, int left)
+{
+    if (left >= 16)
+        return load16(p);
+    v4i v = v4i{0, 0, 0, 0};
+#pragma unroll
+    for (int b = 0; b < 16; ++b)
+        if (b < left)
+            v[b >> 2] |= (int)((unsigned)(unsigned char)p[b] << (8 * (b & 3)));
+    return v;
+}
+
+template <int TYPE, int MT, int W, int EP, int SM>
+__global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
+{
+    constexpr int P = EP == kEpStore ? 1 : 2;    // projections
+    constexpr int U = MT * P > 2 ? 2 : 4;        // steps in flight
+    extern __shared__ __align__(16) unsigned char lds[];
+    float* red = (float*)lds;                    // [W][P][MT][4][64]
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int q = lane >> 4, l16 = lane & 15;
+    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t nl = n0 + l16 < p.n ? n0 + l16 : p.n - 1;   // past the end: the last row
+    const char* bp[P];
+    bp[0] = (const char*)p.b0 + nl * p.ldb0 + q * 16;
+    if constexpr (P == 2)
+        bp[1] = (const char*)p.b1 + nl * p.ldb1 + q * 16;
+    const char* ap[MT];
+    int mr[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) {
+        mr[i] = i * 16 + l16 < p.m ? i * 16 + l16 : (int)p.m - 1;
+        ap[i] = (const char*)p.a + mr[i] * p.lda + q * 16;
+    }
+    int64_t sbn[4];
+#pragma unroll
+    for (int r = 0; r < 4; ++r) {
+        const int64_t n = n0 + q * 4 + r < p.n ? n0 + q * 4 + r : p.n - 1;
+        sbn[r] = SM == 1 ? n / kFfnBlock : n;
+    }
+    v4f acc[P][MT];
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+            acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
+
+    auto add = [&](const v4i (&b)[P][2], const v4i (&a)[MT][2], int64_t kt) {
+        float s[P][4], sa[MT];
+        if constexpr (SM != 0) {
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                sa[i] = p.sa[kt * p.m + mr[i]];
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    s[j][r] = SM == 1 && r ? s[j][0]
+                                           : (j ? p.sb1 : p.sb0)[kt * p.sb_n + sbn[r]];
+        }
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+#pragma unroll
+            for (int i = 0; i < MT; ++i) {
+                if constexpr (SM == 0) {
+                    acc[j][i] = matrix_step<TYPE>(b[j], a[i], acc[j][i]);
+                } else {
+                    const v4f t = matrix_step<TYPE>(b[j], a[i], v4f{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        acc[j][i][r] = __builtin_fmaf(t[r], sa[i] * s[j][r], acc[j][i][r]);
+                }
+            }
+    };
+
+    const int64_t full = p.kbytes / kStep;
+    int64_t kt = wave;
+    for (; kt + (U - 1) * W < full; kt += U * W) {
+        v4i b[U][P][2], a[U][MT][2];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    b[u][j][h] = load16(bp[j] + (kt + u * W) * kStep + h * 64);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    a[u][i][h] = load16(ap[i] + (kt + u * W) * kStep + h * 64);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            add(b[u], a[u], kt + u * W);
+    }
+    for (; kt * kStep < p.kbytes; kt += W) {
+        v4i b[P][2], a[MT][2];
+        const int left = (int)(p.kbytes - kt * kStep < kStep ? p.kbytes - kt * kStep : kStep) - q * 16;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+#pragma unroll
+            for (int j = 0; j < P; ++j)
+                b[j][h] = load16_tail(bp[j] + kt * kStep + h * 64, left - h * 64);
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+                a[i][h] = load16_tail(ap[i] + kt * kStep + h * 64, left - h * 64);
+        }
+        add(b, a, kt);
+    }
+
+#pragma unroll
+    for (int j = 0; j < P; ++j)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+                red[(((wave * P + j) * MT + i) * 4 + r) * 64 + lane] = acc[j][i][r];
+    __syncthreads();
+    const bool bf = p.ctype == kTBf16;
+    for (int t = threadIdx.x; t < MT * 256; t += 64 * W) {
+        // results of one row of A side by side: n on the lowest bits
+        const int nn = t & 15, mm = t >> 4;
+        const int i = mm >> 4, at = (nn >> 2) * 16 + (mm & 15), r = nn & 3;
+        float s[P];
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+            s[j] = 0.f;
+#pragma unroll
+            for (int w = 0; w < W; ++w)
+                s[j] += red[(((w * P + j) * MT + i) * 4 + r) * 64 + at];
+        }
+        const int64_t n = n0 + nn;
+        if (mm >= p.m || n >= p.n)
+            continue;
+        float v = s[0];
+        if constexpr (EP == kEpGate) {
+            float d;
+            activation(p.act, s[0], v, d);
+            v *= s[P - 1];
+        }
+        const int64_t o = mm * p.ldc + n;
+        if (p.ctype == kTF32)
+            ((float*)p.c)[o] = v;
+        else
+            ((unsigned short*)p.c)[o] = to16(v, bf);
+    }
+}
+
+template <int TYPE, int MT, int EP, int SM>
+hipError_t run(const ProductArgs& p, hipStream_t stream)
+{
+    constexpr int W = MT > 2 ? 8 : 16;
+    constexpr int P = EP == kEpStore ? 1 : 2;
+    constexpr size_t kLds = (size_t)W * P * MT * 4 * 64 * 4;
+    static_assert(kLds <= 65536, "dynamic LDS without an attribute");
+    hipLaunchKernelGGL((strip_kernel<TYPE, MT, W, EP, SM>), dim3((unsigned)((p.n + 15) / 16)),
+                       dim3(64 * W), kLds, stream, p);
+    return hipGetLastError();
+}
+
+template <int TYPE, int EP, int SM>
+hipError_t pick(const ProductArgs& p, hipStream_t stream)
+{
+    if (p.m <= 16)
+        return run<TYPE, 1, EP, SM>(p, stream);
+    if (p.m <= 32)
+        return run<TYPE, 2, EP, SM>(p, stream);
+    return run<TYPE, 4, EP, SM>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_strip(const ProductArgs& p, int type, int ep, bool row_scales,
+                        hipStream_t stream)
+{
+    if (type == kTE4m3 && p.ctype == kTF32) {
+        if (ep == kEpGate)
+            return pick<kTE4m3Exact, kEpGate, 1>(p, stream);
+        return row_scales ? pick<kTE4m3Exact, kEpStore, 2>(p, stream)
+                          : pick<kTE4m3Exact, kEpStore, 1>(p, stream);
+    }
+    if (type == kTE4m3) {
+        if (ep == kEpGate)
+            return pick<kTE4m3, kEpGate, 1>(p, stream);
+        return row_scales ? pick<kTE4m3, kEpStore, 2>(p, stream)
+                          : pick<kTE4m3, kEpStore, 1>(p, stream);
+    }
+    if (type == kTBf16)
+        return pick<kTBf16, kEpGate, 0>(p, stream);
+    return pick<kTF16, kEpGate, 0>(p, stream);
+}
+
+}  // namespace qse

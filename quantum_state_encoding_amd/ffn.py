@@ -1,0 +1,268 @@
+"""The feed-forward block around the Walsh-Hadamard rotation, in 8 and 16 bits.
+
+Bindings of ``include/fwt_ffn.h``: rotation with quantisation to e4m3, the
+product of two quantised operands, the gated block and its gradients.  Like
+the rest of the package they only marshal arguments; outputs and scratch are
+torch allocations on the call's stream.
+
+Example (one feed-forward block of a served model; weights prepared once)::
+
+    wq, ws = qse.rotate_quantize(w_down, bits=12, scales="tile")
+    h = qse.gated_ffn(x, w_gate, w_up)                  # bf16
+    hq, hs = qse.rotate_quantize(h, bits=12)
+    y = qse.scaled_matmul(hq, hs, wq, ws)               # h w_down^T
+"""
+import contextlib
+import ctypes
+
+import quantum_state_encoding_amd as _qse
+
+__all__ = ["rotate_quantize", "scaled_matmul", "gated_ffn", "gated_ffn_backward",
+           "ROTATE_MAX_BITS", "ROTATE_MAX_BITS_T", "FFN_SYMBOLS"]
+
+ROTATE_MAX_BITS, ROTATE_MAX_BITS_T = 14, 7   # FWT_ROTATE_MAX_BITS, .._T
+BLOCK = 128                                  # elements of k that share a scale
+
+# Every symbol include/fwt_ffn.h declares.
+FFN_SYMBOLS = ("fwt_rotate_quantize_workspace", "fwt_rotate_quantize", "fwt_scaled_matmul",
+               "fwt_gated_ffn", "fwt_gated_ffn_backward_workspace", "fwt_gated_ffn_backward")
+
+_SCALES = {"row": 0, "tile": 1}
+_ACTS = {"silu": 0, "gelu": 1}
+_lib = None
+_types = None
+
+
+def _load():
+    global _lib, _types
+    if _lib is None:
+        import torch
+        lib = _qse.load_library()
+        vp, i32, i64, sz = ctypes.c_void_p, ctypes.c_int, ctypes.c_int64, ctypes.c_size_t
+        psz = ctypes.POINTER(sz)
+        lib.fwt_rotate_quantize_workspace.argtypes = [i64, i64, i32, i32, i32, psz]
+        lib.fwt_rotate_quantize.argtypes = [vp, i32, i64, i64, i64, i32, i32, i32, vp, i64, vp,
+                                            vp, sz, vp]
+        lib.fwt_scaled_matmul.argtypes = [vp, i64, vp, vp, i64, vp, i32, i64, i64, i64, vp, i32,
+                                          i64, vp]
+        lib.fwt_gated_ffn.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, vp, i32, i64, i64, i64,
+                                      i32, vp, i32, i64, vp]
+        lib.fwt_gated_ffn_backward_workspace.argtypes = [i64, i64, i64, psz]
+        lib.fwt_gated_ffn_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i32, i64, i64,
+                                               i64, i32, vp, i64, vp, i64, vp, i64, vp, sz, vp]
+        for name in FFN_SYMBOLS:
+            getattr(lib, name).restype = i32
+        _types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+        _lib = lib
+    return _lib
+
+
+def _matrix(t, name, dtypes=None):
+    """Checks a 2-d operand; returns its row stride in elements."""
+    import torch
+    if t.dim() != 2:
+        raise ValueError("%s must have two dimensions" % name)
+    if dtypes is not None and t.dtype not in dtypes:
+        raise ValueError("%s must be one of %s" % (name, ", ".join(str(d) for d in dtypes)))
+    if not t.is_cuda:
+        raise ValueError("%s must be a device tensor" % name)
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current device" % name)
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError("the last dimension of %s must be contiguous" % name)
+    if rows > 1:
+        ld = t.stride(0)
+        if ld < cols:
+            raise ValueError("the rows of %s overlap" % name)
+        return ld
+    return -(-cols // 16) * 16
+
+
+def _scales_of(s, name, blocks, rows, kinds):
+    """Checks a scale array; returns its kind ("row" or "tile")."""
+    import torch
+    if s.dtype != torch.float32 or not s.is_contiguous() or s.dim() != 2:
+        raise ValueError("%s must be a contiguous float32 matrix" % name)
+    if not s.is_cuda or s.device.index != torch.cuda.current_device():
+        raise ValueError("%s must be on the current device" % name)
+    shapes = {"row": (blocks, rows), "tile": (blocks, -(-rows // BLOCK))}
+    for kind in kinds:
+        if tuple(s.shape) == shapes[kind]:
+            return kind
+    raise ValueError("%s must have shape %s, not %s"
+                     % (name, " or ".join(str(shapes[k]) for k in kinds), tuple(s.shape)))
+
+
+def _on(stream):
+    """(stream handle, a context in which torch allocates for that stream)."""
+    import torch
+    if stream is None:
+        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), contextlib.nullcontext()
+    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
+
+
+def _result(out, name, rows, cols, dtype, device):
+    """The output tensor and its row stride."""
+    import torch
+    if out is None:
+        return torch.empty((rows, cols), dtype=dtype, device=device), cols
+    if tuple(out.shape) != (rows, cols):
+        raise ValueError("%s must have shape %s" % (name, (rows, cols)))
+    return out, _matrix(out, name, (dtype,))
+
+
+def _raise(status, what):
+    if status != _qse.FWT_OK:
+        raise _qse.FwtError(status, what)
+
+
+def _act(act):
+    if act not in _ACTS:
+        raise ValueError("act must be 'silu' or 'gelu'")
+    return _ACTS[act]
+
+
+def _scratch(nbytes, device):
+    import torch
+    if not nbytes:
+        return None, None
+    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
+    return ws, ctypes.c_void_p(ws.data_ptr())
+
+
+def rotate_quantize(x, bits=0, scales="row", transpose=False, stream=None):
+    """e4m3 codes and scales of ``x (I (x) H_bits) 2^(-bits/2)``.
+
+    ``x`` is (m, k), or (k, m) with ``transpose``; bf16, f16 or f32.
+    ``scales`` "row" gives one scale for 128 elements of a row, shape
+    (ceil(k/128), m); "tile" one for 128 rows of them, shape
+    (ceil(k/128), ceil(m/128)).  Returns (codes, scales): codes are
+    float8_e4m3fn of shape (m, k), in rows padded with zeros to a multiple of
+    16 bytes.  See fwt_rotate_quantize.
+    """
+    import torch
+    lib = _load()
+    if scales not in _SCALES:
+        raise ValueError("scales must be 'row' or 'tile'")
+    ld = _matrix(x, "x", (torch.bfloat16, torch.float16, torch.float32))
+    m, k = x.shape[::-1] if transpose else x.shape
+    kind, bits, t = _SCALES[scales], int(bits), 1 if transpose else 0
+    need = ctypes.c_size_t(0)
+    if kind and bits > ROTATE_MAX_BITS_T:
+        _raise(lib.fwt_rotate_quantize_workspace(m, k, bits, kind, t, ctypes.byref(need)),
+               "fwt_rotate_quantize_workspace")
+    handle, where = _on(stream)
+    with where:
+        ldq = -(-k // 16) * 16
+        codes = torch.empty((m, ldq), dtype=torch.float8_e4m3fn, device=x.device)
+        s = torch.empty((-(-k // BLOCK), -(-m // BLOCK) if kind else m), dtype=torch.float32,
+                        device=x.device)
+        ws, wp = _scratch(need.value, x.device)
+    _raise(lib.fwt_rotate_quantize(x.data_ptr(), _types[x.dtype], m, k, ld, t, bits, kind,
+                                   codes.data_ptr(), ldq, s.data_ptr(), wp, need.value, handle),
+           "fwt_rotate_quantize")
+    return (codes if ldq == k else codes[:, :k]), s
+
+
+def scaled_matmul(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=None):
+    """``a b^T`` of e4m3 codes: a (m, k) with row scales, b (n, k) with row
+    or tile scales (told by their shape).  ``out_dtype``: bfloat16 (default),
+    float16 or float32.  See fwt_scaled_matmul."""
+    import torch
+    lib = _load()
+    f8 = (torch.float8_e4m3fn,)
+    lda, ldb = _matrix(a, "a", f8), _matrix(b, "b", f8)
+    (m, k), (n, kb) = a.shape, b.shape
+    if k != kb:
+        raise ValueError("a and b must have the same number of columns")
+    nblocks = -(-k // BLOCK)
+    _scales_of(a_scales, "a_scales", nblocks, m, ("row",))
+    kind = _scales_of(b_scales, "b_scales", nblocks, n, ("tile", "row"))
+    dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    if dtype not in _types or dtype is torch.float8_e4m3fn:
+        raise ValueError("out_dtype must be bfloat16, float16 or float32")
+    handle, where = _on(stream)
+    with where:
+        c, ldc = _result(out, "out", m, n, dtype, a.device)
+    _raise(lib.fwt_scaled_matmul(a.data_ptr(), lda, a_scales.data_ptr(), b.data_ptr(), ldb,
+                                 b_scales.data_ptr(), _SCALES[kind], m, n, k, c.data_ptr(),
+                                 _types[dtype], ldc, handle), "fwt_scaled_matmul")
+    return c
+
+
+def gated_ffn(x, gate, up, act="silu", x_scales=None, gate_scales=None, up_scales=None,
+              out_dtype=None, out=None, stream=None):
+    """``act(x gate^T) * (x up^T)`` for x (m, k), gate and up (n, k).
+
+    bf16 or f16 operands give an output of their dtype.  e4m3 codes come with
+    ``x_scales`` ("row") and ``gate_scales``/``up_scales`` ("tile") and give
+    ``out_dtype`` (bfloat16 by default).  ``act``: "silu" or "gelu".  See
+    fwt_gated_ffn.
+    """
+    import torch
+    lib = _load()
+    kinds = (torch.bfloat16, torch.float16, torch.float8_e4m3fn)
+    ldx = _matrix(x, "x", kinds)
+    ldg, ldu = _matrix(gate, "gate", (x.dtype,)), _matrix(up, "up", (x.dtype,))
+    m, k = x.shape
+    n = gate.shape[0]
+    if gate.shape[1] != k or tuple(up.shape) != (n, k):
+        raise ValueError("gate and up must have shape (n, %d)" % k)
+    sp = (None, None, None)
+    if x.dtype is torch.float8_e4m3fn:
+        if x_scales is None or gate_scales is None or up_scales is None:
+            raise ValueError("e4m3 operands need x_scales, gate_scales and up_scales")
+        nblocks = -(-k // BLOCK)
+        _scales_of(x_scales, "x_scales", nblocks, m, ("row",))
+        _scales_of(gate_scales, "gate_scales", nblocks, n, ("tile",))
+        _scales_of(up_scales, "up_scales", nblocks, n, ("tile",))
+        sp = (x_scales.data_ptr(), gate_scales.data_ptr(), up_scales.data_ptr())
+        dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+    else:
+        if x_scales is not None or gate_scales is not None or up_scales is not None:
+            raise ValueError("scales belong to e4m3 operands")
+        dtype = out_dtype or x.dtype
+        if dtype != x.dtype:
+            raise ValueError("the output has the operands' dtype")
+    if dtype not in _types or dtype is torch.float8_e4m3fn:
+        raise ValueError("out_dtype must be bfloat16, float16 or float32")
+    a = _act(act)
+    handle, where = _on(stream)
+    with where:
+        h, ldh = _result(out, "out", m, n, dtype, x.device)
+    _raise(lib.fwt_gated_ffn(x.data_ptr(), ldx, sp[0], gate.data_ptr(), ldg, sp[1],
+                             up.data_ptr(), ldu, sp[2], _types[x.dtype], m, n, k, a,
+                             h.data_ptr(), _types[dtype], ldh, handle), "fwt_gated_ffn")
+    return h
+
+
+def gated_ffn_backward(x, gate, up, grad, act="silu", stream=None):
+    """Gradients (dx, dgate, dup) of ``gated_ffn`` on bf16 or f16 operands
+    for ``grad``, that of its output (m, n).  See fwt_gated_ffn_backward."""
+    import torch
+    lib = _load()
+    ldx = _matrix(x, "x", (torch.bfloat16, torch.float16))
+    ldg, ldu = _matrix(gate, "gate", (x.dtype,)), _matrix(up, "up", (x.dtype,))
+    ldd = _matrix(grad, "grad", (x.dtype,))
+    m, k = x.shape
+    n = gate.shape[0]
+    if gate.shape[1] != k or tuple(up.shape) != (n, k):
+        raise ValueError("gate and up must have shape (n, %d)" % k)
+    if tuple(grad.shape) != (m, n):
+        raise ValueError("grad must have shape %s" % ((m, n),))
+    a = _act(act)
+    need = ctypes.c_size_t(0)
+    _raise(lib.fwt_gated_ffn_backward_workspace(m, n, k, ctypes.byref(need)),
+           "fwt_gated_ffn_backward_workspace")
+    handle, where = _on(stream)
+    with where:
+        dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
+        dgate = torch.empty((n, k), dtype=x.dtype, device=x.device)
+        dup = torch.empty((n, k), dtype=x.dtype, device=x.device)
+        ws, wp = _scratch(need.value, x.device)
+    _raise(lib.fwt_gated_ffn_backward(x.data_ptr(), ldx, gate.data_ptr(), ldg, up.data_ptr(),
+                                      ldu, grad.data_ptr(), ldd, _types[x.dtype], m, n, k, a,
+                                      dx.data_ptr(), k, dgate.data_ptr(), k, dup.data_ptr(), k,
+                                      wp, need.value, handle), "fwt_gated_ffn_backward")
+    return dx, dgate, dup
