@@ -24,6 +24,14 @@ enum ScaleMode : int { kNoScale = 0, kTileScale = 1, kRowScale = 2 };
 // halves of the 64 banks.
 __device__ __forceinline__ int slot(int r, int c) { return c ^ ((r >> 1) & 7); }
 
+// The row of A that stands at LDS row r: the 16-row blocks of a wave's
+// `block` rows take every (block / 16)th row, so that a lane's rows (one of
+// each) are neighbours.
+__device__ __forceinline__ constexpr int row_of(int r, int block)
+{
+    return r / block * block + r % 16 * (block / 16) + r % block / 16;
+}
+
 // The tile of workgroup w.  The dispatcher hands consecutive workgroups to
 // the 8 XCDs in turn; each XCD gets a contiguous run of the tile order, and
 // the order goes down columns of up to 8 row tiles, so the tiles that an
@@ -58,6 +66,13 @@ __device__ __forceinline__ v4i chunk_at(const char* p, int left)
     return v;
 }
 
+// Scales at .. at + 3 of the `left` ones from p.
+__device__ __forceinline__ v4f load_row_scales(const float* p, int left, int at)
+{
+    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, left * 4, (int)kRsrcFlags);
+    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at * 4, 0, 0));
+}
+
 // REG: the operands' rows need not be 16-byte aligned; they go through
 // registers, loaded before a step's products and stored to LDS after them.
 template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG>
@@ -86,44 +101,36 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     // chunk that holds a valid byte lies in that byte's page).
     const int64_t kround = (p.kbytes + 15) & ~(int64_t)15;
     const v4i ra = make_rsrc((const char*)p.a + m0 * p.lda, (uint64_t)((mrows - 1) * p.lda + kround));
-    const v4i rb0 =
+    const v4i rb =
         make_rsrc((const char*)p.b0 + n0 * p.ldb0, (uint64_t)((nrows - 1) * p.ldb0 + kround));
-    const v4i rb1 = kDual ? make_rsrc((const char*)p.b1 + n0 * p.ldb1,
+    const v4i ru = kDual ? make_rsrc((const char*)p.b1 + n0 * p.ldb1,
                                       (uint64_t)((nrows - 1) * p.ldb1 + kround))
-                          : rb0;
-    // Row groups of 8: this wave stages groups wave, wave + W, ...  Rows past
-    // the operand's last are read as its last; their results are not stored.
-    unsigned va[GA], vb[GB];
-    const int lr = lane >> 3, lc = lane & 7;
-#pragma unroll
-    for (int g = 0; g < GA; ++g) {
-        const int r = (wave + g * W) * 8 + lr;
-        const int rr = r < mrows ? r : mrows - 1;
-        va[g] = (unsigned)(rr * p.lda) + slot(r, lc) * 16;
-    }
-#pragma unroll
-    for (int g = 0; g < GB; ++g) {
-        const int r = (wave + g * W) * 8 + lr;
-        const bool up = kDual && g >= GB / 2;
-        const int ro = up ? r - BNO : r;
-        const int rr = ro < nrows ? ro : nrows - 1;
-        vb[g] = (unsigned)(rr * (up ? p.ldb1 : p.ldb0)) + slot(r, lc) * 16;
-    }
-    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+                         : rb;
+    // A wave stages groups of 8 LDS rows, wave, wave + W, ...; its first row of
+    // A and of B is rows(...)(0), and group g lies a constant further on.
+    // (Rows past an operand's last are past its descriptor: what stands in
+    // LDS for them feeds results that are not stored.)
+    constexpr int kRowsB = BNO / WN;                 // rows of one projection per wave
+    const int lr = lane >> 3, lc = slot(wave * 8 + (lane >> 3), lane & 7);
+    const int ra0 = row_of(wave * 8 + lr, TM * 16);
+    const int rb0 = wave * 8 + lr;
+    const unsigned va = (unsigned)(ra0 * p.lda) + lc * 16;
+    const unsigned vb = (unsigned)(rb0 * p.ldb0) + lc * 16;
+    const unsigned vu = kDual ? (unsigned)(rb0 * p.ldb1) + lc * 16 : 0;
     v4i held[REG ? GA + GB : 1];
     auto fetch = [&](int kt) {
 #pragma unroll
         for (int g = 0; g < GA + GB; ++g) {
             const bool isb = g >= GA;
             const int gg = isb ? g - GA : g;
-            const int r = (wave + gg * W) * 8 + lr;
             const bool up = isb && kDual && gg >= GB / 2;
-            const int ro = up ? r - BNO : r;
+            const int ro = isb ? rb0 + (up ? gg - GB / 2 : gg) * 8 * W
+                               : ra0 + row_of(gg * 8 * W, TM * 16);
             const int rows = isb ? nrows : mrows;
             const int64_t row = (isb ? n0 : m0) + (ro < rows ? ro : rows - 1);
             const char* base = (const char*)(isb ? (up ? p.b1 : p.b0) : p.a);
             const int64_t ld = isb ? (up ? p.ldb1 : p.ldb0) : p.lda;
-            const int64_t at = (int64_t)kt * kStep + slot(r, lc) * 16;
+            const int64_t at = (int64_t)kt * kStep + lc * 16;
             held[g] = chunk_at(base + row * ld + at, (int)(p.kbytes - at < 16 ? p.kbytes - at : 16));
         }
     };
@@ -135,16 +142,20 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
                     lane * 16) = held[g];
         }
     };
+    const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
     auto stage = [&](int kt) {
-        const unsigned base = lds0 + (kt & 1) * kBuf;
+        const unsigned base = lds0 + (kt & 1) * kBuf + wave * 1024;
         const unsigned so = (unsigned)kt * kStep;
 #pragma unroll
         for (int g = 0; g < GA; ++g)
-            load_to_lds(ra, base + (wave + g * W) * 1024, va[g], so);
+            load_to_lds(ra, base + g * W * 1024, va,
+                        so + (unsigned)(row_of(g * 8 * W, TM * 16) * p.lda));
 #pragma unroll
-        for (int g = 0; g < GB; ++g)
-            load_to_lds(kDual && g >= GB / 2 ? rb1 : rb0, base + BM * kStep + (wave + g * W) * 1024,
-                        vb[g], so);
+        for (int g = 0; g < GB; ++g) {
+            const bool up = kDual && g >= GB / 2;
+            load_to_lds(up ? ru : rb, base + (BM + g * 8 * W) * kStep, up ? vu : vb,
+                        so + (unsigned)((up ? g - GB / 2 : g) * 8 * W * (up ? p.ldb1 : p.ldb0)));
+        }
     };
 
     const int nk = (int)((p.kbytes + kStep - 1) / kStep);
@@ -155,18 +166,23 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         for (int j = 0; j < TN; ++j)
             acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    // Scales: rows of A stand on lanes (16 of each block), rows of B on the
-    // four registers of a result.
+    // Scales: rows of A stand on lanes, TM consecutive ones on a lane (that is
+    // what row_of is for), rows of B on the four registers of a result.
     const int q = lane >> 4, l16 = lane & 15;
-    const float* sap[TM];
     float sa[TM], sa_next[TM];
-    const int nb0 = (int)((n0 + wn * (BNO / WN)) / kFfnBlock);
-    float sb_next[2];
+    float sb[2], sb_next[2];
+    const int nb0 = (int)((n0 + wn * kRowsB) / kFfnBlock);
+    const int mleft = mrows > wm * TM * 16 ? mrows - wm * TM * 16 : 0;
     auto load_scales = [&](int kt) {
         if constexpr (SM != kNoScale) {
 #pragma unroll
-            for (int i = 0; i < TM; ++i)
-                sa_next[i] = sap[i][(int64_t)kt * p.m];
+            for (int i = 0; i < TM; i += 4) {
+                const v4f v = load_row_scales(p.sa + (int64_t)kt * p.m + m0 + wm * TM * 16, mleft,
+                                              l16 * TM + i);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    sa_next[i + r] = v[r];
+            }
             if constexpr (SM == kTileScale) {
                 sb_next[0] = p.sb0[(int64_t)kt * p.sb_n + nb0];
                 if constexpr (kDual)
@@ -174,13 +190,6 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
             }
         }
     };
-    if constexpr (SM != kNoScale) {
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            const int r = wm * (TM * 16) + i * 16 + l16;
-            sap[i] = p.sa + m0 + (r < mrows ? r : mrows - 1);
-        }
-    }
 
     if constexpr (REG) {
         fetch(0);
@@ -192,7 +201,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const int swz = l16 >> 1;
     const int ao = (wm * TM * 16 + l16) * kStep + ((q ^ swz) * 16);
     // B rows of this wave in LDS: gate rows, then up rows BNO further on.
-    const int bo = (BM + wn * (BNO / WN) + l16) * kStep + ((q ^ swz) * 16);
+    const int bo = (BM + wn * kRowsB + l16) * kStep + ((q ^ swz) * 16);
     const int ktail = (int)(p.kbytes % kStep);
 
     for (int kt = 0; kt < nk; ++kt) {
@@ -220,7 +229,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
             }
             __syncthreads();
         }
-        float sb[2] = {sb_next[0], sb_next[1]};
+        sb[0] = sb_next[0];
+        sb[1] = sb_next[1];
 #pragma unroll
         for (int i = 0; i < TM; ++i)
             sa[i] = sa_next[i];
@@ -238,37 +248,64 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
             b[j][0] = *(const v4i*)(buf + bo + row * kStep);
             b[j][1] = *(const v4i*)(buf + (bo ^ 64) + row * kStep);
         }
-        v4f sbr[TN];
+        v4f sbr[SM == kRowScale ? TN : 1];
         if constexpr (SM == kRowScale) {
 #pragma unroll
             for (int j = 0; j < TN; ++j)
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const bool up = kDual && j >= TN / 2;
-                    int n = wn * (BNO / WN) + (up ? j - TN / 2 : j) * 16 + q * 4 + r;
+                    int n = wn * kRowsB + j * 16 + q * 4 + r;
                     n = n < nrows ? n : nrows - 1;
-                    sbr[j][r] = (up ? p.sb1 : p.sb0)[(int64_t)kt * p.sb_n + n0 + n];
+                    sbr[j][r] = p.sb0[(int64_t)kt * p.sb_n + n0 + n];
                 }
         }
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            v4i a[2];
-            a[0] = *(const v4i*)(buf + ao + i * 16 * kStep);
-            a[1] = *(const v4i*)(buf + (ao ^ 64) + i * 16 * kStep);
+        // Rows of A in turn: while the matrix instructions of one run, the
+        // next one's operand comes from LDS, and the sums of the last one
+        // are scaled and added.
+        v4i a[2][2];
+        v4f t[2][SM == kNoScale ? 1 : TN];
+        a[0][0] = *(const v4i*)(buf + ao);
+        a[0][1] = *(const v4i*)(buf + (ao ^ 64));
+        auto add = [&](int i) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
-                if constexpr (SM == kNoScale) {
-                    acc[i][j] = matrix_step<TYPE>(b[j], a, acc[i][j]);
-                } else {
-                    const v4f t = matrix_step<TYPE>(b[j], a, v4f{0.f, 0.f, 0.f, 0.f});
-                    const float s = sa[i] * (kDual && j >= TN / 2 ? sb[1] : sb[0]);
+                const float s = sa[i] * (kDual && j >= TN / 2 ? sb[1] : sb[0]);
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        acc[i][j][r] = __builtin_fmaf(
-                            t[r], SM == kTileScale ? s : sa[i] * sbr[j][r], acc[i][j][r]);
+                for (int r = 0; r < 4; ++r)
+                    acc[i][j][r] =
+                        __builtin_fmaf(t[i & 1][j][r], SM == kTileScale ? s : sa[i] * sbr[j][r],
+                                       acc[i][j][r]);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            if (i + 1 < TM) {
+                a[(i + 1) & 1][0] = *(const v4i*)(buf + ao + (i + 1) * 16 * kStep);
+                a[(i + 1) & 1][1] = *(const v4i*)(buf + (ao ^ 64) + (i + 1) * 16 * kStep);
+            }
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                if constexpr (SM == kNoScale)
+                    acc[i][j] = matrix_step<TYPE>(b[j], a[i & 1], acc[i][j]);
+                else
+                    t[i & 1][j] = matrix_step<TYPE>(b[j], a[i & 1], v4f{0.f, 0.f, 0.f, 0.f});
+            }
+            if constexpr (SM != kNoScale)
+                if (i > 0)
+                    add(i - 1);
+            if (i + 1 < TM)
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // two LDS reads
+            if constexpr (SM != kNoScale) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix
+                    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);   // vector
                 }
             }
+            __builtin_amdgcn_sched_barrier(0);
         }
+        if constexpr (SM != kNoScale)
+            add(TM - 1);
         if constexpr (REG) {
             if (kt + 1 < nk)
                 put(kt + 1);
@@ -279,13 +316,13 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const bool bf = p.ctype == kTBf16;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int r = wm * (TM * 16) + i * 16 + l16;
+        const int r = wm * (TM * 16) + l16 * TM + i;
         if (r >= mrows)
             continue;
         const int64_t m = m0 + r;
 #pragma unroll
         for (int j = 0; j < (kDual ? TN / 2 : TN); ++j) {
-            const int nc = wn * (BNO / WN) + j * 16 + q * 4;
+            const int nc = wn * kRowsB + j * 16 + q * 4;
             if (nc >= nrows)
                 continue;
             const int64_t at = m * p.ldc + n0 + nc;
@@ -359,11 +396,13 @@ hipError_t pick(const ProductArgs& p, hipStream_t stream)
             return run<TYPE, 128, 128, 2, 2, EP, SM, true>(p, stream);
     }
     const int64_t bno = EP != kEpStore ? 128 : 256;
-    if constexpr (TYPE == kTE4m3Exact)   // the widened operands leave no registers for more
-        return run<TYPE, 128, 128, 2, 2, EP, SM>(p, stream);
-    const int64_t big = ((p.m + 255) / 256) * ((p.n + bno - 1) / bno);
-    if (big >= 192)
-        return run<TYPE, 256, 256, 2, 4, EP, SM>(p, stream);
+    // The widened operands, or a scale for each row of B, leave no registers
+    // for the larger tile.
+    if constexpr (TYPE != kTE4m3Exact && SM != kRowScale) {
+        const int64_t bno = EP != kEpStore ? 128 : 256;
+        if (((p.m + 255) / 256) * ((p.n + bno - 1) / bno) >= 192)
+            return run<TYPE, 256, 256, 2, 4, EP, SM>(p, stream);
+    }
     return run<TYPE, 128, 128, 2, 2, EP, SM>(p, stream);
 }
 
