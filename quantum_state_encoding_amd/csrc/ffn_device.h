@@ -109,6 +109,55 @@ __device__ __forceinline__ float from16(unsigned short u, bool bf)
     return (float)__builtin_bit_cast(_Float16, u);
 }
 
+// Four results to c[at ..], the first cnt of which exist; wide: as one
+// aligned store.
+__device__ __forceinline__ void store4(void* c, int64_t at, v4f v, int type, int cnt, int wide)
+{
+    if (type == kTF32) {
+        float* p = (float*)c + at;
+        if (wide && cnt == 4) {
+            *(v4f*)p = v;
+        } else {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                if (k < cnt)
+                    p[k] = v[k];
+        }
+        return;
+    }
+    typedef unsigned short v4h __attribute__((ext_vector_type(4)));
+    v4h h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        h[k] = to16(v[k], type == kTBf16);
+    unsigned short* p = (unsigned short*)c + at;
+    if (wide && cnt == 4) {
+        *(v4h*)p = h;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < cnt)
+                p[k] = h[k];
+    }
+}
+
+// Four 16-bit values from p[at ..], 0 past cnt.
+__device__ __forceinline__ v4f load4(const void* p, int64_t at, bool bf, int cnt, int wide)
+{
+    typedef unsigned short v4h __attribute__((ext_vector_type(4)));
+    const unsigned short* s = (const unsigned short*)p + at;
+    v4h h = v4h{0, 0, 0, 0};
+    if (wide && cnt == 4) {
+        h = *(const v4h*)s;
+    } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (k < cnt)
+                h[k] = s[k];
+    }
+    return v4f{from16(h[0], bf), from16(h[1], bf), from16(h[2], bf), from16(h[3], bf)};
+}
+
 // act(g) and its derivative in 32 bits.  silu: g s and s (1 + g (1 - s))
 // with s = 1 / (1 + e^-g); for e^-g past the fp32 range s is 0.  gelu: g P
 // and P + g e^(-g^2/2) / sqrt(2 pi) with P the normal distribution

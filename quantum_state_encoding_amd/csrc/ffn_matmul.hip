@@ -312,7 +312,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         }
     }
 
-    // Results: lane l holds row l & 15 of A and four consecutive rows of B.
+    // Results: lane l holds rows l % 16 * TM .. of A and four consecutive rows
+    // of B, stored at once where the output's alignment allows.
     const bool bf = p.ctype == kTBf16;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -327,43 +328,26 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
                 continue;
             const int64_t at = m * p.ldc + n0 + nc;
             const int cnt = nrows - nc < 4 ? nrows - nc : 4;
-            float v[4], u[4];
-            if constexpr (EP == kEpStore) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k)
-                    v[k] = acc[i][j][k];
-            } else if constexpr (EP == kEpGate) {
+            v4f v = acc[i][j], u;
+            if constexpr (EP == kEpGate) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float f, d;
                     activation(p.act, acc[i][j][k], f, d);
                     v[k] = f * acc[i][j + TN / 2][k];
                 }
-            } else {
-                const unsigned short* dh =
-                    (const unsigned short*)p.dh + m * p.lddh + n0 + nc;
+            } else if constexpr (EP == kEpGateGrad) {
+                const v4f g = load4(p.dh, m * p.lddh + n0 + nc, bf, cnt, p.wide_dh);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float f, d;
-                    const float up = acc[i][j + TN / 2][k];
-                    const float g = k < cnt ? from16(dh[k], bf) : 0.f;
                     activation(p.act, acc[i][j][k], f, d);
-                    v[k] = g * up * d;
-                    u[k] = g * f;
+                    v[k] = g[k] * acc[i][j + TN / 2][k] * d;
+                    u[k] = g[k] * f;
                 }
+                store4(p.c, at + p.n, u, p.ctype, cnt, p.wide_c);
             }
-            if (p.ctype == kTF32) {
-                float* c = (float*)p.c + at;
-                for (int k = 0; k < cnt; ++k)
-                    c[k] = v[k];
-            } else {
-                unsigned short* c = (unsigned short*)p.c + at;
-                for (int k = 0; k < cnt; ++k)
-                    c[k] = to16(v[k], bf);
-                if constexpr (EP == kEpGateGrad)
-                    for (int k = 0; k < cnt; ++k)
-                        c[p.n + k] = to16(u[k], bf);
-            }
+            store4(p.c, at, v, p.ctype, cnt, p.wide_c);
         }
     }
 }
@@ -373,6 +357,10 @@ hipError_t run(ProductArgs p, hipStream_t stream)
 {
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
     constexpr size_t kLds = 2 * (size_t)(BM + BN) * kStep;
+    const int64_t csize = p.ctype == kTF32 ? 4 : 2;
+    p.wide_c = (((uintptr_t)p.c | (uintptr_t)(p.ldc * csize)) & (4 * csize - 1)) == 0 &&
+               (EP != kEpGateGrad || p.n % 4 == 0);
+    p.wide_dh = (((uintptr_t)p.dh | (uintptr_t)(p.lddh * 2)) & 7) == 0;
     p.tiles_m = (int)((p.m + BM - 1) / BM);
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
     auto* k = &product_kernel<TYPE, BM, BN, WM, WN, EP, SM, REG>;
