@@ -117,26 +117,9 @@ constexpr Array kNone{nullptr, 0, 0, 0, 0, false};
 // 16-bit elements of a row padded to whole 16-byte chunks.
 int64_t pad8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 
-// The backward pass's scratch, in 16-bit elements: dg beside du (m x 2n),
-// that transposed (2n x m), x transposed (k x m), gate and up transposed
-// side by side (k x 2n).
-struct BackwardScratch {
-    int64_t ldd, ldt, ldw;
-    int64_t d, dt, xt, wt, total;
-};
-BackwardScratch backward_scratch(int64_t m, int64_t n, int64_t k)
-{
-    BackwardScratch s;
-    s.ldd = pad8(2 * n);
-    s.ldt = pad8(m);
-    s.ldw = pad8(2 * n);
-    s.d = 0;
-    s.dt = s.d + m * s.ldd;
-    s.xt = s.dt + 2 * n * s.ldt;
-    s.wt = s.xt + k * s.ldt;
-    s.total = s.wt + k * s.ldw;
-    return s;
-}
+// The backward pass's scratch: dg beside du, m rows of 2 pad8(n) 16-bit
+// elements.
+size_t backward_scratch(int64_t m, int64_t n) { return (size_t)m * 4 * (size_t)pad8(n); }
 
 }  // namespace
 
@@ -296,7 +279,7 @@ int fwt_gated_ffn_backward_workspace(int64_t m, int64_t n, int64_t k, size_t* by
 {
     if (!bytes || !dims_ok(m, n, k))
         return FWT_EINVAL;
-    *bytes = m == 0 || n == 0 ? 0 : 2 * (size_t)backward_scratch(m, n, k).total;
+    *bytes = m == 0 || n == 0 ? 0 : backward_scratch(m, n);
     return FWT_OK;
 }
 
@@ -323,8 +306,7 @@ int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t
     if (sums && !aligned16(ws, 0))
         return FWT_EALIGN;
     if (ldx * 2 >= qse::kFfnMaxStride || ldgate * 2 >= qse::kFfnMaxStride ||
-        ldup * 2 >= qse::kFfnMaxStride || pad8(2 * n) * 2 >= qse::kFfnMaxStride ||
-        pad8(m) * 2 >= qse::kFfnMaxStride)
+        ldup * 2 >= qse::kFfnMaxStride || pad8(n) * 4 >= qse::kFfnMaxStride)
         return FWT_EUNSUPPORTED;
     const Array arrays[] = {
         sums ? Array{x, m, k, ldx, 2, false} : kNone,
@@ -346,9 +328,8 @@ int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t
             e = qse::launch_zero16(dup, lddup, n, k, stream);
         return status(e);
     }
-    const BackwardScratch b = backward_scratch(m, n, k);
-    uint16_t* const w = (uint16_t*)ws;
     // dg and du, from the two products
+    const int64_t np = pad8(n);
     ProductArgs p{};
     p.a = x;
     p.b0 = gate;
@@ -359,51 +340,52 @@ int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t
     p.m = m;
     p.n = n;
     p.kbytes = k * 2;
-    p.c = w + b.d;
-    p.ldc = b.ldd;
+    p.c = ws;
+    p.ldc = 2 * np;
+    p.part_c = np;
     p.ctype = (int)dtype;
     p.dh = dh;
     p.lddh = lddh;
     p.act = (int)act;
     hipError_t e = qse::launch_product(p, (int)dtype, qse::kEpGateGrad, false, stream);
-    // dx = [dg du] [gate; up]
-    if (e == hipSuccess)
-        e = qse::launch_transpose16(gate, ldgate, w + b.wt, b.ldw, n, k, stream);
-    if (e == hipSuccess)
-        e = qse::launch_transpose16(up, ldup, w + b.wt + n, b.ldw, n, k, stream);
-    if (e == hipSuccess) {
-        ProductArgs d{};
-        d.a = w + b.d;
-        d.lda = b.ldd * 2;
-        d.b0 = w + b.wt;
-        d.ldb0 = b.ldw * 2;
-        d.m = m;
-        d.n = k;
-        d.kbytes = 4 * n;
-        d.c = dx;
-        d.ldc = lddx;
-        d.ctype = (int)dtype;
-        e = qse::launch_product(d, (int)dtype, qse::kEpStore, false, stream);
-    }
-    // dgate = dg^T x, dup = du^T x
-    if (e == hipSuccess)
-        e = qse::launch_transpose16(w + b.d, b.ldd, w + b.dt, b.ldt, m, 2 * n, stream);
-    if (e == hipSuccess)
-        e = qse::launch_transpose16(x, ldx, w + b.xt, b.ldt, m, k, stream);
-    for (int i = 0; i < 2 && e == hipSuccess; ++i) {
-        ProductArgs d{};
-        d.a = w + b.dt + i * n * b.ldt;
-        d.lda = b.ldt * 2;
-        d.b0 = w + b.xt;
-        d.ldb0 = b.ldt * 2;
-        d.m = n;
-        d.n = k;
-        d.kbytes = 2 * m;
-        d.c = i ? dup : dgate;
-        d.ldc = i ? lddup : lddgate;
-        d.ctype = (int)dtype;
-        e = qse::launch_product(d, (int)dtype, qse::kEpStore, false, stream);
-    }
+    if (e != hipSuccess)
+        return status(e);
+    // dx = dg gate + du up: the contraction runs over n of gate, then of up
+    ProductArgs d{};
+    d.a = ws;
+    d.lda = 4 * np;
+    d.b0 = gate;
+    d.b1 = up;
+    d.ldb0 = ldgate * 2;
+    d.ldb1 = ldup * 2;
+    d.m = m;
+    d.n = k;
+    d.kbytes = 2 * n;
+    d.parts = 2;
+    d.part_a = 2 * np;
+    d.c = dx;
+    d.ldc = lddx;
+    d.ctype = (int)dtype;
+    e = qse::launch_product(d, (int)dtype, qse::kEpStore, false, stream);
+    if (e != hipSuccess)
+        return status(e);
+    // [dgate; dup] = [dg du]^T x
+    ProductArgs g{};
+    g.a = ws;
+    g.lda = 4 * np;
+    g.b0 = x;
+    g.ldb0 = ldx * 2;
+    g.m = 2 * np;
+    g.n = k;
+    g.kbytes = 2 * m;
+    g.c = dgate;
+    g.c1 = dup;
+    g.split = np;
+    g.split_rows = n;
+    g.ldc = lddgate;
+    g.ldc1 = lddup;
+    g.ctype = (int)dtype;
+    e = qse::launch_product(g, (int)dtype, qse::kEpStoreT, false, stream);
     return status(e);
 }
 

@@ -22,9 +22,10 @@ constexpr int64_t kFfnMaxStride = (int64_t)1 << 23;
 
 // What a product's epilogue does with its accumulators.
 enum FfnEpilogue : int {
-    kEpStore = 0,     // C = A B^T
+    kEpStore = 0,     // C = A B^T; 16-bit operands: with B stored [k][n]
     kEpGate = 1,      // C = act(A B0^T) * (A B1^T)
     kEpGateGrad = 2,  // the gradients of A B0^T and A B1^T from that of C
+    kEpStoreT = 3,    // 16-bit operands: kEpStore with A stored [k][m] too
 };
 
 // One product A B^T (A: m x k, B: n x k, both with k contiguous), or two
@@ -40,8 +41,14 @@ struct ProductArgs {
     const float* sb0;       // scales [k block][sb_n]
     const float* sb1;
     int64_t sb_n;           // n (one for each row of B) or ceil(n / 128)
-    void* c;                // m x n; kEpGateGrad: m x 2n, dg beside du
-    int64_t ldc;
+    int parts;              // 2: the contraction goes on over b1 (kEpStore)
+    int64_t part_a;         // for columns of A this many bytes further on
+    void* c;                // m x n; kEpGateGrad: dg
+    int64_t part_c;         // du this many elements further on
+    void* c1;               // kEpStoreT: the results' rows from split on, as
+    int64_t split;          // many as of the first, split_rows; 0: none
+    int64_t split_rows;
+    int64_t ldc, ldc1;
     int ctype;
     const void* dh;         // kEpGateGrad: gradient of C, m x n
     int64_t lddh;
@@ -59,10 +66,6 @@ hipError_t launch_product(const ProductArgs& p, int type, int epilogue, bool row
 constexpr int kStripRows = 64;
 hipError_t launch_strip(const ProductArgs& p, int type, int epilogue, bool row_scales,
                         hipStream_t stream);
-
-// dst (cols x rows, stride ldd) = src (rows x cols, stride lds)^T, 16-bit.
-hipError_t launch_transpose16(const void* src, int64_t lds, void* dst, int64_t ldd, int64_t rows,
-                              int64_t cols, hipStream_t stream);
 
 // Zeros to rows x cols 16-bit elements.
 hipError_t launch_zero16(void* dst, int64_t ld, int64_t rows, int64_t cols, hipStream_t stream);

@@ -73,9 +73,35 @@ __device__ __forceinline__ v4f load_row_scales(const float* p, int left, int at)
     return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at * 4, 0, 0));
 }
 
+// An operand that is stored with its rows side by side, [k][rows] (AT, BT;
+// 16-bit types): a step stages 64 k of it as they are, and the transposing
+// LDS read gives a lane four k of its row.  Its 16 lanes take four k rows of
+// 32 bytes each, so those 32-byte units are spread over the banks by k.
+__device__ __forceinline__ int unit_mask(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
+
+template <int BR>
+__device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile, int block, int lane)
+{
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    const int q = lane >> 4, l16 = lane & 15;
+    const unsigned char* at = tile + (q * 8 + (l16 >> 2)) * (BR * 2) +
+                              ((block ^ unit_mask(q * 8 + (l16 >> 2))) * 32) + (l16 & 3) * 8;
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        v4s r[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e)
+            r[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) v4s*)(at + (h * 32 + e * 4) * (BR * 2)));
+        out[h] = __builtin_bit_cast(v4i, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7));
+    }
+}
+
 // REG: the operands' rows need not be 16-byte aligned; they go through
 // registers, loaded before a step's products and stored to LDS after them.
-template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG>
+// AT, BT: A or B is stored [k][rows].  With p.parts = 2 the contraction goes
+// on in a second B (b1), for columns part_a bytes further on in A's rows.
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG, bool AT, bool BT>
 __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs p)
 {
     constexpr int W = WM * WN;                   // waves
@@ -97,44 +123,76 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const int mrows = (int)(p.m - m0 < BM ? p.m - m0 : BM);
     const int nrows = (int)(p.n - n0 < BNO ? p.n - n0 : BNO);
 
-    // Descriptors end with the last row's last chunk (a 16-byte aligned
-    // chunk that holds a valid byte lies in that byte's page).
-    const int64_t kround = (p.kbytes + 15) & ~(int64_t)15;
-    const v4i ra = make_rsrc((const char*)p.a + m0 * p.lda, (uint64_t)((mrows - 1) * p.lda + kround));
-    const v4i rb =
-        make_rsrc((const char*)p.b0 + n0 * p.ldb0, (uint64_t)((nrows - 1) * p.ldb0 + kround));
-    const v4i ru = kDual ? make_rsrc((const char*)p.b1 + n0 * p.ldb1,
-                                      (uint64_t)((nrows - 1) * p.ldb1 + kround))
-                         : rb;
-    // A wave stages groups of 8 LDS rows, wave, wave + W, ...; its first row of
-    // A and of B is rows(...)(0), and group g lies a constant further on.
-    // (Rows past an operand's last are past its descriptor: what stands in
-    // LDS for them feeds results that are not stored.)
+    static_assert(!(AT || BT) || (SM == kNoScale && !kDual && GA == 4 && GB == 4), "[k][rows]");
     constexpr int kRowsB = BNO / WN;                 // rows of one projection per wave
+    const int nks = (int)((p.kbytes + kStep - 1) / kStep);   // steps of a part
+    // A wave stages 1 KiB at a time, pieces wave, wave + W, ...: 8 LDS rows of
+    // an operand, or 64 k / (4 W) rows of k of one that is [k][rows].  Piece g
+    // lies a constant number of rows behind the wave's first.  Descriptors
+    // end with the last row's last chunk (a 16-byte aligned chunk that holds
+    // a valid byte lies in that byte's page).  What lies past the operand's
+    // last row is past its descriptor; it feeds results that are not stored.
+    const int64_t kround = (p.kbytes + 15) & ~(int64_t)15;
     const int lr = lane >> 3, lc = slot(wave * 8 + (lane >> 3), lane & 7);
     const int ra0 = row_of(wave * 8 + lr, TM * 16);
     const int rb0 = wave * 8 + lr;
-    const unsigned va = (unsigned)(ra0 * p.lda) + lc * 16;
-    const unsigned vb = (unsigned)(rb0 * p.ldb0) + lc * 16;
-    const unsigned vu = kDual ? (unsigned)(rb0 * p.ldb1) + lc * 16 : 0;
+    constexpr int kCa = BM / 8, kCb = BN / 8;        // chunks in a row of k
+    const int ka0 = wave * (64 / kCa) + lane / kCa, kb0 = wave * (64 / kCb) + lane / kCb;
+    const int ca = (((lane % kCa) >> 1) ^ unit_mask(ka0)) * 2 + (lane & 1);
+    const int cb = (((lane % kCb) >> 1) ^ unit_mask(kb0)) * 2 + (lane & 1);
+    const unsigned va = AT ? (unsigned)(ka0 * p.lda) + ca * 16 : (unsigned)(ra0 * p.lda) + lc * 16;
+    const unsigned vb = BT ? (unsigned)(kb0 * p.ldb0) + cb * 16 : (unsigned)(rb0 * p.ldb0) + lc * 16;
+    const unsigned vu = kDual || BT ? (unsigned)((BT ? kb0 : rb0) * p.ldb1) + (BT ? cb : lc) * 16 : 0;
+    const v4i ra = make_rsrc((const char*)p.a + m0 * p.lda,
+                       (uint64_t)((mrows - 1) * p.lda + (p.parts > 1 ? p.part_a : 0) + kround));
+    const v4i rb = make_rsrc((const char*)p.b0 + n0 * p.ldb0, (uint64_t)((nrows - 1) * p.ldb0 + kround));
+    const v4i ru = kDual ? make_rsrc((const char*)p.b1 + n0 * p.ldb1,
+                                      (uint64_t)((nrows - 1) * p.ldb1 + kround))
+                         : rb;
+    // k rows of a [k][rows] operand from step ks on
+    auto rows_of_k = [=](const void* base, int64_t ld, int64_t r0, int64_t rows,
+                         int ks) __attribute__((always_inline)) {
+        const int64_t left = p.kbytes / 2 - (int64_t)ks * 64;
+        return make_rsrc((const char*)base + (int64_t)ks * 64 * ld + r0 * 2,
+                         (uint64_t)((left - 1) * ld + (((rows - r0) * 2 + 15) & ~(int64_t)15)));
+    };
     v4i held[REG ? GA + GB : 1];
-    auto fetch = [&](int kt) {
+    auto fetch = [&](int kt) __attribute__((always_inline)) {
+        const bool second = p.parts > 1 && kt >= nks;
+        const int ks = second ? kt - nks : kt;
+        const int64_t at = (int64_t)ks * kStep + lc * 16;
+        const int left = (int)(p.kbytes - at < 16 ? p.kbytes - at : 16);
 #pragma unroll
-        for (int g = 0; g < GA + GB; ++g) {
-            const bool isb = g >= GA;
-            const int gg = isb ? g - GA : g;
-            const bool up = isb && kDual && gg >= GB / 2;
-            const int ro = isb ? rb0 + (up ? gg - GB / 2 : gg) * 8 * W
-                               : ra0 + row_of(gg * 8 * W, TM * 16);
-            const int rows = isb ? nrows : mrows;
-            const int64_t row = (isb ? n0 : m0) + (ro < rows ? ro : rows - 1);
-            const char* base = (const char*)(isb ? (up ? p.b1 : p.b0) : p.a);
-            const int64_t ld = isb ? (up ? p.ldb1 : p.ldb0) : p.lda;
-            const int64_t at = (int64_t)kt * kStep + lc * 16;
-            held[g] = chunk_at(base + row * ld + at, (int)(p.kbytes - at < 16 ? p.kbytes - at : 16));
+        for (int g = 0; g < GA; ++g) {
+            if constexpr (AT) {
+                const int64_t k = (int64_t)ks * 64 + ka0 + g * 16;
+                const int64_t end = (p.m - m0 - ca * 8) * 2;
+                held[g] = chunk_at((const char*)p.a + k * p.lda + (m0 + ca * 8) * 2,
+                                   k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
+            } else {
+                const int r = ra0 + row_of(g * 8 * W, TM * 16);
+                held[g] = chunk_at((const char*)p.a + (m0 + (r < mrows ? r : mrows - 1)) * p.lda +
+                                       (second ? p.part_a : 0) + at,
+                                   left);
+            }
+        }
+#pragma unroll
+        for (int g = 0; g < GB; ++g) {
+            const bool up = kDual ? g >= GB / 2 : second;
+            const char* base = (const char*)(up ? p.b1 : p.b0);
+            const int64_t ld = up ? p.ldb1 : p.ldb0;
+            if constexpr (BT) {
+                const int64_t k = (int64_t)ks * 64 + kb0 + g * 16;
+                const int64_t end = (p.n - n0 - cb * 8) * 2;
+                held[GA + g] = chunk_at(base + k * ld + (n0 + cb * 8) * 2,
+                                        k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
+            } else {
+                const int r = rb0 + (kDual && up ? g - GB / 2 : g) * 8 * W;
+                held[GA + g] = chunk_at(base + (n0 + (r < nrows ? r : nrows - 1)) * ld + at, left);
+            }
         }
     };
-    auto put = [&](int kt) {
+    auto put = [&](int kt) __attribute__((always_inline)) {
 #pragma unroll
         for (int g = 0; g < GA + GB; ++g) {
             const int gg = g >= GA ? g - GA : g;
@@ -143,22 +201,30 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         }
     };
     const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-    auto stage = [&](int kt) {
+    auto stage = [=](int kt) __attribute__((always_inline)) {
+        const bool second = BT && p.parts > 1 && kt >= nks;
+        const int ks = second ? kt - nks : kt;
         const unsigned base = lds0 + (kt & 1) * kBuf + wave * 1024;
-        const unsigned so = (unsigned)kt * kStep;
+        const unsigned so = (unsigned)ks * kStep;
+        const v4i da = AT ? rows_of_k(p.a, p.lda, m0, p.m, ks) : ra;
+        const v4i db =
+            BT ? rows_of_k(second ? p.b1 : p.b0, second ? p.ldb1 : p.ldb0, n0, p.n, ks) : rb;
 #pragma unroll
         for (int g = 0; g < GA; ++g)
-            load_to_lds(ra, base + g * W * 1024, va,
-                        so + (unsigned)(row_of(g * 8 * W, TM * 16) * p.lda));
+            load_to_lds(da, base + g * W * 1024, va,
+                        AT ? (unsigned)(g * 16 * p.lda)
+                           : so + (second ? (unsigned)p.part_a : 0u) +
+                                 (unsigned)(row_of(g * 8 * W, TM * 16) * p.lda));
 #pragma unroll
         for (int g = 0; g < GB; ++g) {
             const bool up = kDual && g >= GB / 2;
-            load_to_lds(up ? ru : rb, base + (BM + g * 8 * W) * kStep, up ? vu : vb,
-                        so + (unsigned)((up ? g - GB / 2 : g) * 8 * W * (up ? p.ldb1 : p.ldb0)));
+            load_to_lds(up ? ru : db, base + (BM + g * 8 * W) * kStep, up || second ? vu : vb,
+                        BT ? (unsigned)(g * 16 * (second ? p.ldb1 : p.ldb0))
+                           : so + (unsigned)((up ? g - GB / 2 : g) * 8 * W * (up ? p.ldb1 : p.ldb0)));
         }
     };
 
-    const int nk = (int)((p.kbytes + kStep - 1) / kStep);
+    const int nk = p.parts > 1 ? 2 * nks : nks;
     v4f acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -171,9 +237,11 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const int q = lane >> 4, l16 = lane & 15;
     float sa[TM], sa_next[TM];
     float sb[2], sb_next[2];
-    const int nb0 = (int)((n0 + wn * kRowsB) / kFfnBlock);
+    // (a wave whose columns all lie past n takes the last scale)
+    const int64_t nbw = (n0 + wn * kRowsB) / kFfnBlock;
+    const int64_t nb0 = nbw < p.sb_n ? nbw : p.sb_n - 1;
     const int mleft = mrows > wm * TM * 16 ? mrows - wm * TM * 16 : 0;
-    auto load_scales = [&](int kt) {
+    auto load_scales = [&](int kt) __attribute__((always_inline)) {
         if constexpr (SM != kNoScale) {
 #pragma unroll
             for (int i = 0; i < TM; i += 4) {
@@ -209,9 +277,15 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
             wait_vm<0>();
         __syncthreads();
         unsigned char* buf = lds + (kt & 1) * kBuf;
-        if (!REG && kt == nk - 1 && ktail) {
+        if (!REG && ktail && (kt == nk - 1 || kt == nks - 1)) {
             // Past the end of k both operands are 0, whatever was read there.
-            for (int r = threadIdx.x; r < BM + BN; r += 64 * W) {
+            if constexpr (AT)
+                for (int c = (ktail / 2) * kCa + threadIdx.x; c < BM * 8; c += 64 * W)
+                    *(v4i*)(buf + c * 16) = v4i{0, 0, 0, 0};
+            if constexpr (BT)
+                for (int c = (ktail / 2) * kCb + threadIdx.x; c < BN * 8; c += 64 * W)
+                    *(v4i*)(buf + BM * kStep + c * 16) = v4i{0, 0, 0, 0};
+            for (int r = threadIdx.x + (AT ? BM : 0); r < BM + (BT ? 0 : BN); r += 64 * W) {
                 for (int c = ktail >> 4; c < 8; ++c) {
                     v4i* at = (v4i*)(buf + r * kStep + slot(r, c) * 16);
                     const int keep = ktail - c * 16;   // bytes of this chunk
@@ -245,8 +319,12 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
 #pragma unroll
         for (int j = 0; j < TN; ++j) {
             const int row = kDual && j >= TN / 2 ? BNO + (j - TN / 2) * 16 : j * 16;
-            b[j][0] = *(const v4i*)(buf + bo + row * kStep);
-            b[j][1] = *(const v4i*)(buf + (bo ^ 64) + row * kStep);
+            if constexpr (BT) {
+                read_t<BN>(b[j], buf + BM * kStep, wn * TN + j, lane);
+            } else {
+                b[j][0] = *(const v4i*)(buf + bo + row * kStep);
+                b[j][1] = *(const v4i*)(buf + (bo ^ 64) + row * kStep);
+            }
         }
         v4f sbr[SM == kRowScale ? TN : 1];
         if constexpr (SM == kRowScale) {
@@ -264,9 +342,16 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         // are scaled and added.
         v4i a[2][2];
         v4f t[2][SM == kNoScale ? 1 : TN];
-        a[0][0] = *(const v4i*)(buf + ao);
-        a[0][1] = *(const v4i*)(buf + (ao ^ 64));
-        auto add = [&](int i) {
+        auto read_a = [&](int i) __attribute__((always_inline)) {
+            if constexpr (AT) {
+                read_t<BM>(a[i & 1], buf, wm * TM + i, lane);
+            } else {
+                a[i & 1][0] = *(const v4i*)(buf + ao + i * 16 * kStep);
+                a[i & 1][1] = *(const v4i*)(buf + (ao ^ 64) + i * 16 * kStep);
+            }
+        };
+        read_a(0);
+        auto add = [&](int i) __attribute__((always_inline)) {
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 const float s = sa[i] * (kDual && j >= TN / 2 ? sb[1] : sb[0]);
@@ -279,10 +364,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
         };
 #pragma unroll
         for (int i = 0; i < TM; ++i) {
-            if (i + 1 < TM) {
-                a[(i + 1) & 1][0] = *(const v4i*)(buf + ao + (i + 1) * 16 * kStep);
-                a[(i + 1) & 1][1] = *(const v4i*)(buf + (ao ^ 64) + (i + 1) * 16 * kStep);
-            }
+            if (i + 1 < TM)
+                read_a(i + 1);
 #pragma unroll
             for (int j = 0; j < TN; ++j) {
                 if constexpr (SM == kNoScale)
@@ -294,7 +377,7 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
                 if (i > 0)
                     add(i - 1);
             if (i + 1 < TM)
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);   // two LDS reads
+                __builtin_amdgcn_sched_group_barrier(0x100, AT ? 4 : 2, 0);   // LDS reads
             if constexpr (SM != kNoScale) {
 #pragma unroll
                 for (int j = 0; j < TN; ++j) {
@@ -317,16 +400,27 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const bool bf = p.ctype == kTBf16;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
-        const int r = wm * (TM * 16) + l16 * TM + i;
+        const int r = wm * (TM * 16) + (AT ? i * 16 + l16 : l16 * TM + i);
         if (r >= mrows)
             continue;
-        const int64_t m = m0 + r;
+        int64_t m = m0 + r;
+        void* c = p.c;
+        int64_t ldc = p.ldc;
+        if (AT && p.split) {      // rows from split on: another matrix
+            if (m >= p.split) {
+                m -= p.split;
+                c = p.c1;
+                ldc = p.ldc1;
+            }
+            if (m >= p.split_rows)
+                continue;
+        }
 #pragma unroll
         for (int j = 0; j < (kDual ? TN / 2 : TN); ++j) {
             const int nc = wn * kRowsB + j * 16 + q * 4;
             if (nc >= nrows)
                 continue;
-            const int64_t at = m * p.ldc + n0 + nc;
+            const int64_t at = m * ldc + n0 + nc;
             const int cnt = nrows - nc < 4 ? nrows - nc : 4;
             v4f v = acc[i][j], u;
             if constexpr (EP == kEpGate) {
@@ -345,25 +439,26 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
                     v[k] = g[k] * acc[i][j + TN / 2][k] * d;
                     u[k] = g[k] * f;
                 }
-                store4(p.c, at + p.n, u, p.ctype, cnt, p.wide_c);
+                store4(c, at + p.part_c, u, p.ctype, cnt, p.wide_c);
             }
-            store4(p.c, at, v, p.ctype, cnt, p.wide_c);
+            store4(c, at, v, p.ctype, cnt, p.wide_c);
         }
     }
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG = false>
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG = false,
+          bool AT = false, bool BT = false>
 hipError_t run(ProductArgs p, hipStream_t stream)
 {
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
     constexpr size_t kLds = 2 * (size_t)(BM + BN) * kStep;
     const int64_t csize = p.ctype == kTF32 ? 4 : 2;
-    p.wide_c = (((uintptr_t)p.c | (uintptr_t)(p.ldc * csize)) & (4 * csize - 1)) == 0 &&
-               (EP != kEpGateGrad || p.n % 4 == 0);
+    p.wide_c = (((uintptr_t)p.c | (uintptr_t)p.c1 | (uintptr_t)((p.ldc | p.ldc1 | p.part_c) * csize)) &
+                (4 * csize - 1)) == 0;
     p.wide_dh = (((uintptr_t)p.dh | (uintptr_t)(p.lddh * 2)) & 7) == 0;
     p.tiles_m = (int)((p.m + BM - 1) / BM);
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
-    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, EP, SM, REG>;
+    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, EP, SM, REG, AT, BT>;
     if (kLds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)k,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
@@ -374,24 +469,34 @@ hipError_t run(ProductArgs p, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <int TYPE, int EP, int SM>
+template <int TYPE, int EP, int SM, bool AT = false, bool BT = false>
 hipError_t pick(const ProductArgs& p, hipStream_t stream)
 {
-    if constexpr (EP != kEpStore && SM == kNoScale) {
+    if constexpr (SM == kNoScale) {
         const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 |
                               (uintptr_t)p.lda | (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
         if (any & 15)
-            return run<TYPE, 128, 128, 2, 2, EP, SM, true>(p, stream);
+            return run<TYPE, 128, 128, 2, 2, EP, SM, true, AT, BT>(p, stream);
     }
-    const int64_t bno = EP != kEpStore ? 128 : 256;
     // The widened operands, or a scale for each row of B, leave no registers
     // for the larger tile.
     if constexpr (TYPE != kTE4m3Exact && SM != kRowScale) {
         const int64_t bno = EP != kEpStore ? 128 : 256;
         if (((p.m + 255) / 256) * ((p.n + bno - 1) / bno) >= 192)
-            return run<TYPE, 256, 256, 2, 4, EP, SM>(p, stream);
+            return run<TYPE, 256, 256, 2, 4, EP, SM, false, AT, BT>(p, stream);
     }
-    return run<TYPE, 128, 128, 2, 2, EP, SM>(p, stream);
+    return run<TYPE, 128, 128, 2, 2, EP, SM, false, AT, BT>(p, stream);
+}
+
+template <int TYPE>
+hipError_t pick16(const ProductArgs& p, int ep, hipStream_t stream)
+{
+    if (ep == kEpGate)
+        return pick<TYPE, kEpGate, kNoScale>(p, stream);
+    if (ep == kEpGateGrad)
+        return pick<TYPE, kEpGateGrad, kNoScale>(p, stream);
+    return ep == kEpStoreT ? pick<TYPE, kEpStore, kNoScale, true, true>(p, stream)
+                           : pick<TYPE, kEpStore, kNoScale, false, true>(p, stream);
 }
 
 }  // namespace
@@ -399,7 +504,7 @@ hipError_t pick(const ProductArgs& p, hipStream_t stream)
 hipError_t launch_product(const ProductArgs& p, int type, int ep, bool row_scales,
                           hipStream_t stream)
 {
-    if (p.m <= kStripRows && ep != kEpGateGrad && (ep == kEpGate || type == kTE4m3))
+    if (p.m <= kStripRows && (ep == kEpGate || type == kTE4m3))
         return launch_strip(p, type, ep, row_scales, stream);
     if (type == kTE4m3 && p.ctype == kTF32) {
         if (ep == kEpGate)
@@ -413,18 +518,7 @@ hipError_t launch_product(const ProductArgs& p, int type, int ep, bool row_scale
         return row_scales ? pick<kTE4m3, kEpStore, kRowScale>(p, stream)
                           : pick<kTE4m3, kEpStore, kTileScale>(p, stream);
     }
-    if (type == kTBf16) {
-        if (ep == kEpGate)
-            return pick<kTBf16, kEpGate, kNoScale>(p, stream);
-        if (ep == kEpGateGrad)
-            return pick<kTBf16, kEpGateGrad, kNoScale>(p, stream);
-        return pick<kTBf16, kEpStore, kNoScale>(p, stream);
-    }
-    if (ep == kEpGate)
-        return pick<kTF16, kEpGate, kNoScale>(p, stream);
-    if (ep == kEpGateGrad)
-        return pick<kTF16, kEpGateGrad, kNoScale>(p, stream);
-    return pick<kTF16, kEpStore, kNoScale>(p, stream);
+    return type == kTBf16 ? pick16<kTBf16>(p, ep, stream) : pick16<kTF16>(p, ep, stream);
 }
 
 }  // namespace qse

@@ -377,29 +377,6 @@ hipError_t rotate(const RotateArgs& p, bool tile, bool transpose, hipStream_t st
     return e != hipSuccess ? e : rows<TYPE, kTileGiven>(p, norm, stream);
 }
 
-// 64 x 64 tiles of 16-bit words through LDS.
-__global__ __launch_bounds__(256) void transpose16_kernel(const unsigned short* src, int64_t lds_,
-                                                          unsigned short* dst, int64_t ldd,
-                                                          int64_t rows, int64_t cols)
-{
-    __shared__ unsigned short tile[64][66];
-    const int64_t r0 = (int64_t)blockIdx.y * 64, c0 = (int64_t)blockIdx.x * 64;
-    const int x = threadIdx.x & 63, y = threadIdx.x >> 6;
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t r = r0 + y + 4 * i, c = c0 + x;
-        if (r < rows && c < cols)
-            tile[y + 4 * i][x] = src[r * lds_ + c];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int64_t c = c0 + y + 4 * i, r = r0 + x;
-        if (r < rows && c < cols)
-            dst[c * ldd + r] = tile[x][y + 4 * i];
-    }
-}
-
 __global__ __launch_bounds__(256) void zero16_kernel(unsigned short* dst, int64_t ld, int64_t rows,
                                                      int64_t cols)
 {
@@ -434,16 +411,6 @@ hipError_t launch_rotate(const RotateArgs& p, int type, bool tile, bool transpos
     if (type == kTBf16)
         return rotate<kTBf16>(p, tile, transpose, stream);
     return rotate<kTF16>(p, tile, transpose, stream);
-}
-
-hipError_t launch_transpose16(const void* src, int64_t lds, void* dst, int64_t ldd, int64_t rows,
-                              int64_t cols, hipStream_t stream)
-{
-    hipLaunchKernelGGL(transpose16_kernel,
-                       dim3((unsigned)((cols + 63) / 64), (unsigned)((rows + 63) / 64)), dim3(256),
-                       0, stream, (const unsigned short*)src, lds, (unsigned short*)dst, ldd, rows,
-                       cols);
-    return hipGetLastError();
 }
 
 }  // namespace qse
