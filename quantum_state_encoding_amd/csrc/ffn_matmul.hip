@@ -102,7 +102,8 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 // AT, BT: A or B is stored [k][rows].  With p.parts = 2 the contraction goes
 // on in a second B (b1), for columns part_a bytes further on in A's rows.
 template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG, bool AT, bool BT>
-__global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs p)
+__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void
+product_kernel(const ProductArgs p)
 {
     constexpr int W = WM * WN;                   // waves
     constexpr bool kDual = EP != kEpStore;
@@ -237,6 +238,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
     const int q = lane >> 4, l16 = lane & 15;
     float sa[TM], sa_next[TM];
     float sb[2], sb_next[2];
+    v4f sbr_next[SM == kRowScale ? TN : 1];
+    const int nleft = nrows > wn * kRowsB ? nrows - wn * kRowsB : 0;
     // (a wave whose columns all lie past n takes the last scale)
     const int64_t nbw = (n0 + wn * kRowsB) / kFfnBlock;
     const int64_t nb0 = nbw < p.sb_n ? nbw : p.sb_n - 1;
@@ -250,6 +253,12 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
 #pragma unroll
                 for (int r = 0; r < 4; ++r)
                     sa_next[i + r] = v[r];
+            }
+            if constexpr (SM == kRowScale) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    sbr_next[j] = load_row_scales(p.sb0 + (int64_t)kt * p.sb_n + n0 + wn * kRowsB,
+                                                  nleft, j * 16 + q * 4);
             }
             if constexpr (SM == kTileScale) {
                 sb_next[0] = p.sb0[(int64_t)kt * p.sb_n + nb0];
@@ -308,6 +317,12 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
 #pragma unroll
         for (int i = 0; i < TM; ++i)
             sa[i] = sa_next[i];
+        v4f sbr[SM == kRowScale ? TN : 1];
+        if constexpr (SM == kRowScale) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                sbr[j] = sbr_next[j];
+        }
         if (kt + 1 < nk) {
             if constexpr (REG)
                 fetch(kt + 1);
@@ -326,17 +341,8 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
                 b[j][1] = *(const v4i*)(buf + (bo ^ 64) + row * kStep);
             }
         }
-        v4f sbr[SM == kRowScale ? TN : 1];
-        if constexpr (SM == kRowScale) {
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    int n = wn * kRowsB + j * 16 + q * 4 + r;
-                    n = n < nrows ? n : nrows - 1;
-                    sbr[j][r] = p.sb0[(int64_t)kt * p.sb_n + n0 + n];
-                }
-        }
+        constexpr int kMfmas = TYPE == kTE4m3Exact ? 4 : 1;
+        constexpr int kValus = TYPE == kTE4m3Exact ? 4 : SM == kRowScale ? 8 : 5;
         // Rows of A in turn: while the matrix instructions of one run, the
         // next one's operand comes from LDS, and the sums of the last one
         // are scaled and added.
@@ -380,9 +386,9 @@ __global__ __launch_bounds__(64 * WM * WN) void product_kernel(const ProductArgs
                 __builtin_amdgcn_sched_group_barrier(0x100, AT ? 4 : 2, 0);   // LDS reads
             if constexpr (SM != kNoScale) {
 #pragma unroll
-                for (int j = 0; j < TN; ++j) {
+                for (int j = 0; j < TN * kMfmas; ++j) {
                     __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix
-                    __builtin_amdgcn_sched_group_barrier(0x002, 5, 0);   // vector
+                    __builtin_amdgcn_sched_group_barrier(0x002, kValus, 0);   // vector
                 }
             }
             __builtin_amdgcn_sched_barrier(0);
