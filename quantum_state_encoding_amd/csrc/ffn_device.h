@@ -40,6 +40,15 @@ __device__ __forceinline__ void load_to_lds(v4i rsrc, unsigned lds, unsigned vof
                  : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
                  : "memory");
 }
+// The same, four bytes a lane.
+__device__ __forceinline__ void load4_to_lds(v4i rsrc, unsigned lds, unsigned voff)
+{
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(voff), "s"(rsrc)
+                 : "memory");
+}
+// Waits until at most the last N memory operations of the wave are unfinished.
 template <int N>
 __device__ __forceinline__ void wait_vm()
 {

@@ -66,13 +66,6 @@ __device__ __forceinline__ v4i chunk_at(const char* p, int left)
     return v;
 }
 
-// Scales at .. at + 3 of the `left` ones from p.
-__device__ __forceinline__ v4f load_row_scales(const float* p, int left, int at)
-{
-    const auto rsrc = __builtin_amdgcn_make_buffer_rsrc((void*)p, 0, left * 4, (int)kRsrcFlags);
-    return __builtin_bit_cast(v4f, __builtin_amdgcn_raw_buffer_load_b128(rsrc, at * 4, 0, 0));
-}
-
 // An operand that is stored with its rows side by side, [k][rows] (AT, BT;
 // 16-bit types): a step stages 64 k of it as they are, and the transposing
 // LDS read gives a lane four k of its row.  Its 16 lanes take four k rows of
@@ -101,7 +94,8 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 // registers, loaded before a step's products and stored to LDS after them.
 // AT, BT: A or B is stored [k][rows].  With p.parts = 2 the contraction goes
 // on in a second B (b1), for columns part_a bytes further on in A's rows.
-template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG, bool AT, bool BT>
+template <int TYPE, int BM, int BN, int WM, int WN, int NS, int EP, int SM, bool REG, bool AT,
+          bool BT>
 __global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void
 product_kernel(const ProductArgs p)
 {
@@ -111,7 +105,9 @@ product_kernel(const ProductArgs p)
     constexpr int TN = BN / WN / 16;             // of B (dual: half gate, half up)
     constexpr int BNO = kDual ? BN / 2 : BN;     // output columns of the tile
     constexpr int GA = BM / 8 / W, GB = BN / 8 / W;
-    constexpr int kBuf = (BM + BN) * kStep;
+    constexpr int kScaleBytes = SM != kNoScale ? (BM + BN) * 4 : 0;
+    constexpr int kBuf = (BM + BN) * kStep + kScaleBytes;   // rows, then their scales
+    constexpr int kLoads = GA + GB + (SM != kNoScale ? 1 : 0);   // of a wave and step
     static_assert(BM % (8 * W) == 0 && BNO % (8 * W) == 0, "whole 8-row groups per wave");
     extern __shared__ __align__(16) unsigned char lds[];
 
@@ -197,15 +193,25 @@ product_kernel(const ProductArgs p)
 #pragma unroll
         for (int g = 0; g < GA + GB; ++g) {
             const int gg = g >= GA ? g - GA : g;
-            *(v4i*)(lds + (kt & 1) * kBuf + (g >= GA ? BM * kStep : 0) + (wave + gg * W) * 1024 +
+            *(v4i*)(lds + (kt & (NS - 1)) * kBuf + (g >= GA ? BM * kStep : 0) + (wave + gg * W) * 1024 +
                     lane * 16) = held[g];
         }
     };
     const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
+    // Scales of the wave's 64 rows of the tile: a lane's row, in rows of A or
+    // B or past the last one (which repeats it).
+    const int srow = wave * 64 < BM ? wave * 64 : wave * 64 - BM;   // B: from gate's first
+    const bool sup = kDual && wave * 64 >= BM + BNO;
+    const float* sbase = wave * 64 < BM ? p.sa : sup ? p.sb1 : p.sb0;
+    const int64_t sn = wave * 64 < BM ? p.m : p.sb_n;
+    int64_t sat = srow - (sup ? BNO : 0) + lane + (wave * 64 < BM ? m0 : n0);
+    if (SM == kTileScale && wave * 64 >= BM)
+        sat /= kFfnBlock;
+    const unsigned vs = (unsigned)(sat < sn ? sat : sn - 1) * 4;
     auto stage = [=](int kt) __attribute__((always_inline)) {
         const bool second = BT && p.parts > 1 && kt >= nks;
         const int ks = second ? kt - nks : kt;
-        const unsigned base = lds0 + (kt & 1) * kBuf + wave * 1024;
+        const unsigned base = lds0 + (kt & (NS - 1)) * kBuf + wave * 1024;
         const unsigned so = (unsigned)ks * kStep;
         const v4i da = AT ? rows_of_k(p.a, p.lda, m0, p.m, ks) : ra;
         const v4i db =
@@ -223,6 +229,9 @@ product_kernel(const ProductArgs p)
                         BT ? (unsigned)(g * 16 * (second ? p.ldb1 : p.ldb0))
                            : so + (unsigned)((up ? g - GB / 2 : g) * 8 * W * (up ? p.ldb1 : p.ldb0)));
         }
+        if constexpr (SM != kNoScale)
+            load4_to_lds(make_rsrc(sbase + (int64_t)ks * sn, (uint64_t)sn * 4),
+                         base - wave * 1024 + (BM + BN) * kStep + wave * 256, vs);
     };
 
     const int nk = p.parts > 1 ? 2 * nks : nks;
@@ -236,56 +245,33 @@ product_kernel(const ProductArgs p)
     // Scales: rows of A stand on lanes, TM consecutive ones on a lane (that is
     // what row_of is for), rows of B on the four registers of a result.
     const int q = lane >> 4, l16 = lane & 15;
-    float sa[TM], sa_next[TM];
-    float sb[2], sb_next[2];
-    v4f sbr_next[SM == kRowScale ? TN : 1];
-    const int nleft = nrows > wn * kRowsB ? nrows - wn * kRowsB : 0;
-    // (a wave whose columns all lie past n takes the last scale)
-    const int64_t nbw = (n0 + wn * kRowsB) / kFfnBlock;
-    const int64_t nb0 = nbw < p.sb_n ? nbw : p.sb_n - 1;
-    const int mleft = mrows > wm * TM * 16 ? mrows - wm * TM * 16 : 0;
-    auto load_scales = [&](int kt) __attribute__((always_inline)) {
-        if constexpr (SM != kNoScale) {
-#pragma unroll
-            for (int i = 0; i < TM; i += 4) {
-                const v4f v = load_row_scales(p.sa + (int64_t)kt * p.m + m0 + wm * TM * 16, mleft,
-                                              l16 * TM + i);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    sa_next[i + r] = v[r];
-            }
-            if constexpr (SM == kRowScale) {
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    sbr_next[j] = load_row_scales(p.sb0 + (int64_t)kt * p.sb_n + n0 + wn * kRowsB,
-                                                  nleft, j * 16 + q * 4);
-            }
-            if constexpr (SM == kTileScale) {
-                sb_next[0] = p.sb0[(int64_t)kt * p.sb_n + nb0];
-                if constexpr (kDual)
-                    sb_next[1] = p.sb1[(int64_t)kt * p.sb_n + nb0];
-            }
-        }
-    };
-
     if constexpr (REG) {
         fetch(0);
         put(0);
     } else {
-        stage(0);
+#pragma unroll
+        for (int s = 0; s < NS - 1; ++s)
+            if (s < nk)
+                stage(s);
     }
-    load_scales(0);
     const int swz = l16 >> 1;
     const int ao = (wm * TM * 16 + l16) * kStep + ((q ^ swz) * 16);
     // B rows of this wave in LDS: gate rows, then up rows BNO further on.
     const int bo = (BM + wn * kRowsB + l16) * kStep + ((q ^ swz) * 16);
+    const int so = (BM + BN) * kStep + (wm * TM * 16 + l16 * TM) * 4;   // scales of A's rows
+    const int sbo = (BM + BN) * kStep + (BM + wn * kRowsB + q * 4) * 4;
     const int ktail = (int)(p.kbytes % kStep);
 
     for (int kt = 0; kt < nk; ++kt) {
-        if constexpr (!REG)
-            wait_vm<0>();
+        // The step's own loads have arrived, those of later steps go on.
+        if constexpr (!REG) {
+            if (NS > 2 && kt + NS - 2 < nk)
+                wait_vm<(NS - 2) * kLoads>();
+            else
+                wait_vm<0>();
+        }
         __syncthreads();
-        unsigned char* buf = lds + (kt & 1) * kBuf;
+        unsigned char* buf = lds + (kt & (NS - 1)) * kBuf;
         if (!REG && ktail && (kt == nk - 1 || kt == nks - 1)) {
             // Past the end of k both operands are 0, whatever was read there.
             if constexpr (AT)
@@ -312,23 +298,27 @@ product_kernel(const ProductArgs p)
             }
             __syncthreads();
         }
-        sb[0] = sb_next[0];
-        sb[1] = sb_next[1];
-#pragma unroll
-        for (int i = 0; i < TM; ++i)
-            sa[i] = sa_next[i];
-        v4f sbr[SM == kRowScale ? TN : 1];
-        if constexpr (SM == kRowScale) {
-#pragma unroll
-            for (int j = 0; j < TN; ++j)
-                sbr[j] = sbr_next[j];
-        }
-        if (kt + 1 < nk) {
-            if constexpr (REG)
+        if constexpr (REG) {
+            if (kt + 1 < nk)
                 fetch(kt + 1);
-            else
-                stage(kt + 1);
-            load_scales(kt + 1);
+        } else if (kt + NS - 1 < nk) {
+            stage(kt + NS - 1);
+        }
+        float sa[TM], sb[2];
+        v4f sbr[TN];
+        if constexpr (SM != kNoScale) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                sa[i] = ((const float*)(buf + so))[i];
+            if constexpr (SM == kRowScale) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    sbr[j] = *(const v4f*)(buf + sbo + j * 64);
+            } else {
+                sb[0] = *(const float*)(buf + sbo);
+                if constexpr (kDual)
+                    sb[1] = *(const float*)(buf + sbo + BNO * 4);
+            }
         }
         v4i b[TN][2];
 #pragma unroll
@@ -452,19 +442,19 @@ product_kernel(const ProductArgs p)
     }
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int EP, int SM, bool REG = false,
+template <int TYPE, int BM, int BN, int WM, int WN, int NS, int EP, int SM, bool REG = false,
           bool AT = false, bool BT = false>
 hipError_t run(ProductArgs p, hipStream_t stream)
 {
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
-    constexpr size_t kLds = 2 * (size_t)(BM + BN) * kStep;
+    constexpr size_t kLds = NS * (size_t)(BM + BN) * (kStep + (SM != kNoScale ? 4 : 0));
     const int64_t csize = p.ctype == kTF32 ? 4 : 2;
     p.wide_c = (((uintptr_t)p.c | (uintptr_t)p.c1 | (uintptr_t)((p.ldc | p.ldc1 | p.part_c) * csize)) &
                 (4 * csize - 1)) == 0;
     p.wide_dh = (((uintptr_t)p.dh | (uintptr_t)(p.lddh * 2)) & 7) == 0;
     p.tiles_m = (int)((p.m + BM - 1) / BM);
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
-    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, EP, SM, REG, AT, BT>;
+    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, NS, EP, SM, REG, AT, BT>;
     if (kLds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)k,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
@@ -482,16 +472,16 @@ hipError_t pick(const ProductArgs& p, hipStream_t stream)
         const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 |
                               (uintptr_t)p.lda | (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
         if (any & 15)
-            return run<TYPE, 128, 128, 2, 2, EP, SM, true, AT, BT>(p, stream);
+            return run<TYPE, 128, 128, 2, 2, 2, EP, SM, true, AT, BT>(p, stream);
     }
     // The widened operands, or a scale for each row of B, leave no registers
     // for the larger tile.
     if constexpr (TYPE != kTE4m3Exact && SM != kRowScale) {
         const int64_t bno = EP != kEpStore ? 128 : 256;
         if (((p.m + 255) / 256) * ((p.n + bno - 1) / bno) >= 192)
-            return run<TYPE, 256, 256, 2, 4, EP, SM, false, AT, BT>(p, stream);
+            return run<TYPE, 256, 256, 2, 4, 2, EP, SM, false, AT, BT>(p, stream);
     }
-    return run<TYPE, 128, 128, 2, 2, EP, SM, false, AT, BT>(p, stream);
+    return run<TYPE, 128, 128, 2, 2, 2, EP, SM, false, AT, BT>(p, stream);
 }
 
 template <int TYPE>
