@@ -94,12 +94,14 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 // registers, loaded before a step's products and stored to LDS after them.
 // AT, BT: A or B is stored [k][rows].  With p.parts = 2 the contraction goes
 // on in a second B (b1), for columns part_a bytes further on in A's rows.
-template <int TYPE, int BM, int BN, int WM, int WN, int NS, int EP, int SM, bool REG, bool AT,
-          bool BT>
-__global__ __launch_bounds__(64 * WM * WN) __attribute__((amdgpu_waves_per_eu(2))) void
+// WK groups of WM x WN waves compute the tile, each WKth step of k; LDS holds
+// NS rounds of them.
+template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, bool REG,
+          bool AT, bool BT>
+__global__ __launch_bounds__(64 * WM * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void
 product_kernel(const ProductArgs p)
 {
-    constexpr int W = WM * WN;                   // waves
+    constexpr int W = WM * WN;                   // waves of a group
     constexpr bool kDual = EP != kEpStore;
     constexpr int TM = BM / WM / 16;             // 16-row blocks of A per wave
     constexpr int TN = BN / WN / 16;             // of B (dual: half gate, half up)
@@ -108,11 +110,15 @@ product_kernel(const ProductArgs p)
     constexpr int kScaleBytes = SM != kNoScale ? (BM + BN) * 4 : 0;
     constexpr int kBuf = (BM + BN) * kStep + kScaleBytes;   // rows, then their scales
     constexpr int kLoads = GA + GB + (SM != kNoScale ? 1 : 0);   // of a wave and step
+    static_assert(SM == kNoScale || (BM % 64 == 0 && BNO % 64 == 0 && BM + BN <= 64 * W),
+                  "scales: a wave for 64 rows");
     static_assert(BM % (8 * W) == 0 && BNO % (8 * W) == 0, "whole 8-row groups per wave");
     extern __shared__ __align__(16) unsigned char lds[];
 
     const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int wave = __builtin_amdgcn_readfirstlane(((int)threadIdx.x >> 6) % W);
+    const int kg = __builtin_amdgcn_readfirstlane((int)threadIdx.x / (64 * W));
+    const int tid = (int)threadIdx.x - kg * 64 * W;   // in the group
     const int wm = wave / WN, wn = wave % WN;
     int tm, tn;
     tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
@@ -152,6 +158,10 @@ product_kernel(const ProductArgs p)
         const int64_t left = p.kbytes / 2 - (int64_t)ks * 64;
         return make_rsrc((const char*)base + (int64_t)ks * 64 * ld + r0 * 2,
                          (uint64_t)((left - 1) * ld + (((rows - r0) * 2 + 15) & ~(int64_t)15)));
+    };
+    // step kt = round * WK + group
+    auto buffer_of = [=](int kt) __attribute__((always_inline)) {
+        return (((kt / WK) & (NS - 1)) * WK + kg) * kBuf;
     };
     v4i held[REG ? GA + GB : 1];
     auto fetch = [&](int kt) __attribute__((always_inline)) {
@@ -193,25 +203,25 @@ product_kernel(const ProductArgs p)
 #pragma unroll
         for (int g = 0; g < GA + GB; ++g) {
             const int gg = g >= GA ? g - GA : g;
-            *(v4i*)(lds + (kt & (NS - 1)) * kBuf + (g >= GA ? BM * kStep : 0) + (wave + gg * W) * 1024 +
+            *(v4i*)(lds + buffer_of(kt) + (g >= GA ? BM * kStep : 0) + (wave + gg * W) * 1024 +
                     lane * 16) = held[g];
         }
     };
     const unsigned lds0 = (unsigned)(uintptr_t)(__attribute__((address_space(3))) void*)lds;
-    // Scales of the wave's 64 rows of the tile: a lane's row, in rows of A or
-    // B or past the last one (which repeats it).
-    const int srow = wave * 64 < BM ? wave * 64 : wave * 64 - BM;   // B: from gate's first
-    const bool sup = kDual && wave * 64 >= BM + BNO;
-    const float* sbase = wave * 64 < BM ? p.sa : sup ? p.sb1 : p.sb0;
-    const int64_t sn = wave * 64 < BM ? p.m : p.sb_n;
-    int64_t sat = srow - (sup ? BNO : 0) + lane + (wave * 64 < BM ? m0 : n0);
-    if (SM == kTileScale && wave * 64 >= BM)
+    // Scales of 64 rows of the tile per wave (waves past them repeat the last
+    // 64): a lane's row, in rows of A or B; past the last one, the last.
+    const int sw = wave < (BM + BN) / 64 ? wave : (BM + BN) / 64 - 1;
+    const bool sup = kDual && sw * 64 >= BM + BNO;
+    const float* sbase = sw * 64 < BM ? p.sa : sup ? p.sb1 : p.sb0;
+    const int64_t sn = sw * 64 < BM ? p.m : p.sb_n;
+    int64_t sat = sw * 64 + lane + (sw * 64 < BM ? m0 : n0 - BM - (sup ? BNO : 0));
+    if (SM == kTileScale && sw * 64 >= BM)
         sat /= kFfnBlock;
     const unsigned vs = (unsigned)(sat < sn ? sat : sn - 1) * 4;
     auto stage = [=](int kt) __attribute__((always_inline)) {
         const bool second = BT && p.parts > 1 && kt >= nks;
         const int ks = second ? kt - nks : kt;
-        const unsigned base = lds0 + (kt & (NS - 1)) * kBuf + wave * 1024;
+        const unsigned base = lds0 + buffer_of(kt) + wave * 1024;
         const unsigned so = (unsigned)ks * kStep;
         const v4i da = AT ? rows_of_k(p.a, p.lda, m0, p.m, ks) : ra;
         const v4i db =
@@ -231,7 +241,7 @@ product_kernel(const ProductArgs p)
         }
         if constexpr (SM != kNoScale)
             load4_to_lds(make_rsrc(sbase + (int64_t)ks * sn, (uint64_t)sn * 4),
-                         base - wave * 1024 + (BM + BN) * kStep + wave * 256, vs);
+                         base - wave * 1024 + (BM + BN) * kStep + sw * 256, vs);
     };
 
     const int nk = p.parts > 1 ? 2 * nks : nks;
@@ -246,13 +256,15 @@ product_kernel(const ProductArgs p)
     // what row_of is for), rows of B on the four registers of a result.
     const int q = lane >> 4, l16 = lane & 15;
     if constexpr (REG) {
-        fetch(0);
-        put(0);
+        if (kg < nk) {
+            fetch(kg);
+            put(kg);
+        }
     } else {
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s)
-            if (s < nk)
-                stage(s);
+            if (s * WK + kg < nk)
+                stage(s * WK + kg);
     }
     const int swz = l16 >> 1;
     const int ao = (wm * TM * 16 + l16) * kStep + ((q ^ swz) * 16);
@@ -262,25 +274,27 @@ product_kernel(const ProductArgs p)
     const int sbo = (BM + BN) * kStep + (BM + wn * kRowsB + q * 4) * 4;
     const int ktail = (int)(p.kbytes % kStep);
 
-    for (int kt = 0; kt < nk; ++kt) {
+    for (int kt = kg; kt - kg < nk; kt += WK) {
         // The step's own loads have arrived, those of later steps go on.
         if constexpr (!REG) {
-            if (NS > 2 && kt + NS - 2 < nk)
+            if (NS > 2 && kt + (NS - 2) * WK < nk)
                 wait_vm<(NS - 2) * kLoads>();
             else
                 wait_vm<0>();
         }
         __syncthreads();
-        unsigned char* buf = lds + (kt & (NS - 1)) * kBuf;
-        if (!REG && ktail && (kt == nk - 1 || kt == nks - 1)) {
+        unsigned char* buf = lds + buffer_of(kt);
+        const int k0 = kt - kg;      // the round's first step
+        if (!REG && ktail && (k0 + WK >= nk || (p.parts > 1 && k0 < nks && k0 + WK >= nks))) {
             // Past the end of k both operands are 0, whatever was read there.
+            const bool mine = kt == nk - 1 || kt == nks - 1;
             if constexpr (AT)
-                for (int c = (ktail / 2) * kCa + threadIdx.x; c < BM * 8; c += 64 * W)
+                for (int c = (ktail / 2) * kCa + tid; mine && c < BM * 8; c += 64 * W)
                     *(v4i*)(buf + c * 16) = v4i{0, 0, 0, 0};
             if constexpr (BT)
-                for (int c = (ktail / 2) * kCb + threadIdx.x; c < BN * 8; c += 64 * W)
+                for (int c = (ktail / 2) * kCb + tid; mine && c < BN * 8; c += 64 * W)
                     *(v4i*)(buf + BM * kStep + c * 16) = v4i{0, 0, 0, 0};
-            for (int r = threadIdx.x + (AT ? BM : 0); r < BM + (BT ? 0 : BN); r += 64 * W) {
+            for (int r = tid + (AT ? BM : 0); mine && r < BM + (BT ? 0 : BN); r += 64 * W) {
                 for (int c = ktail >> 4; c < 8; ++c) {
                     v4i* at = (v4i*)(buf + r * kStep + slot(r, c) * 16);
                     const int keep = ktail - c * 16;   // bytes of this chunk
@@ -299,11 +313,13 @@ product_kernel(const ProductArgs p)
             __syncthreads();
         }
         if constexpr (REG) {
-            if (kt + 1 < nk)
-                fetch(kt + 1);
-        } else if (kt + NS - 1 < nk) {
-            stage(kt + NS - 1);
+            if (kt + WK < nk)
+                fetch(kt + WK);
+        } else if (kt + (NS - 1) * WK < nk) {
+            stage(kt + (NS - 1) * WK);
         }
+        if (WK > 1 && kt >= nk)
+            break;     // (the last round: no barrier follows in the loop)
         float sa[TM], sb[2];
         v4f sbr[TN];
         if constexpr (SM != kNoScale) {
@@ -386,9 +402,32 @@ product_kernel(const ProductArgs p)
         if constexpr (SM != kNoScale)
             add(TM - 1);
         if constexpr (REG) {
-            if (kt + 1 < nk)
-                put(kt + 1);
+            if (kt + WK < nk)
+                put(kt + WK);
         }
+    }
+
+    // The groups' sums join in LDS, in the groups' order.
+    if constexpr (WK > 1) {
+        v4f* sums = (v4f*)lds;     // [group - 1][i][j][thread]
+        __syncthreads();
+        if (kg > 0) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    sums[(((kg - 1) * TM + i) * TN + j) * 64 * W + tid] = acc[i][j];
+        }
+        __syncthreads();
+        if (kg > 0)
+            return;
+#pragma unroll
+        for (int g = 0; g < WK - 1; ++g)
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] += sums[((g * TM + i) * TN + j) * 64 * W + tid];
     }
 
     // Results: lane l holds rows l % 16 * TM .. of A and four consecutive rows
@@ -442,26 +481,27 @@ product_kernel(const ProductArgs p)
     }
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int NS, int EP, int SM, bool REG = false,
+template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, bool REG = false,
           bool AT = false, bool BT = false>
 hipError_t run(ProductArgs p, hipStream_t stream)
 {
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
-    constexpr size_t kLds = NS * (size_t)(BM + BN) * (kStep + (SM != kNoScale ? 4 : 0));
+    constexpr size_t kLds = WK * NS * (size_t)(BM + BN) * (kStep + (SM != kNoScale ? 4 : 0));
+    static_assert(kLds <= 160 * 1024 && (size_t)(WK - 1) * BM * BN * 4 <= kLds, "LDS of a CU");
     const int64_t csize = p.ctype == kTF32 ? 4 : 2;
     p.wide_c = (((uintptr_t)p.c | (uintptr_t)p.c1 | (uintptr_t)((p.ldc | p.ldc1 | p.part_c) * csize)) &
                 (4 * csize - 1)) == 0;
     p.wide_dh = (((uintptr_t)p.dh | (uintptr_t)(p.lddh * 2)) & 7) == 0;
     p.tiles_m = (int)((p.m + BM - 1) / BM);
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
-    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, NS, EP, SM, REG, AT, BT>;
+    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT>;
     if (kLds > 65536) {
         const hipError_t e = hipFuncSetAttribute((const void*)k,
                                                  hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(k, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(64 * WM * WN), kLds, stream, p);
+    hipLaunchKernelGGL(k, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(64 * WM * WN * WK), kLds, stream, p);
     return hipGetLastError();
 }
 
@@ -472,16 +512,16 @@ hipError_t pick(const ProductArgs& p, hipStream_t stream)
         const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 |
                               (uintptr_t)p.lda | (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
         if (any & 15)
-            return run<TYPE, 128, 128, 2, 2, 2, EP, SM, true, AT, BT>(p, stream);
+            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM, true, AT, BT>(p, stream);
     }
     // The widened operands, or a scale for each row of B, leave no registers
     // for the larger tile.
     if constexpr (TYPE != kTE4m3Exact && SM != kRowScale) {
         const int64_t bno = EP != kEpStore ? 128 : 256;
         if (((p.m + 255) / 256) * ((p.n + bno - 1) / bno) >= 192)
-            return run<TYPE, 256, 256, 2, 4, 2, EP, SM, false, AT, BT>(p, stream);
+            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, SM, false, AT, BT>(p, stream);
     }
-    return run<TYPE, 128, 128, 2, 2, 2, EP, SM, false, AT, BT>(p, stream);
+    return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM, false, AT, BT>(p, stream);
 }
 
 template <int TYPE>
