@@ -63,7 +63,7 @@ struct ProductArgs {
 hipError_t launch_product(const ProductArgs& p, int type, int epilogue, bool row_scales,
                           hipStream_t stream);
 // Its form for few rows of A (kEpStore: e4m3 only).
-constexpr int kStripRows = 64;
+constexpr int kStripRows = 32;
 hipError_t launch_strip(const ProductArgs& p, int type, int epilogue, bool row_scales,
                         hipStream_t stream);
 

@@ -10,6 +10,8 @@
 // LDS buffers while the other feeds the matrix instructions.
 #include <hip/hip_runtime.h>
 
+#include <atomic>
+
 #include "ffn_device.h"
 
 namespace qse {
@@ -496,8 +498,16 @@ hipError_t run(ProductArgs p, hipStream_t stream)
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
     auto* k = &product_kernel<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT>;
     if (kLds > 65536) {
-        const hipError_t e = hipFuncSetAttribute((const void*)k,
-                                                 hipFuncAttributeMaxDynamicSharedMemorySize, (int)kLds);
+        // once for each device
+        static std::atomic<uint64_t> done{0};
+        int dev = 0;
+        hipError_t e = hipGetDevice(&dev);
+        if (e == hipSuccess && (dev >= 64 || !((done.load() >> dev) & 1))) {
+            e = hipFuncSetAttribute((const void*)k, hipFuncAttributeMaxDynamicSharedMemorySize,
+                                    (int)kLds);
+            if (e == hipSuccess && dev < 64)
+                done.fetch_or((uint64_t)1 << dev);
+        }
         if (e != hipSuccess)
             return e;
     }
@@ -505,34 +515,149 @@ hipError_t run(ProductArgs p, hipStream_t stream)
     return hipGetLastError();
 }
 
-template <int TYPE, int EP, int SM, bool AT = false, bool BT = false>
-hipError_t pick(const ProductArgs& p, hipStream_t stream)
+// Which tile.  A round of workgroups (one on each of 256 CUs, or two where
+// two fit) takes about a fixed time for each 128-byte step of k, so a product
+// takes ceil(tiles / slots) of those.  Microseconds a step, measured with full
+// rounds at k of 16384 bytes and more:
+//                                  slots   e4m3   fp32 out   16 bits
+//   256 x 256                        256   1.75      -         1.6
+//   128 x 128, two on a CU           512   1.05     2.0        1.06
+//   128 x 128, deeper (*)            256   0.65     1.1        0.62
+//   64 x 64, two on a CU             512   0.40     0.70        -
+//   64 x 64 (gated: 64 x 128)        256   0.26     0.36       0.42
+// (*) two groups of waves for e4m3, four rounds in LDS for 16 bits.  So m 512
+// n 4096 k 16384 (e4m3) takes 49 us with 64 x 64 tiles and 82 with 128 x 128
+// ones, m 4096 takes 451 and 260, and 227 with 256 x 256 ones.
+struct Tile {
+    int bm, bn, slots;   // bn: output columns
+    float step;
+};
+template <int N>
+int cheapest(const Tile (&tiles)[N], int64_t m, int64_t n)
 {
-    if constexpr (SM == kNoScale) {
-        const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 |
-                              (uintptr_t)p.lda | (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
-        if (any & 15)
-            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM, true, AT, BT>(p, stream);
+    int best = 0;
+    double least = 0;
+    for (int i = 0; i < N; ++i) {
+        const int64_t count = ((m + tiles[i].bm - 1) / tiles[i].bm) *
+                              ((n + tiles[i].bn - 1) / tiles[i].bn);
+        const double cost = (double)((count + tiles[i].slots - 1) / tiles[i].slots) * tiles[i].step;
+        if (i == 0 || cost < least) {
+            best = i;
+            least = cost;
+        }
     }
-    // The widened operands, or a scale for each row of B, leave no registers
-    // for the larger tile.
-    if constexpr (TYPE != kTE4m3Exact && SM != kRowScale) {
-        const int64_t bno = EP != kEpStore ? 128 : 256;
-        if (((p.m + 255) / 256) * ((p.n + bno - 1) / bno) >= 192)
-            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, SM, false, AT, BT>(p, stream);
+    return best;
+}
+
+// 16-bit operands.
+template <int TYPE, int EP, bool AT, bool BT>
+hipError_t pick16(const ProductArgs& p, hipStream_t stream)
+{
+    const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 | (uintptr_t)p.lda |
+                          (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
+    if (any & 15)
+        return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, true, AT, BT>(p, stream);
+    if constexpr (EP == kEpStore) {
+        constexpr Tile tiles[] = {{256, 256, 256, 1.6f}, {128, 128, 512, 1.06f}, {128, 128, 256, .62f}};
+        switch (cheapest(tiles, p.m, p.n)) {
+        case 0:
+            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, false, AT, BT>(p, stream);
+        case 1:
+            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, false, AT, BT>(p, stream);
+        default:
+            return run<TYPE, 128, 128, 2, 2, 1, 4, EP, kNoScale, false, AT, BT>(p, stream);
+        }
+    } else {
+        constexpr Tile tiles[] = {{256, 128, 256, 1.6f}, {128, 64, 512, 1.06f}, {128, 64, 256, .62f},
+                                  {64, 64, 256, .42f}};
+        switch (cheapest(tiles, p.m, p.n)) {
+        case 0:
+            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale>(p, stream);
+        case 1:
+            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale>(p, stream);
+        case 2:
+            return run<TYPE, 128, 128, 2, 2, 1, 4, EP, kNoScale>(p, stream);
+        default:
+            return run<TYPE, 64, 128, 1, 4, 1, 4, EP, kNoScale>(p, stream);
+        }
     }
-    return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM, false, AT, BT>(p, stream);
+}
+
+// e4m3 operands.  The widened operands of an fp32 result, or a scale for each
+// row of B, leave no registers for the largest tile.
+template <int TYPE, int EP, int SM>
+hipError_t pick8(const ProductArgs& p, hipStream_t stream)
+{
+    constexpr bool exact = TYPE == kTE4m3Exact;
+    constexpr float never = 1e30f;
+    constexpr float large = exact || SM == kRowScale ? never : 1.75f;
+    if constexpr (EP == kEpStore) {
+        constexpr Tile tiles[] = {{128, 128, 512, exact ? 2.0f : 1.05f},
+                                  {128, 128, 256, exact ? 1.1f : .65f},
+                                  {64, 64, 512, exact ? .70f : .40f},
+                                  {64, 64, 256, exact ? .36f : .26f},
+                                  {256, 256, 256, large}};
+        switch (cheapest(tiles, p.m, p.n)) {
+        case 0:
+            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM>(p, stream);
+        case 1:
+            return run<TYPE, 128, 128, 2, 2, 2, 2, EP, SM>(p, stream);
+        case 2:
+            return run<TYPE, 64, 64, 2, 2, 2, 2, EP, SM>(p, stream);
+        case 3:
+            // (fp32 results: four groups of waves 10-15 % faster than two
+            // with four rounds in LDS; 16-bit results 5-10 % slower)
+            return run<TYPE, 64, 64, 2, 2, exact ? 4 : 2, exact ? 2 : 4, EP, SM>(p, stream);
+        }
+    } else {
+        constexpr Tile tiles[] = {{128, 64, 512, exact ? 2.0f : 1.05f},
+                                  {128, 64, 256, exact ? 1.1f : .65f},
+                                  {64, 64, 256, exact ? .60f : .40f},
+                                  {256, 128, 256, large}};
+        switch (cheapest(tiles, p.m, p.n)) {
+        case 0:
+            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM>(p, stream);
+        case 1:
+            return run<TYPE, 128, 128, 2, 2, 2, 2, EP, SM>(p, stream);
+        case 2:
+            return run<TYPE, 64, 128, 1, 4, 3, 2, EP, SM>(p, stream);
+        }
+    }
+    if constexpr (large != never)
+        return run<TYPE, 256, 256, 2, 4, 1, 2, EP, SM>(p, stream);
+    return hipErrorInvalidValue;
 }
 
 template <int TYPE>
-hipError_t pick16(const ProductArgs& p, int ep, hipStream_t stream)
+hipError_t launch16(const ProductArgs& p, int ep, hipStream_t stream)
 {
     if (ep == kEpGate)
-        return pick<TYPE, kEpGate, kNoScale>(p, stream);
+        return pick16<TYPE, kEpGate, false, false>(p, stream);
     if (ep == kEpGateGrad)
-        return pick<TYPE, kEpGateGrad, kNoScale>(p, stream);
-    return ep == kEpStoreT ? pick<TYPE, kEpStore, kNoScale, true, true>(p, stream)
-                           : pick<TYPE, kEpStore, kNoScale, false, true>(p, stream);
+        return pick16<TYPE, kEpGateGrad, false, false>(p, stream);
+    return ep == kEpStoreT ? pick16<TYPE, kEpStore, true, true>(p, stream)
+                           : pick16<TYPE, kEpStore, false, true>(p, stream);
+}
+
+template <int TYPE>
+hipError_t launch8(const ProductArgs& p, int ep, bool row_scales, hipStream_t stream)
+{
+    if (ep == kEpGate)
+        return pick8<TYPE, kEpGate, kTileScale>(p, stream);
+    return row_scales ? pick8<TYPE, kEpStore, kRowScale>(p, stream)
+                      : pick8<TYPE, kEpStore, kTileScale>(p, stream);
+}
+
+// Few rows: the strip kernel, except where 64-row tiles fill the CUs and their
+// shared rows of A pay: e4m3 n 16384 k 4096 takes 13.3 us with tiles and 18.0
+// with strips at m = 16 (12.5 and 13.1 at m = 1), n 4096 k 16384 33 and 19;
+// gated bf16 n 16384 k 4096 takes 53 and 66 us at m = 32, 52 and 51 at 16.
+bool strips(const ProductArgs& p, int type, int ep)
+{
+    if (p.m > kStripRows || ep == kEpGateGrad || (ep != kEpGate && type != kTE4m3))
+        return false;
+    const bool fills = (p.n + 63) / 64 >= 256;
+    return !fills || (ep == kEpGate && p.m <= 16);
 }
 
 }  // namespace
@@ -540,21 +665,12 @@ hipError_t pick16(const ProductArgs& p, int ep, hipStream_t stream)
 hipError_t launch_product(const ProductArgs& p, int type, int ep, bool row_scales,
                           hipStream_t stream)
 {
-    if (p.m <= kStripRows && (ep == kEpGate || type == kTE4m3))
+    if (strips(p, type, ep))
         return launch_strip(p, type, ep, row_scales, stream);
-    if (type == kTE4m3 && p.ctype == kTF32) {
-        if (ep == kEpGate)
-            return pick<kTE4m3Exact, kEpGate, kTileScale>(p, stream);
-        return row_scales ? pick<kTE4m3Exact, kEpStore, kRowScale>(p, stream)
-                          : pick<kTE4m3Exact, kEpStore, kTileScale>(p, stream);
-    }
-    if (type == kTE4m3) {
-        if (ep == kEpGate)
-            return pick<kTE4m3, kEpGate, kTileScale>(p, stream);
-        return row_scales ? pick<kTE4m3, kEpStore, kRowScale>(p, stream)
-                          : pick<kTE4m3, kEpStore, kTileScale>(p, stream);
-    }
-    return type == kTBf16 ? pick16<kTBf16>(p, ep, stream) : pick16<kTF16>(p, ep, stream);
+    if (type == kTE4m3)
+        return p.ctype == kTF32 ? launch8<kTE4m3Exact>(p, ep, row_scales, stream)
+                                : launch8<kTE4m3>(p, ep, row_scales, stream);
+    return type == kTBf16 ? launch16<kTBf16>(p, ep, stream) : launch16<kTF16>(p, ep, stream);
 }
 
 }  // namespace qse

@@ -1,4 +1,4 @@
-// Products of few rows: A B^T (and the gated block) for m up to 64.
+// Products of few rows: A B^T (and the gated block) for m up to 32.
 //
 // The rows of B are read once and bound the time, so a workgroup takes 16 of
 // them (16 of each projection) and all of A, its waves take the 128-byte
@@ -35,11 +35,10 @@ __device__ __forceinline__ v4i load16_tail(const char* p, int left)
     return v;
 }
 
-template <int TYPE, int MT, int W, int EP, int SM>
+template <int TYPE, int MT, int W, int U, int EP, int SM>
 __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
 {
     constexpr int P = EP == kEpStore ? 1 : 2;    // projections
-    constexpr int U = MT * P > 2 ? 2 : 4;        // steps in flight
     extern __shared__ __align__(16) unsigned char lds[];
     float* red = (float*)lds;                    // [W][P][MT][4][64]
     const int lane = threadIdx.x & 63;
@@ -71,30 +70,37 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
         for (int i = 0; i < MT; ++i)
             acc[j][i] = v4f{0.f, 0.f, 0.f, 0.f};
 
-    auto add = [&](const v4i (&b)[P][2], const v4i (&a)[MT][2], int64_t kt) {
-        float s[P][4], sa[MT];
+    // A step: both operands and their scales; all loads of the steps in flight
+    // are issued before the first is used.
+    struct Step {
+        v4i b[P][2], a[MT][2];
+        float sb[SM ? P : 1][SM == 2 ? 4 : 1], sa[SM ? MT : 1];
+    };
+    auto load_scales = [&](Step& t, int64_t kt) __attribute__((always_inline)) {
         if constexpr (SM != 0) {
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                sa[i] = p.sa[kt * p.m + mr[i]];
+                t.sa[i] = p.sa[kt * p.m + mr[i]];
 #pragma unroll
             for (int j = 0; j < P; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    s[j][r] = SM == 1 && r ? s[j][0]
-                                           : (j ? p.sb1 : p.sb0)[kt * p.sb_n + sbn[r]];
+                for (int r = 0; r < (SM == 2 ? 4 : 1); ++r)
+                    t.sb[j][r] = (j ? p.sb1 : p.sb0)[kt * p.sb_n + sbn[r]];
         }
+    };
+    auto add = [&](const Step& t) __attribute__((always_inline)) {
 #pragma unroll
         for (int j = 0; j < P; ++j)
 #pragma unroll
             for (int i = 0; i < MT; ++i) {
                 if constexpr (SM == 0) {
-                    acc[j][i] = matrix_step<TYPE>(b[j], a[i], acc[j][i]);
+                    acc[j][i] = matrix_step<TYPE>(t.b[j], t.a[i], acc[j][i]);
                 } else {
-                    const v4f t = matrix_step<TYPE>(b[j], a[i], v4f{0.f, 0.f, 0.f, 0.f});
+                    const v4f v = matrix_step<TYPE>(t.b[j], t.a[i], v4f{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
                     for (int r = 0; r < 4; ++r)
-                        acc[j][i][r] = __builtin_fmaf(t[r], sa[i] * s[j][r], acc[j][i][r]);
+                        acc[j][i][r] = __builtin_fmaf(v[r], t.sa[i] * t.sb[j][SM == 2 ? r : 0],
+                                                      acc[j][i][r]);
                 }
             }
     };
@@ -102,38 +108,40 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
     const int64_t full = p.kbytes / kStep;
     int64_t kt = wave;
     for (; kt + (U - 1) * W < full; kt += U * W) {
-        v4i b[U][P][2], a[U][MT][2];
+        Step t[U];
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
 #pragma unroll
             for (int j = 0; j < P; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    b[u][j][h] = load16(bp[j] + (kt + u * W) * kStep + h * 64);
-#pragma unroll
-        for (int u = 0; u < U; ++u)
+                    t[u].b[j][h] = load16(bp[j] + (kt + u * W) * kStep + h * 64);
+            load_scales(t[u], kt + u * W);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    a[u][i][h] = load16(ap[i] + (kt + u * W) * kStep + h * 64);
+                    t[u].a[i][h] = load16(ap[i] + (kt + u * W) * kStep + h * 64);
+        }
+        __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int u = 0; u < U; ++u)
-            add(b[u], a[u], kt + u * W);
+            add(t[u]);
     }
     for (; kt * kStep < p.kbytes; kt += W) {
-        v4i b[P][2], a[MT][2];
+        Step t;
         const int left = (int)(p.kbytes - kt * kStep < kStep ? p.kbytes - kt * kStep : kStep) - q * 16;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                b[j][h] = load16_tail(bp[j] + kt * kStep + h * 64, left - h * 64);
+                t.b[j][h] = load16_tail(bp[j] + kt * kStep + h * 64, left - h * 64);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                a[i][h] = load16_tail(ap[i] + kt * kStep + h * 64, left - h * 64);
+                t.a[i][h] = load16_tail(ap[i] + kt * kStep + h * 64, left - h * 64);
         }
-        add(b, a, kt);
+        load_scales(t, kt);
+        add(t);
     }
 
 #pragma unroll
@@ -174,26 +182,31 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
     }
 }
 
-template <int TYPE, int MT, int EP, int SM>
+template <int TYPE, int MT, int W, int U, int EP, int SM>
 hipError_t run(const ProductArgs& p, hipStream_t stream)
 {
-    constexpr int W = MT > 2 ? 8 : 16;
     constexpr int P = EP == kEpStore ? 1 : 2;
     constexpr size_t kLds = (size_t)W * P * MT * 4 * 64 * 4;
     static_assert(kLds <= 65536, "dynamic LDS without an attribute");
-    hipLaunchKernelGGL((strip_kernel<TYPE, MT, W, EP, SM>), dim3((unsigned)((p.n + 15) / 16)),
+    hipLaunchKernelGGL((strip_kernel<TYPE, MT, W, U, EP, SM>), dim3((unsigned)((p.n + 15) / 16)),
                        dim3(64 * W), kLds, stream, p);
     return hipGetLastError();
 }
 
+// Waves and steps in flight: sixteen waves pay for a long k alone (e4m3, m 1:
+// n 4096 k 16384 13.9 us, with eight waves 17.3; n 16384 k 4096, where eight
+// waves of four steps are all of k, 20.0 and 13.1), and only where their four
+// steps fit 128 registers.
 template <int TYPE, int EP, int SM>
 hipError_t pick(const ProductArgs& p, hipStream_t stream)
 {
-    if (p.m <= 16)
-        return run<TYPE, 1, EP, SM>(p, stream);
-    if (p.m <= 32)
-        return run<TYPE, 2, EP, SM>(p, stream);
-    return run<TYPE, 4, EP, SM>(p, stream);
+    if (p.m > 16)
+        return run<TYPE, 2, 8, 2, EP, SM>(p, stream);
+    if constexpr (EP == kEpStore && SM == 1 && TYPE == kTE4m3) {
+        if (p.kbytes >= 64 * kStep)
+            return run<TYPE, 1, 16, 4, EP, SM>(p, stream);
+    }
+    return run<TYPE, 1, 8, 4, EP, SM>(p, stream);
 }
 
 }  // namespace

@@ -30,11 +30,13 @@ FFN_SYMBOLS = ("fwt_rotate_quantize_workspace", "fwt_rotate_quantize", "fwt_scal
 _SCALES = {"row": 0, "tile": 1}
 _ACTS = {"silu": 0, "gelu": 1}
 _lib = None
-_types = None
+# of torch, set by _load
+_types = _f32 = _f8 = _floats = _halves = _gated = _raw_stream = _device = None
+_here = contextlib.nullcontext()
 
 
 def _load():
-    global _lib, _types
+    global _lib, _types, _f32, _f8, _floats, _halves, _gated, _raw_stream, _device
     if _lib is None:
         import torch
         lib = _qse.load_library()
@@ -53,63 +55,71 @@ def _load():
         for name in FFN_SYMBOLS:
             getattr(lib, name).restype = i32
         _types = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2, torch.float8_e4m3fn: 3}
+        _f32, _f8, _device = torch.float32, torch.float8_e4m3fn, torch.cuda.current_device
+        _halves = (torch.bfloat16, torch.float16)
+        _floats, _gated = _halves + (_f32,), _halves + (_f8,)
+        _raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: no Stream object
         _lib = lib
     return _lib
 
 
-def _matrix(t, name, dtypes=None):
-    """Checks a 2-d operand; returns its row stride in elements."""
-    import torch
-    if t.dim() != 2:
+def _matrix(t, name, dtypes, dev):
+    """Checks a 2-d operand; returns its rows, columns and row stride."""
+    if t.dtype not in dtypes:
+        raise ValueError("%s must be %s" % (name, " or ".join(str(d) for d in dtypes)))
+    if t.get_device() != dev:
+        raise ValueError("%s must be a tensor of the current device" % name)
+    shape, strides = t.shape, t.stride()
+    if len(shape) != 2:
         raise ValueError("%s must have two dimensions" % name)
-    if dtypes is not None and t.dtype not in dtypes:
-        raise ValueError("%s must be one of %s" % (name, ", ".join(str(d) for d in dtypes)))
-    if not t.is_cuda:
-        raise ValueError("%s must be a device tensor" % name)
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError("%s must be on the current device" % name)
-    rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    rows, cols = shape
+    if strides[1] != 1 and cols > 1:
         raise ValueError("the last dimension of %s must be contiguous" % name)
     if rows > 1:
-        ld = t.stride(0)
+        ld = strides[0]
         if ld < cols:
             raise ValueError("the rows of %s overlap" % name)
-        return ld
-    return -(-cols // 16) * 16
+        return rows, cols, ld
+    return rows, cols, -(-cols // 16) * 16
 
 
-def _scales_of(s, name, blocks, rows, kinds):
+def _scales_of(s, name, dev, blocks, rows, kinds):
     """Checks a scale array; returns its kind ("row" or "tile")."""
-    import torch
-    if s.dtype != torch.float32 or not s.is_contiguous() or s.dim() != 2:
+    if s.dtype is not _f32 or not s.is_contiguous():
         raise ValueError("%s must be a contiguous float32 matrix" % name)
-    if not s.is_cuda or s.device.index != torch.cuda.current_device():
-        raise ValueError("%s must be on the current device" % name)
-    shapes = {"row": (blocks, rows), "tile": (blocks, -(-rows // BLOCK))}
+    if s.get_device() != dev:
+        raise ValueError("%s must be a tensor of the current device" % name)
+    shape = tuple(s.shape)
     for kind in kinds:
-        if tuple(s.shape) == shapes[kind]:
+        if shape == (blocks, rows if kind == "row" else -(-rows // BLOCK)):
             return kind
-    raise ValueError("%s must have shape %s, not %s"
-                     % (name, " or ".join(str(shapes[k]) for k in kinds), tuple(s.shape)))
+    raise ValueError("%s must have shape %s, not %s" % (name, " or ".join(
+        str((blocks, rows if k == "row" else -(-rows // BLOCK))) for k in kinds), shape))
 
 
-def _on(stream):
+def _on(stream, dev):
     """(stream handle, a context in which torch allocates for that stream)."""
-    import torch
     if stream is None:
-        return ctypes.c_void_p(torch.cuda.current_stream().cuda_stream), contextlib.nullcontext()
-    return ctypes.c_void_p(stream.cuda_stream), torch.cuda.stream(stream)
-
-
-def _result(out, name, rows, cols, dtype, device):
-    """The output tensor and its row stride."""
+        return _raw_stream(dev), _here
     import torch
+    return stream.cuda_stream, torch.cuda.stream(stream)
+
+
+def _result(out, name, dev, rows, cols, dtype, like):
+    """The output tensor and its row stride."""
     if out is None:
-        return torch.empty((rows, cols), dtype=dtype, device=device), cols
-    if tuple(out.shape) != (rows, cols):
+        return like.new_empty((rows, cols), dtype=dtype), cols
+    r, c, ld = _matrix(out, name, (dtype,), dev)
+    if (r, c) != (rows, cols):
         raise ValueError("%s must have shape %s" % (name, (rows, cols)))
-    return out, _matrix(out, name, (dtype,))
+    return out, ld
+
+
+def _out_dtype(out_dtype, out):
+    dtype = out_dtype or (_floats[0] if out is None else out.dtype)
+    if dtype not in _floats:
+        raise ValueError("out_dtype must be bfloat16, float16 or float32")
+    return dtype
 
 
 def _raise(status, what):
@@ -123,12 +133,20 @@ def _act(act):
     return _ACTS[act]
 
 
-def _scratch(nbytes, device):
+def _scratch(nbytes, like):
     import torch
     if not nbytes:
         return None, None
-    ws = torch.empty(nbytes, dtype=torch.uint8, device=device)
-    return ws, ctypes.c_void_p(ws.data_ptr())
+    ws = like.new_empty(nbytes, dtype=torch.uint8)
+    return ws, ws.data_ptr()
+
+
+def _current():
+    """The current device, or the reason that there is none."""
+    try:
+        return _device()
+    except Exception as e:      # torch has no device to ask
+        raise ValueError("no current device: %s" % e)
 
 
 def rotate_quantize(x, bits=0, scales="row", transpose=False, stream=None):
@@ -141,26 +159,28 @@ def rotate_quantize(x, bits=0, scales="row", transpose=False, stream=None):
     float8_e4m3fn of shape (m, k), in rows padded with zeros to a multiple of
     16 bytes.  See fwt_rotate_quantize.
     """
-    import torch
-    lib = _load()
+    lib = _lib or _load()
     if scales not in _SCALES:
         raise ValueError("scales must be 'row' or 'tile'")
-    ld = _matrix(x, "x", (torch.bfloat16, torch.float16, torch.float32))
-    m, k = x.shape[::-1] if transpose else x.shape
+    dev = _current()
+    m, k, ld = _matrix(x, "x", _floats, dev)
+    if transpose:
+        m, k = k, m
     kind, bits, t = _SCALES[scales], int(bits), 1 if transpose else 0
-    need = ctypes.c_size_t(0)
+    need = 0
     if kind and bits > ROTATE_MAX_BITS_T:
-        _raise(lib.fwt_rotate_quantize_workspace(m, k, bits, kind, t, ctypes.byref(need)),
+        size = ctypes.c_size_t(0)
+        _raise(lib.fwt_rotate_quantize_workspace(m, k, bits, kind, t, ctypes.byref(size)),
                "fwt_rotate_quantize_workspace")
-    handle, where = _on(stream)
+        need = size.value
+    handle, where = _on(stream, dev)
     with where:
         ldq = -(-k // 16) * 16
-        codes = torch.empty((m, ldq), dtype=torch.float8_e4m3fn, device=x.device)
-        s = torch.empty((-(-k // BLOCK), -(-m // BLOCK) if kind else m), dtype=torch.float32,
-                        device=x.device)
-        ws, wp = _scratch(need.value, x.device)
+        codes = x.new_empty((m, ldq), dtype=_f8)
+        s = x.new_empty((-(-k // BLOCK), -(-m // BLOCK) if kind else m), dtype=_f32)
+        ws, wp = _scratch(need, x)
     _raise(lib.fwt_rotate_quantize(x.data_ptr(), _types[x.dtype], m, k, ld, t, bits, kind,
-                                   codes.data_ptr(), ldq, s.data_ptr(), wp, need.value, handle),
+                                   codes.data_ptr(), ldq, s.data_ptr(), wp, need, handle),
            "fwt_rotate_quantize")
     return (codes if ldq == k else codes[:, :k]), s
 
@@ -169,22 +189,19 @@ def scaled_matmul(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=Non
     """``a b^T`` of e4m3 codes: a (m, k) with row scales, b (n, k) with row
     or tile scales (told by their shape).  ``out_dtype``: bfloat16 (default),
     float16 or float32.  See fwt_scaled_matmul."""
-    import torch
-    lib = _load()
-    f8 = (torch.float8_e4m3fn,)
-    lda, ldb = _matrix(a, "a", f8), _matrix(b, "b", f8)
-    (m, k), (n, kb) = a.shape, b.shape
+    lib = _lib or _load()
+    dev = _current()
+    m, k, lda = _matrix(a, "a", (_f8,), dev)
+    n, kb, ldb = _matrix(b, "b", (_f8,), dev)
     if k != kb:
         raise ValueError("a and b must have the same number of columns")
     nblocks = -(-k // BLOCK)
-    _scales_of(a_scales, "a_scales", nblocks, m, ("row",))
-    kind = _scales_of(b_scales, "b_scales", nblocks, n, ("tile", "row"))
-    dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
-    if dtype not in _types or dtype is torch.float8_e4m3fn:
-        raise ValueError("out_dtype must be bfloat16, float16 or float32")
-    handle, where = _on(stream)
+    _scales_of(a_scales, "a_scales", dev, nblocks, m, ("row",))
+    kind = _scales_of(b_scales, "b_scales", dev, nblocks, n, ("tile", "row"))
+    dtype = _out_dtype(out_dtype, out)
+    handle, where = _on(stream, dev)
     with where:
-        c, ldc = _result(out, "out", m, n, dtype, a.device)
+        c, ldc = _result(out, "out", dev, m, n, dtype, a)
     _raise(lib.fwt_scaled_matmul(a.data_ptr(), lda, a_scales.data_ptr(), b.data_ptr(), ldb,
                                  b_scales.data_ptr(), _SCALES[kind], m, n, k, c.data_ptr(),
                                  _types[dtype], ldc, handle), "fwt_scaled_matmul")
@@ -200,39 +217,35 @@ def gated_ffn(x, gate, up, act="silu", x_scales=None, gate_scales=None, up_scale
     ``out_dtype`` (bfloat16 by default).  ``act``: "silu" or "gelu".  See
     fwt_gated_ffn.
     """
-    import torch
-    lib = _load()
-    kinds = (torch.bfloat16, torch.float16, torch.float8_e4m3fn)
-    ldx = _matrix(x, "x", kinds)
-    ldg, ldu = _matrix(gate, "gate", (x.dtype,)), _matrix(up, "up", (x.dtype,))
-    m, k = x.shape
-    n = gate.shape[0]
-    if gate.shape[1] != k or tuple(up.shape) != (n, k):
+    lib = _lib or _load()
+    dev = _current()
+    m, k, ldx = _matrix(x, "x", _gated, dev)
+    n, kg, ldg = _matrix(gate, "gate", (x.dtype,), dev)
+    nu, ku, ldu = _matrix(up, "up", (x.dtype,), dev)
+    if kg != k or ku != k or nu != n:
         raise ValueError("gate and up must have shape (n, %d)" % k)
     sp = (None, None, None)
-    if x.dtype is torch.float8_e4m3fn:
+    if x.dtype is _f8:
         if x_scales is None or gate_scales is None or up_scales is None:
             raise ValueError("e4m3 operands need x_scales, gate_scales and up_scales")
         nblocks = -(-k // BLOCK)
-        _scales_of(x_scales, "x_scales", nblocks, m, ("row",))
-        _scales_of(gate_scales, "gate_scales", nblocks, n, ("tile",))
-        _scales_of(up_scales, "up_scales", nblocks, n, ("tile",))
+        _scales_of(x_scales, "x_scales", dev, nblocks, m, ("row",))
+        _scales_of(gate_scales, "gate_scales", dev, nblocks, n, ("tile",))
+        _scales_of(up_scales, "up_scales", dev, nblocks, n, ("tile",))
         sp = (x_scales.data_ptr(), gate_scales.data_ptr(), up_scales.data_ptr())
-        dtype = out_dtype or (torch.bfloat16 if out is None else out.dtype)
+        dtype = _out_dtype(out_dtype, out)
     else:
         if x_scales is not None or gate_scales is not None or up_scales is not None:
             raise ValueError("scales belong to e4m3 operands")
         dtype = out_dtype or x.dtype
-        if dtype != x.dtype:
+        if dtype is not x.dtype:
             raise ValueError("the output has the operands' dtype")
-    if dtype not in _types or dtype is torch.float8_e4m3fn:
-        raise ValueError("out_dtype must be bfloat16, float16 or float32")
-    a = _act(act)
-    handle, where = _on(stream)
+    code = _act(act)
+    handle, where = _on(stream, dev)
     with where:
-        h, ldh = _result(out, "out", m, n, dtype, x.device)
+        h, ldh = _result(out, "out", dev, m, n, dtype, x)
     _raise(lib.fwt_gated_ffn(x.data_ptr(), ldx, sp[0], gate.data_ptr(), ldg, sp[1],
-                             up.data_ptr(), ldu, sp[2], _types[x.dtype], m, n, k, a,
+                             up.data_ptr(), ldu, sp[2], _types[x.dtype], m, n, k, code,
                              h.data_ptr(), _types[dtype], ldh, handle), "fwt_gated_ffn")
     return h
 
@@ -240,29 +253,28 @@ def gated_ffn(x, gate, up, act="silu", x_scales=None, gate_scales=None, up_scale
 def gated_ffn_backward(x, gate, up, grad, act="silu", stream=None):
     """Gradients (dx, dgate, dup) of ``gated_ffn`` on bf16 or f16 operands
     for ``grad``, that of its output (m, n).  See fwt_gated_ffn_backward."""
-    import torch
-    lib = _load()
-    ldx = _matrix(x, "x", (torch.bfloat16, torch.float16))
-    ldg, ldu = _matrix(gate, "gate", (x.dtype,)), _matrix(up, "up", (x.dtype,))
-    ldd = _matrix(grad, "grad", (x.dtype,))
-    m, k = x.shape
-    n = gate.shape[0]
-    if gate.shape[1] != k or tuple(up.shape) != (n, k):
+    lib = _lib or _load()
+    dev = _current()
+    m, k, ldx = _matrix(x, "x", _halves, dev)
+    n, kg, ldg = _matrix(gate, "gate", (x.dtype,), dev)
+    nu, ku, ldu = _matrix(up, "up", (x.dtype,), dev)
+    mg, ng, ldd = _matrix(grad, "grad", (x.dtype,), dev)
+    if kg != k or ku != k or nu != n:
         raise ValueError("gate and up must have shape (n, %d)" % k)
-    if tuple(grad.shape) != (m, n):
+    if (mg, ng) != (m, n):
         raise ValueError("grad must have shape %s" % ((m, n),))
-    a = _act(act)
-    need = ctypes.c_size_t(0)
-    _raise(lib.fwt_gated_ffn_backward_workspace(m, n, k, ctypes.byref(need)),
+    code = _act(act)
+    size = ctypes.c_size_t(0)
+    _raise(lib.fwt_gated_ffn_backward_workspace(m, n, k, ctypes.byref(size)),
            "fwt_gated_ffn_backward_workspace")
-    handle, where = _on(stream)
+    handle, where = _on(stream, dev)
     with where:
-        dx = torch.empty((m, k), dtype=x.dtype, device=x.device)
-        dgate = torch.empty((n, k), dtype=x.dtype, device=x.device)
-        dup = torch.empty((n, k), dtype=x.dtype, device=x.device)
-        ws, wp = _scratch(need.value, x.device)
+        dx = x.new_empty((m, k))
+        dgate = x.new_empty((n, k))
+        dup = x.new_empty((n, k))
+        ws, wp = _scratch(size.value, x)
     _raise(lib.fwt_gated_ffn_backward(x.data_ptr(), ldx, gate.data_ptr(), ldg, up.data_ptr(),
-                                      ldu, grad.data_ptr(), ldd, _types[x.dtype], m, n, k, a,
+                                      ldu, grad.data_ptr(), ldd, _types[x.dtype], m, n, k, code,
                                       dx.data_ptr(), k, dgate.data_ptr(), k, dup.data_ptr(), k,
-                                      wp, need.value, handle), "fwt_gated_ffn_backward")
+                                      wp, size.value, handle), "fwt_gated_ffn_backward")
     return dx, dgate, dup
