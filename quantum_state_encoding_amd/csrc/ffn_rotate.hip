@@ -60,17 +60,17 @@ __device__ __forceinline__ void load_elements(const void* x, int64_t at, int lef
 }
 
 // The stage on lane bit LB: (a, b) -> (a + b, a - b) over the pairs.
-template <int LB>
-__device__ __forceinline__ void lane_stage(float (&v)[16], int lane)
+template <int LB, int N>
+__device__ __forceinline__ void lane_stage(float (&v)[N], int lane)
 {
     if constexpr (LB < 4) {
         const float s = (lane >> LB) & 1 ? -1.0f : 1.0f;
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
+        for (int i = 0; i < N; ++i)
             v[i] = fma_sign(v[i], s, lane_partner<LB>(v[i]));
     } else {
 #pragma unroll
-        for (int i = 0; i < 16; i += 2) {
+        for (int i = 0; i < N; i += 2) {
             permlane_swap<LB>(v[i], v[i + 1]);
             butterfly(v[i], v[i + 1]);
             permlane_swap<LB>(v[i], v[i + 1]);
@@ -103,13 +103,15 @@ __device__ __forceinline__ void wave_stages(float (&v)[16], int bits, int lane)
         lane_stage<5>(v, lane);
 }
 
-// Largest magnitude of the block's 128 values, as bits: as unsigned numbers
-// they order like the magnitudes, with infinity and then NaN on top.
-__device__ __forceinline__ unsigned block_max(const float (&v)[16])
+// Largest magnitude of the block's 128 values (16 on each of 8 lanes, or 32
+// on each of 4), as bits: as unsigned numbers they order like the magnitudes,
+// with infinity and then NaN on top.
+template <int N>
+__device__ __forceinline__ unsigned block_max(const float (&v)[N])
 {
     unsigned m = 0;
 #pragma unroll
-    for (int i = 0; i < 16; ++i) {
+    for (int i = 0; i < N; ++i) {
         const unsigned u = __float_as_uint(v[i]) & 0x7fffffffu;
         m = m > u ? m : u;
     }
@@ -117,8 +119,11 @@ __device__ __forceinline__ unsigned block_max(const float (&v)[16])
     m = m > o ? m : o;
     o = lane_partner_u32<1>(m);
     m = m > o ? m : o;
-    o = lane_partner_u32<2>(m);
-    return m > o ? m : o;
+    if constexpr (N == 16) {
+        o = lane_partner_u32<2>(m);
+        m = m > o ? m : o;
+    }
+    return m;
 }
 
 __device__ __forceinline__ float scale_of(unsigned maxbits)
@@ -129,12 +134,11 @@ __device__ __forceinline__ float scale_of(unsigned maxbits)
     return s > 0x1p-126f ? s : 0x1p-126f;
 }
 
-// e4m3 codes of v / s: the quotient is refined once, so that it rounds as
-// the division does (a code is a few bits; ties between two codes are
-// common where the inputs have few bits too).
-__device__ __forceinline__ v4i encode(const float (&v)[16], float s)
+// e4m3 codes of v[0 .. 15] / s: the quotient is refined once, so that it
+// rounds as the division does (a code is a few bits; ties between two codes
+// are common where the inputs have few bits too).
+__device__ __forceinline__ v4i encode(const float* v, float s, float inv)
 {
-    const float inv = 1.0f / s;
     v4i out;
 #pragma unroll
     for (int w = 0; w < 4; ++w) {
@@ -151,19 +155,28 @@ __device__ __forceinline__ v4i encode(const float (&v)[16], float s)
     return out;
 }
 
-// What follows a rotation: maximum, scale and codes of block kb of a row.
-template <int MODE>
-__device__ __forceinline__ void finish(const RotateArgs& p, float (&v)[16], int64_t row, int64_t kb,
-                                       int lane, bool live)
+// What follows a rotation, whose factor `norm` (exact: a power of two) is
+// still to come: maximum, scale and codes of block kb of a row.  `part` of the
+// block's 128 / N lanes has N of its elements.  A power of two moves into the
+// scale, where it changes no rounding (subnormal results apart, which the
+// smallest scale rounds to 0 codes either way).
+template <int MODE, int N>
+__device__ __forceinline__ void finish(const RotateArgs& p, float (&v)[N], float norm, bool exact,
+                                       int64_t row, int64_t kb, int part, bool live)
 {
-    const int l8 = lane & 7;
+    if (!exact) {
+#pragma unroll
+        for (int i = 0; i < N; ++i)
+            v[i] *= norm;
+        norm = 1.0f;
+    }
     float s;
     if constexpr (MODE == kTileGiven) {
         s = live ? p.s[kb * ((p.m + kFfnBlock - 1) / kFfnBlock) + row / kFfnBlock] : 1.0f;
     } else {
-        const unsigned top = block_max(v);
+        const unsigned top = __float_as_uint(__uint_as_float(block_max(v)) * norm);
         s = scale_of(top);
-        if (live && l8 == 0) {
+        if (live && part == 0) {
             if constexpr (MODE == kMaxima)
                 p.amax[kb * p.m + row] = __uint_as_float(top);
             else
@@ -172,9 +185,14 @@ __device__ __forceinline__ void finish(const RotateArgs& p, float (&v)[16], int6
         if constexpr (MODE == kMaxima)
             return;
     }
-    const v4i c = encode(v, s);
-    if (live && kb * kFfnBlock + l8 * 16 < p.k)
-        *(v4i*)(p.q + row * p.ldq + kb * kFfnBlock + l8 * 16) = c;
+    const float sv = s / norm;
+    const float inv = 1.0f / sv;
+#pragma unroll
+    for (int h = 0; h < N; h += 16) {
+        const v4i c = encode(v + h, sv, inv);
+        if (live && kb * kFfnBlock + part * N + h < p.k)
+            *(v4i*)(p.q + row * p.ldq + kb * kFfnBlock + part * N + h) = c;
+    }
 }
 
 // Rotations of at most 2^10: the blocks of all rows one after another, 8 to a
@@ -192,66 +210,112 @@ __global__ __launch_bounds__(256) void rows_kernel(const RotateArgs p, float nor
     float v[16];
     load_elements<TYPE>(p.x, row * p.ldx + k0, left, v);
     wave_stages(v, p.bits, lane);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] *= norm;
-    finish<MODE>(p, v, row, kb, lane, live);
+    finish<MODE>(p, v, norm, !(p.bits & 1), row, kb, lane & 7, live);
 }
 
-// Rotations of 2^11 to 2^14: a workgroup of 2^(b - 10) waves for each.  The
-// waves' bits are register stages on a second layout, through LDS and back.
-template <int TYPE, int MODE, int WB>
-__global__ __launch_bounds__(64 << WB) void long_kernel(const RotateArgs p, float norm)
+// Rotations of 2^11 to 2^14: a workgroup of 2^b / 32 threads for each, all
+// stages on 32 registers a thread, in three layouts with LDS between them:
+//   A  bits 10 .. b-1 and 0 .. 14-b: 2^(15-b) neighbours of every 1024
+//   B  bits 5 .. 9: every 32nd of a 1024
+//   C  bits 15-b .. 4: 32 neighbours, a quarter of a block
+// (A lane stage costs two instructions an element, a register stage one, and
+// the vector instructions are what comes closest to the memory's time: about
+// 20 an element, 68 us of the 78 that 8192 x 16384 bf16 take from memory.)
+//
+// Where element i stands in LDS: the 16-byte accesses of C (16 lanes, 32
+// elements apart) and the 4-byte ones of B (two runs of 32) take all banks.
+__device__ __forceinline__ int place(int i)
 {
-    constexpr int kLow = 16 >> WB;      // neighbours a thread takes with the waves' bits
-    __shared__ __align__(16) float lds[(1024 << WB) / 16 * 20];
-    const int t = threadIdx.x, lane = t & 63;
-    const int64_t per = p.k >> (10 + WB);
-    const int64_t row = blockIdx.x / per;
-    const int64_t k0 = (blockIdx.x - row * per) * (1024 << WB) + t * 16;
-    float v[16];
-    load_elements<TYPE>(p.x, row * p.ldx + k0, 16, v);
-    wave_stages(v, 10, lane);
-    // 16 floats and 4 of padding: 16 lanes' 16-byte accesses take all banks
+    return i ^ (((i >> 6) & 7) << 2) ^ (((i >> 10) & 1) << 5);
+}
+
+// Stages on register bits [LO, HI) of 32 values.
+template <int LO, int HI>
+__device__ __forceinline__ void stages32(float (&v)[32])
+{
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        *(v4f*)(lds + t * 20 + 4 * i) = v4f{v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]};
+    for (int b = LO; b < HI; ++b)
+#pragma unroll
+        for (int i = 0; i < 32; ++i)
+            if (!(i & (1 << b)))
+                butterfly(v[i], v[i | (1 << b)]);
+}
+
+template <int TYPE, int MODE, int BITS>
+__global__ __launch_bounds__(1 << (BITS - 5)) void long_kernel(const RotateArgs p, float norm)
+{
+    constexpr int kNear = 1 << (15 - BITS);     // neighbours of layout A
+    constexpr int kSegs = 1 << (BITS - 10);
+    __shared__ __align__(16) float lds[1 << BITS];
+    const int t = threadIdx.x;
+    const int64_t per = p.k >> BITS;
+    // Rotations of the 32 rows whose scales share a line of memory run on one
+    // XCD (workgroup w on XCD w mod 8), whose L2 gathers them.
+    int64_t w = blockIdx.x;
+    const int64_t group = 256 * per;
+    if (w < p.m * per / group * group) {
+        const int64_t r = w % group;
+        w += (r & 7) * (32 * per) + (r >> 3) - r;
+    }
+    const int64_t row = w / per;
+    const int64_t k0 = (w - row * per) << BITS;
+    const int64_t x0 = row * p.ldx + k0 + t * kNear;
+    float v[32];
+    // kNear elements at one address
+    using Word = typename std::conditional<TYPE == kTF32, float, unsigned short>::type;
+    struct __attribute__((packed)) Near {
+        Word w[kNear];
+    };
+#pragma unroll
+    for (int g = 0; g < kSegs; ++g) {
+        const Near n = *(const Near*)((const Word*)p.x + x0 + g * 1024);
+#pragma unroll
+        for (int i = 0; i < kNear; ++i) {
+            if constexpr (TYPE == kTF32)
+                v[g * kNear + i] = n.w[i];
+            else
+                v[g * kNear + i] = from16(n.w[i], TYPE == kTBf16);
+        }
+    }
+    stages32<0, 5>(v);
+#pragma unroll
+    for (int g = 0; g < kSegs; ++g)
+#pragma unroll
+        for (int i = 0; i < kNear; i += 2) {
+            typedef float v2f __attribute__((ext_vector_type(2)));
+            *(v2f*)(lds + place(g * 1024 + t * kNear + i)) =
+                v2f{v[g * kNear + i], v[g * kNear + i + 1]};
+        }
     __syncthreads();
-    float u[1 << WB][kLow];
-    const int low = t * kLow;
+    const int b0 = (t >> 5) * 1024 + (t & 31);
 #pragma unroll
-    for (int w = 0; w < (1 << WB); ++w)
+    for (int i = 0; i < 32; ++i)
+        v[i] = lds[place(b0 + i * 32)];
+    stages32<0, 5>(v);
 #pragma unroll
-        for (int i = 0; i < kLow; ++i)
-            u[w][i] = lds[(w * 64 + (low + i) / 16) * 20 + (low + i) % 16];
-#pragma unroll
-    for (int b = 0; b < WB; ++b)
-#pragma unroll
-        for (int w = 0; w < (1 << WB); ++w)
-            if (!(w & (1 << b)))
-#pragma unroll
-                for (int i = 0; i < kLow; ++i)
-                    butterfly(u[w][i], u[w | (1 << b)][i]);
-#pragma unroll
-    for (int w = 0; w < (1 << WB); ++w)
-#pragma unroll
-        for (int i = 0; i < kLow; ++i)
-            lds[(w * 64 + (low + i) / 16) * 20 + (low + i) % 16] = u[w][i];
+    for (int i = 0; i < 32; ++i)
+        lds[place(b0 + i * 32)] = v[i];
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] = lds[t * 20 + i] * norm;
-    finish<MODE>(p, v, row, k0 / kFfnBlock, lane, true);
+    for (int i = 0; i < 32; i += 4) {
+        const v4f c = *(const v4f*)(lds + place(t * 32 + i));
+        v[i] = c[0];
+        v[i + 1] = c[1];
+        v[i + 2] = c[2];
+        v[i + 3] = c[3];
+    }
+    stages32<15 - BITS, 5>(v);
+    finish<MODE>(p, v, norm, !(BITS & 1), row, k0 / kFfnBlock + (t >> 2), t & 3, true);
 }
 
 // Rotations of at most 2^7 on a 128 x 128 tile: tile scales, or a transposed
-// input (k x m), which crosses LDS on its way in.
+// fp32 input (k x m), which crosses LDS on its way in.
 template <int TYPE, bool TILE, bool TRANS>
 __global__ __launch_bounds__(1024) void tile_kernel(const RotateArgs p, float norm)
 {
-    constexpr int kPad = 128 + (TYPE == kTF32 ? 1 : 2);
-    using Word = typename std::conditional<TYPE == kTF32, float, unsigned short>::type;
-    __shared__ Word in[TRANS ? 128 * kPad : 1];
+    constexpr int kPad = 129;
+    static_assert(!TRANS || TYPE == kTF32, "tile_t16_kernel");
+    __shared__ float in[TRANS ? 128 * kPad : 1];
     __shared__ unsigned top[16];
     const int t = threadIdx.x, lane = t & 63;
     const int64_t kb = blockIdx.x, mb = blockIdx.y;
@@ -265,23 +329,23 @@ __global__ __launch_bounds__(1024) void tile_kernel(const RotateArgs p, float no
         for (int i = 0; i < 16; ++i) {
             const int64_t k = kb * 128 + i * 8 + (t >> 7);
             in[(i * 8 + (t >> 7)) * kPad + (t & 127)] =
-                m < p.m && k < p.k ? ((const Word*)p.x)[k * p.ldx + m] : (Word)0;
+                m < p.m && k < p.k ? ((const float*)p.x)[k * p.ldx + m] : 0.0f;
         }
         __syncthreads();
 #pragma unroll
         for (int i = 0; i < 16; ++i)
-            v[i] = element<TYPE>(in, ((lane & 7) * 16 + i) * kPad + (t >> 3));
+            v[i] = in[((lane & 7) * 16 + i) * kPad + (t >> 3)];
     } else {
         const int left = live ? (int)(p.k - k0 < 16 ? p.k - k0 : 16) : 0;
         load_elements<TYPE>(p.x, row * p.ldx + k0, left, v);
     }
     wave_stages(v, p.bits, lane);
-#pragma unroll
-    for (int i = 0; i < 16; ++i)
-        v[i] *= norm;
     if constexpr (!TILE) {
-        finish<kRowScales>(p, v, row, kb, lane, live);
+        finish<kRowScales>(p, v, norm, !(p.bits & 1), row, kb, lane & 7, live);
     } else {
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            v[i] *= norm;
         unsigned m = block_max(v);
 #pragma unroll
         for (int d = 8; d < 64; d *= 2) {
@@ -297,9 +361,128 @@ __global__ __launch_bounds__(1024) void tile_kernel(const RotateArgs p, float no
         const float s = scale_of(m);
         if (t == 0)
             p.s[kb * ((p.m + kFfnBlock - 1) / kFfnBlock) + mb] = s;
-        const v4i c = encode(v, s);
+        const v4i c = encode(v, s, 1.0f / s);
         if (live && k0 < p.k)
             *(v4i*)(p.q + row * p.ldq + k0) = c;
+    }
+}
+
+// The same for a transposed input of 16-bit elements: 128 k of 128 rows, in
+// 16-byte loads along the rows, stand in LDS as they come, and the transposing
+// read gives a lane four k of its row.  16 lanes take a row each, four lanes
+// (16 apart) 32 k each: bits 0-4 are register stages, 5 and 6 cross the lanes.
+template <int TYPE, bool TILE>
+__global__ __launch_bounds__(256) void tile_t16_kernel(const RotateArgs p, float norm)
+{
+    typedef short v4s __attribute__((ext_vector_type(4)));
+    __shared__ __align__(16) unsigned char in[128 * 256];
+    __shared__ unsigned top[4];
+    const int t = threadIdx.x, lane = t & 63, wave = t >> 6, q = lane >> 4, l16 = lane & 15;
+    const int64_t kb = blockIdx.x, mb = blockIdx.y;
+    // 32-byte units of a k row are spread over the banks by k: a read takes
+    // four k rows at once, and those of k and k + 32
+    const auto mask = [](int k) { return (k & 3) | ((k >> 5) & 1) << 2; };
+    v4i c[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int kr = i * 16 + (t >> 4), ch = t & 15;
+        const int64_t k = kb * 128 + kr, m = mb * 128 + ch * 8;
+        const unsigned short* src = (const unsigned short*)p.x + k * p.ldx + m;
+        c[i] = v4i{0, 0, 0, 0};
+        if (k < p.k && m + 8 <= p.m) {
+            struct __attribute__((packed)) Any {
+                v4i v;
+            };
+            c[i] = ((const Any*)src)->v;
+        } else if (k < p.k) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (m + e < p.m)
+                    c[i][e >> 1] |= (int)((unsigned)src[e] << (16 * (e & 1)));
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int kr = i * 16 + (t >> 4), ch = t & 15;
+        *(v4i*)(in + kr * 256 + ((ch >> 1) ^ mask(kr)) * 32 + (ch & 1) * 16) = c[i];
+    }
+    __syncthreads();
+    float v[2][32];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const unsigned char* at = in + (q * 32 + (l16 >> 2)) * 256 +
+                                  ((wave + 4 * h) ^ mask(q * 32 + (l16 >> 2))) * 32 + (l16 & 3) * 8;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const v4s r = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                (__attribute__((address_space(3))) v4s*)(at + e * 4 * 256));
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                v[h][e * 4 + i] = from16((unsigned short)r[i], TYPE == kTBf16);
+        }
+    }
+    unsigned most = 0;
+    float s[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+#pragma unroll
+        for (int b = 0; b < 5; ++b)
+            if (b < p.bits)
+#pragma unroll
+                for (int i = 0; i < 32; ++i)
+                    if (!(i & (1 << b)))
+                        butterfly(v[h][i], v[h][i | (1 << b)]);
+        if (p.bits > 5)
+            lane_stage<4>(v[h], lane);
+        if (p.bits > 6)
+            lane_stage<5>(v[h], lane);
+        unsigned m = 0;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+            v[h][i] *= norm;
+            const unsigned u = __float_as_uint(v[h][i]) & 0x7fffffffu;
+            m = m > u ? m : u;
+        }
+#pragma unroll
+        for (int d = 16; d < 64; d *= 2) {
+            const unsigned o = (unsigned)__shfl_xor((int)m, d);
+            m = m > o ? m : o;
+        }
+        if constexpr (TILE) {
+#pragma unroll
+            for (int d = 1; d < 16; d *= 2) {
+                const unsigned o = (unsigned)__shfl_xor((int)m, d);
+                m = m > o ? m : o;
+            }
+            most = most > m ? most : m;
+        } else {
+            s[h] = scale_of(m);
+        }
+    }
+    if constexpr (TILE) {
+        if (lane == 0)
+            top[wave] = most;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            most = most > top[w] ? most : top[w];
+        s[0] = s[1] = scale_of(most);
+        if (t == 0)
+            p.s[kb * ((p.m + kFfnBlock - 1) / kFfnBlock) + mb] = s[0];
+    }
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+        const int64_t row = mb * 128 + (wave + 4 * h) * 16 + l16;
+        const float inv = 1.0f / s[h];
+        if (!TILE && q == 0 && row < p.m)
+            p.s[kb * p.m + row] = s[h];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int64_t k = kb * 128 + q * 32 + e * 16;
+            const v4i code = encode(v[h] + e * 16, s[h], inv);
+            if (row < p.m && k < p.k)
+                *(v4i*)(p.q + row * p.ldq + k) = code;
+        }
     }
 }
 
@@ -332,19 +515,19 @@ hipError_t rows(const RotateArgs& p, float norm, hipStream_t stream)
                            dim3(256), 0, stream, p, norm);
     } else {
         const dim3 grid((unsigned)(p.m * (p.k >> p.bits)));
-        const dim3 block(64u << (p.bits - 10));
+        const dim3 block(1u << (p.bits - 5));
         switch (p.bits) {
         case 11:
-            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 1>), grid, block, 0, stream, p, norm);
+            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 11>), grid, block, 0, stream, p, norm);
             break;
         case 12:
-            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 2>), grid, block, 0, stream, p, norm);
+            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 12>), grid, block, 0, stream, p, norm);
             break;
         case 13:
-            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 3>), grid, block, 0, stream, p, norm);
+            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 13>), grid, block, 0, stream, p, norm);
             break;
         default:
-            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 4>), grid, block, 0, stream, p, norm);
+            hipLaunchKernelGGL((long_kernel<TYPE, MODE, 14>), grid, block, 0, stream, p, norm);
         }
     }
     return hipGetLastError();
@@ -356,7 +539,15 @@ hipError_t rotate(const RotateArgs& p, bool tile, bool transpose, hipStream_t st
     const float norm = p.bits & 1 ? (float)(0.70710678118654752440 / (1 << (p.bits / 2)))
                                   : 1.0f / (float)(1 << (p.bits / 2));
     const dim3 tiles((unsigned)((p.k + 127) / 128), (unsigned)((p.m + 127) / 128));
-    if (transpose) {
+    if constexpr (TYPE != kTF32) {
+        if (transpose) {
+            if (tile)
+                hipLaunchKernelGGL((tile_t16_kernel<TYPE, true>), tiles, dim3(256), 0, stream, p, norm);
+            else
+                hipLaunchKernelGGL((tile_t16_kernel<TYPE, false>), tiles, dim3(256), 0, stream, p, norm);
+            return hipGetLastError();
+        }
+    } else if (transpose) {
         if (tile)
             hipLaunchKernelGGL((tile_kernel<TYPE, true, true>), tiles, dim3(1024), 0, stream, p, norm);
         else
