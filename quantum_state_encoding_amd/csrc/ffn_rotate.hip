@@ -222,13 +222,10 @@ __global__ __launch_bounds__(256) void rows_kernel(const RotateArgs p, float nor
 // the vector instructions are what comes closest to the memory's time: about
 // 20 an element, 68 us of the 78 that 8192 x 16384 bf16 take from memory.)
 //
-// Where element i stands in LDS: the 16-byte accesses of C (16 lanes, 32
-// elements apart) and the 4-byte ones of B (two runs of 32) take all banks.
-__device__ __forceinline__ int place(int i)
-{
-    return i ^ (((i >> 6) & 7) << 2) ^ (((i >> 10) & 1) << 5);
-}
-
+// Element i stands in LDS at i ^ (bits 6-8 of i at 2-4) ^ (bit 10 at 5): so
+// the 16-byte accesses of C (16 lanes, 32 elements apart) and the 4-byte ones
+// of B (two runs of 32) take all banks.  Each layout's addresses are a few
+// lane values and constants that are added.
 // Stages on register bits [LO, HI) of 32 values.
 template <int LO, int HI>
 __device__ __forceinline__ void stages32(float (&v)[32])
@@ -278,27 +275,36 @@ __global__ __launch_bounds__(1 << (BITS - 5)) void long_kernel(const RotateArgs 
         }
     }
     stages32<0, 5>(v);
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    const int a0 = t * kNear, am = ((a0 >> 6) & 7) << 2;
 #pragma unroll
-    for (int g = 0; g < kSegs; ++g)
+    for (int i = 0; i < kNear; i += 2) {
+        float* const even = lds + ((a0 + i) ^ am);
+        float* const odd = lds + ((a0 + i) ^ am ^ 32);
 #pragma unroll
-        for (int i = 0; i < kNear; i += 2) {
-            typedef float v2f __attribute__((ext_vector_type(2)));
-            *(v2f*)(lds + place(g * 1024 + t * kNear + i)) =
-                v2f{v[g * kNear + i], v[g * kNear + i + 1]};
-        }
+        for (int g = 0; g < kSegs; ++g)
+            *(v2f*)((g & 1 ? odd : even) + g * 1024) = v2f{v[g * kNear + i], v[g * kNear + i + 1]};
+    }
     __syncthreads();
-    const int b0 = (t >> 5) * 1024 + (t & 31);
+    // i = bit 5 (e), bits 6-8 (j), bit 9 (h): where bits 2-5 come out
+    const int b0 = (t >> 5) * 1024 + ((t & 31) ^ (t & 32));
+    float* at[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        at[j] = lds + (b0 ^ ((j >> 1) << 2) ^ ((j & 1) << 5)) + (j >> 1) * 64;
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        v[i] = lds[place(b0 + i * 32)];
+        v[i] = at[i & 15][(i >> 4) * 512];
     stages32<0, 5>(v);
 #pragma unroll
     for (int i = 0; i < 32; ++i)
-        lds[place(b0 + i * 32)] = v[i];
+        at[i & 15][(i >> 4) * 512] = v[i];
     __syncthreads();
+    const float* const c0 = lds + ((t * 32) ^ (t & 32));
+    const int cm = ((t >> 1) & 7) << 2;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
-        const v4f c = *(const v4f*)(lds + place(t * 32 + i));
+        const v4f c = *(const v4f*)(c0 + (i ^ cm));
         v[i] = c[0];
         v[i + 1] = c[1];
         v[i + 2] = c[2];
@@ -407,9 +413,9 @@ __global__ __launch_bounds__(256) void tile_t16_kernel(const RotateArgs p, float
         *(v4i*)(in + kr * 256 + ((ch >> 1) ^ mask(kr)) * 32 + (ch & 1) * 16) = c[i];
     }
     __syncthreads();
-    float v[2][32];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+    // Sixteen rows: 32 rotated elements a lane, and their largest magnitude
+    // over the row's four lanes.
+    auto rotated = [&](int h, float (&v)[32]) __attribute__((always_inline)) {
         const unsigned char* at = in + (q * 32 + (l16 >> 2)) * 256 +
                                   ((wave + 4 * h) ^ mask(q * 32 + (l16 >> 2))) * 32 + (l16 & 3) * 8;
 #pragma unroll
@@ -418,29 +424,24 @@ __global__ __launch_bounds__(256) void tile_t16_kernel(const RotateArgs p, float
                 (__attribute__((address_space(3))) v4s*)(at + e * 4 * 256));
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                v[h][e * 4 + i] = from16((unsigned short)r[i], TYPE == kTBf16);
+                v[e * 4 + i] = from16((unsigned short)r[i], TYPE == kTBf16);
         }
-    }
-    unsigned most = 0;
-    float s[2];
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
 #pragma unroll
         for (int b = 0; b < 5; ++b)
             if (b < p.bits)
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
                     if (!(i & (1 << b)))
-                        butterfly(v[h][i], v[h][i | (1 << b)]);
+                        butterfly(v[i], v[i | (1 << b)]);
         if (p.bits > 5)
-            lane_stage<4>(v[h], lane);
+            lane_stage<4>(v, lane);
         if (p.bits > 6)
-            lane_stage<5>(v[h], lane);
+            lane_stage<5>(v, lane);
         unsigned m = 0;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
-            v[h][i] *= norm;
-            const unsigned u = __float_as_uint(v[h][i]) & 0x7fffffffu;
+            v[i] *= norm;
+            const unsigned u = __float_as_uint(v[i]) & 0x7fffffffu;
             m = m > u ? m : u;
         }
 #pragma unroll
@@ -448,41 +449,49 @@ __global__ __launch_bounds__(256) void tile_t16_kernel(const RotateArgs p, float
             const unsigned o = (unsigned)__shfl_xor((int)m, d);
             m = m > o ? m : o;
         }
-        if constexpr (TILE) {
-#pragma unroll
-            for (int d = 1; d < 16; d *= 2) {
-                const unsigned o = (unsigned)__shfl_xor((int)m, d);
-                m = m > o ? m : o;
-            }
-            most = most > m ? most : m;
-        } else {
-            s[h] = scale_of(m);
-        }
-    }
-    if constexpr (TILE) {
-        if (lane == 0)
-            top[wave] = most;
-        __syncthreads();
-#pragma unroll
-        for (int w = 0; w < 4; ++w)
-            most = most > top[w] ? most : top[w];
-        s[0] = s[1] = scale_of(most);
-        if (t == 0)
-            p.s[kb * ((p.m + kFfnBlock - 1) / kFfnBlock) + mb] = s[0];
-    }
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
+        return m;
+    };
+    auto write = [&](int h, const float (&v)[32], float s) __attribute__((always_inline)) {
         const int64_t row = mb * 128 + (wave + 4 * h) * 16 + l16;
-        const float inv = 1.0f / s[h];
+        const float inv = 1.0f / s;
         if (!TILE && q == 0 && row < p.m)
-            p.s[kb * p.m + row] = s[h];
+            p.s[kb * p.m + row] = s;
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
             const int64_t k = kb * 128 + q * 32 + e * 16;
-            const v4i code = encode(v[h] + e * 16, s[h], inv);
+            const v4i code = encode(v + e * 16, s, inv);
             if (row < p.m && k < p.k)
                 *(v4i*)(p.q + row * p.ldq + k) = code;
         }
+    };
+    if constexpr (!TILE) {
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            float v[32];
+            const unsigned m = rotated(h, v);
+            write(h, v, scale_of(m));
+        }
+    } else {
+        float v[2][32];
+        unsigned m = rotated(0, v[0]);
+        const unsigned m1 = rotated(1, v[1]);
+        m = m > m1 ? m : m1;
+#pragma unroll
+        for (int d = 1; d < 16; d *= 2) {
+            const unsigned o = (unsigned)__shfl_xor((int)m, d);
+            m = m > o ? m : o;
+        }
+        if (lane == 0)
+            top[wave] = m;
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < 4; ++w)
+            m = m > top[w] ? m : top[w];
+        const float s = scale_of(m);
+        if (t == 0)
+            p.s[kb * ((p.m + kFfnBlock - 1) / kFfnBlock) + mb] = s;
+        write(0, v[0], s);
+        write(1, v[1], s);
     }
 }
 
