@@ -377,8 +377,9 @@ __global__ __launch_bounds__(1024) void tile_kernel(const RotateArgs p, float no
 // 16-byte loads along the rows, stand in LDS as they come, and the transposing
 // read gives a lane four k of its row.  16 lanes take a row each, four lanes
 // (16 apart) 32 k each: bits 0-4 are register stages, 5 and 6 cross the lanes.
-template <int TYPE, bool TILE>
-__global__ __launch_bounds__(256) void tile_t16_kernel(const RotateArgs p, float norm)
+template <int TYPE, bool TILE, int BITS>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(4))) void
+tile_t16_kernel(const RotateArgs p, float norm)
 {
     typedef short v4s __attribute__((ext_vector_type(4)));
     __shared__ __align__(16) unsigned char in[128 * 256];
@@ -388,23 +389,31 @@ __global__ __launch_bounds__(256) void tile_t16_kernel(const RotateArgs p, float
     // 32-byte units of a k row are spread over the banks by k: a read takes
     // four k rows at once, and those of k and k + 32
     const auto mask = [](int k) { return (k & 3) | ((k >> 5) & 1) << 2; };
+    struct __attribute__((packed)) Any {
+        v4i v;
+    };
+    const unsigned short* src =
+        (const unsigned short*)p.x + (kb * 128 + (t >> 4)) * p.ldx + mb * 128 + (t & 15) * 8;
     v4i c[8];
+    if (kb * 128 + 128 <= p.k && mb * 128 + 128 <= p.m) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int kr = i * 16 + (t >> 4), ch = t & 15;
-        const int64_t k = kb * 128 + kr, m = mb * 128 + ch * 8;
-        const unsigned short* src = (const unsigned short*)p.x + k * p.ldx + m;
-        c[i] = v4i{0, 0, 0, 0};
-        if (k < p.k && m + 8 <= p.m) {
-            struct __attribute__((packed)) Any {
-                v4i v;
-            };
-            c[i] = ((const Any*)src)->v;
-        } else if (k < p.k) {
+        for (int i = 0; i < 8; ++i)
+            c[i] = ((const Any*)(src + i * 16 * p.ldx))->v;
+    } else {
+        const int64_t left = p.m - mb * 128 - (t & 15) * 8;
 #pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (m + e < p.m)
-                    c[i][e >> 1] |= (int)((unsigned)src[e] << (16 * (e & 1)));
+        for (int i = 0; i < 8; ++i) {
+            c[i] = v4i{0, 0, 0, 0};
+            if (kb * 128 + i * 16 + (t >> 4) >= p.k)
+                continue;
+            if (left >= 8) {
+                c[i] = ((const Any*)(src + i * 16 * p.ldx))->v;
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    if (e < left)
+                        c[i][e >> 1] |= (int)((unsigned)src[i * 16 * p.ldx + e] << (16 * (e & 1)));
+            }
         }
     }
 #pragma unroll
@@ -426,16 +435,10 @@ __global__ __launch_bounds__(256) void tile_t16_kernel(const RotateArgs p, float
             for (int i = 0; i < 4; ++i)
                 v[e * 4 + i] = from16((unsigned short)r[i], TYPE == kTBf16);
         }
-#pragma unroll
-        for (int b = 0; b < 5; ++b)
-            if (b < p.bits)
-#pragma unroll
-                for (int i = 0; i < 32; ++i)
-                    if (!(i & (1 << b)))
-                        butterfly(v[i], v[i | (1 << b)]);
-        if (p.bits > 5)
+        stages32<0, BITS < 5 ? BITS : 5>(v);
+        if constexpr (BITS > 5)
             lane_stage<4>(v, lane);
-        if (p.bits > 6)
+        if constexpr (BITS > 6)
             lane_stage<5>(v, lane);
         unsigned m = 0;
 #pragma unroll
@@ -542,6 +545,17 @@ hipError_t rows(const RotateArgs& p, float norm, hipStream_t stream)
     return hipGetLastError();
 }
 
+template <int TYPE, bool TILE, int BITS = kFfnMaxBitsT>
+hipError_t transposed16(const RotateArgs& p, float norm, dim3 tiles, hipStream_t stream)
+{
+    if constexpr (BITS > 0) {
+        if (p.bits != BITS)
+            return transposed16<TYPE, TILE, BITS - 1>(p, norm, tiles, stream);
+    }
+    hipLaunchKernelGGL((tile_t16_kernel<TYPE, TILE, BITS>), tiles, dim3(256), 0, stream, p, norm);
+    return hipGetLastError();
+}
+
 template <int TYPE>
 hipError_t rotate(const RotateArgs& p, bool tile, bool transpose, hipStream_t stream)
 {
@@ -549,13 +563,9 @@ hipError_t rotate(const RotateArgs& p, bool tile, bool transpose, hipStream_t st
                                   : 1.0f / (float)(1 << (p.bits / 2));
     const dim3 tiles((unsigned)((p.k + 127) / 128), (unsigned)((p.m + 127) / 128));
     if constexpr (TYPE != kTF32) {
-        if (transpose) {
-            if (tile)
-                hipLaunchKernelGGL((tile_t16_kernel<TYPE, true>), tiles, dim3(256), 0, stream, p, norm);
-            else
-                hipLaunchKernelGGL((tile_t16_kernel<TYPE, false>), tiles, dim3(256), 0, stream, p, norm);
-            return hipGetLastError();
-        }
+        if (transpose)
+            return tile ? transposed16<TYPE, true>(p, norm, tiles, stream)
+                        : transposed16<TYPE, false>(p, norm, tiles, stream);
     } else if (transpose) {
         if (tile)
             hipLaunchKernelGGL((tile_kernel<TYPE, true, true>), tiles, dim3(1024), 0, stream, p, norm);
