@@ -11,6 +11,7 @@
 #include <hip/hip_runtime.h>
 
 #include <atomic>
+#include <type_traits>
 
 #include "ffn_device.h"
 
@@ -166,21 +167,23 @@ product_kernel(const ProductArgs p)
         return (((kt / WK) & (NS - 1)) * WK + kg) * kBuf;
     };
     v4i held[REG ? GA + GB : 1];
-    auto fetch = [&](int kt) __attribute__((always_inline)) {
+    // The step's chunks into registers; whole: all of them exist.
+    auto fetch_chunks = [&](int kt, auto whole) __attribute__((always_inline)) {
         const bool second = p.parts > 1 && kt >= nks;
         const int ks = second ? kt - nks : kt;
         const int64_t at = (int64_t)ks * kStep + lc * 16;
-        const int left = (int)(p.kbytes - at < 16 ? p.kbytes - at : 16);
+        const int left = whole ? 16 : (int)(p.kbytes - at < 16 ? p.kbytes - at : 16);
 #pragma unroll
         for (int g = 0; g < GA; ++g) {
             if constexpr (AT) {
                 const int64_t k = (int64_t)ks * 64 + ka0 + g * 16;
                 const int64_t end = (p.m - m0 - ca * 8) * 2;
                 held[g] = chunk_at((const char*)p.a + k * p.lda + (m0 + ca * 8) * 2,
-                                   k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
+                                   whole ? 16 : k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
             } else {
                 const int r = ra0 + row_of(g * 8 * W, TM * 16);
-                held[g] = chunk_at((const char*)p.a + (m0 + (r < mrows ? r : mrows - 1)) * p.lda +
+                held[g] = chunk_at((const char*)p.a +
+                                       (m0 + (r < mrows ? r : mrows - 1)) * p.lda +
                                        (second ? p.part_a : 0) + at,
                                    left);
             }
@@ -193,13 +196,21 @@ product_kernel(const ProductArgs p)
             if constexpr (BT) {
                 const int64_t k = (int64_t)ks * 64 + kb0 + g * 16;
                 const int64_t end = (p.n - n0 - cb * 8) * 2;
-                held[GA + g] = chunk_at(base + k * ld + (n0 + cb * 8) * 2,
-                                        k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
+                held[GA + g] =
+                    chunk_at(base + k * ld + (n0 + cb * 8) * 2,
+                             whole ? 16 : k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
             } else {
                 const int r = rb0 + (kDual && up ? g - GB / 2 : g) * 8 * W;
                 held[GA + g] = chunk_at(base + (n0 + (r < nrows ? r : nrows - 1)) * ld + at, left);
             }
         }
+    };
+    auto fetch = [&](int kt) __attribute__((always_inline)) {
+        const int ks = p.parts > 1 && kt >= nks ? kt - nks : kt;
+        if (((int64_t)ks + 1) * kStep <= p.kbytes && (!AT || mrows == BM) && (!BT || nrows == BN))
+            fetch_chunks(kt, std::true_type{});
+        else
+            fetch_chunks(kt, std::false_type{});
     };
     auto put = [&](int kt) __attribute__((always_inline)) {
 #pragma unroll
@@ -555,8 +566,13 @@ hipError_t pick16(const ProductArgs& p, hipStream_t stream)
 {
     const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 | (uintptr_t)p.lda |
                           (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
-    if (any & 15)
+    if (any & 15) {
+        constexpr Tile tiles[] = {{256, EP == kEpStore ? 256 : 128, 256, 1.9f},
+                                  {128, EP == kEpStore ? 128 : 64, 512, 1.2f}};
+        if (cheapest(tiles, p.m, p.n) == 0)
+            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, true, AT, BT>(p, stream);
         return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, true, AT, BT>(p, stream);
+    }
     if constexpr (EP == kEpStore) {
         constexpr Tile tiles[] = {{256, 256, 256, 1.6f}, {128, 128, 512, 1.06f}, {128, 128, 256, .62f}};
         switch (cheapest(tiles, p.m, p.n)) {
