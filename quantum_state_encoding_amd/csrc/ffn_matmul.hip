@@ -53,19 +53,48 @@ __device__ __forceinline__ void tile_of(int w, int tiles_m, int tiles_n, int& tm
     tn = t / rows;
 }
 
-// A 16-byte chunk of 16-bit elements at any address, zeros past `left` bytes.
-__device__ __forceinline__ v4i chunk_at(const char* p, int left)
+// Sixteen bytes at any address.
+__device__ __forceinline__ v4i load16(const char* p)
 {
     struct __attribute__((packed)) Any {
         v4i v;
     };
-    if (left >= 16)
-        return ((const Any*)p)->v;
+    return ((const Any*)p)->v;
+}
+
+// A 16-byte chunk of 16-bit elements that ends `past` bytes behind its row is
+// read `past` bytes earlier, from the row's last 16: moved to its place, with
+// zeros behind the row.
+__device__ __forceinline__ v4i drop(v4i v, int past)
+{
+    if (past & 8)
+        v = v4i{v[2], v[3], 0, 0};
+    if (past & 4)
+        v = v4i{v[1], v[2], v[3], 0};
+    if (past & 2)
+        v = v4i{(int)__builtin_amdgcn_alignbyte((unsigned)v[1], (unsigned)v[0], 2),
+                (int)__builtin_amdgcn_alignbyte((unsigned)v[2], (unsigned)v[1], 2),
+                (int)__builtin_amdgcn_alignbyte((unsigned)v[3], (unsigned)v[2], 2),
+                (int)((unsigned)v[3] >> 16)};
+    return past >= 16 ? v4i{0, 0, 0, 0} : v;
+}
+
+// The same of a row of fewer than 16 bytes, element by element.
+__device__ __forceinline__ v4i chunk_of_short_row(const char* p, int left)
+{
     v4i v = v4i{0, 0, 0, 0};
-#pragma unroll
-    for (int e = 0; e < 8; ++e)
-        if (2 * e < left)
-            v[e >> 1] |= (int)((unsigned)((const unsigned short*)p)[e] << (16 * (e & 1)));
+#pragma unroll 1
+    for (int e = 0; 2 * e < left; ++e) {
+        const int u = (int)((unsigned)((const unsigned short*)p)[e] << (16 * (e & 1)));
+        if (e < 2)
+            v[0] |= u;
+        else if (e < 4)
+            v[1] |= u;
+        else if (e < 6)
+            v[2] |= u;
+        else
+            v[3] |= u;
+    }
     return v;
 }
 
@@ -95,11 +124,16 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 
 // REG: the operands' rows need not be 16-byte aligned; they go through
 // registers, loaded before a step's products and stored to LDS after them.
+enum Alignment : int {
+    kAligned = 0,
+    kAnyAddress = 1,
+    kShortRows = 2,    // rows of fewer than 16 bytes, element by element
+};
 // AT, BT: A or B is stored [k][rows].  With p.parts = 2 the contraction goes
 // on in a second B (b1), for columns part_a bytes further on in A's rows.
 // WK groups of WM x WN waves compute the tile, each WKth step of k; LDS holds
 // NS rounds of them.
-template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, bool REG,
+template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG,
           bool AT, bool BT>
 __global__ __launch_bounds__(64 * WM * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void
 product_kernel(const ProductArgs p)
@@ -129,6 +163,7 @@ product_kernel(const ProductArgs p)
     const int mrows = (int)(p.m - m0 < BM ? p.m - m0 : BM);
     const int nrows = (int)(p.n - n0 < BNO ? p.n - n0 : BNO);
 
+    static_assert(!REG || (WK == 1 && NS == 2), "REG");
     static_assert(!(AT || BT) || (SM == kNoScale && !kDual && GA == 4 && GB == 4), "[k][rows]");
     constexpr int kRowsB = BNO / WN;                 // rows of one projection per wave
     const int nks = (int)((p.kbytes + kStep - 1) / kStep);   // steps of a part
@@ -166,53 +201,94 @@ product_kernel(const ProductArgs p)
     auto buffer_of = [=](int kt) __attribute__((always_inline)) {
         return (((kt / WK) & (NS - 1)) * WK + kg) * kBuf;
     };
-    v4i held[REG ? GA + GB : 1];
-    // The step's chunks into registers; whole: all of them exist.
-    auto fetch_chunks = [&](int kt, auto whole) __attribute__((always_inline)) {
+    // A step's chunks into registers: where they lie in their row (bytes), and
+    // what of it they miss.  [k][rows]: rows of k past the last are zeros.
+    const int64_t lena = AT ? p.m * 2 : p.kbytes, lenb = BT ? p.n * 2 : p.kbytes;
+    auto from_row = [&](int64_t at, int64_t len) __attribute__((always_inline)) {
+        return at < len - 16 ? at : len >= 16 ? len - 16 : 0;
+    };
+    unsigned rowa[REG && !AT ? GA : 1], rowb[REG && !BT ? GB : 1];   // the rows' offsets
+    if constexpr (REG && !AT) {
+#pragma unroll
+        for (int g = 0; g < GA; ++g) {
+            const int r = ra0 + row_of(g * 8 * W, TM * 16);
+            rowa[g] = (unsigned)((r < mrows ? r : mrows - 1) * p.lda);
+        }
+    }
+    if constexpr (REG && !BT) {
+#pragma unroll
+        for (int g = 0; g < GB; ++g) {
+            const bool up = kDual && g >= GB / 2;
+            const int r = rb0 + (up ? g - GB / 2 : g) * 8 * W;
+            rowb[g] = (unsigned)((r < nrows ? r : nrows - 1) * (up ? p.ldb1 : p.ldb0));
+        }
+    }
+    auto fetch = [&](int kt, v4i (&held)[GA + GB]) __attribute__((always_inline)) {
         const bool second = p.parts > 1 && kt >= nks;
         const int ks = second ? kt - nks : kt;
         const int64_t at = (int64_t)ks * kStep + lc * 16;
-        const int left = whole ? 16 : (int)(p.kbytes - at < 16 ? p.kbytes - at : 16);
+        const unsigned oa = (unsigned)from_row(AT ? (m0 + ca * 8) * 2 : at, lena);
+        const unsigned ob = (unsigned)from_row(BT ? (n0 + cb * 8) * 2 : at, lenb);
+        const int64_t left = p.kbytes / 2 - 1 - (int64_t)ks * 64;
+        const int klast = (int)(left < 63 ? left : 63);     // of the step's 64 rows of k
 #pragma unroll
         for (int g = 0; g < GA; ++g) {
-            if constexpr (AT) {
-                const int64_t k = (int64_t)ks * 64 + ka0 + g * 16;
-                const int64_t end = (p.m - m0 - ca * 8) * 2;
-                held[g] = chunk_at((const char*)p.a + k * p.lda + (m0 + ca * 8) * 2,
-                                   whole ? 16 : k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
-            } else {
-                const int r = ra0 + row_of(g * 8 * W, TM * 16);
-                held[g] = chunk_at((const char*)p.a +
-                                       (m0 + (r < mrows ? r : mrows - 1)) * p.lda +
-                                       (second ? p.part_a : 0) + at,
-                                   left);
-            }
+            const int k = ka0 + g * 16 < klast ? ka0 + g * 16 : klast;
+            const char* base = (const char*)p.a + (AT ? (int64_t)ks * 64 * p.lda : m0 * p.lda) +
+                               (second ? p.part_a : 0);
+            held[g] = load16(base + (uint64_t)((AT ? (unsigned)(k * p.lda) : rowa[g]) + oa));
         }
 #pragma unroll
         for (int g = 0; g < GB; ++g) {
             const bool up = kDual ? g >= GB / 2 : second;
-            const char* base = (const char*)(up ? p.b1 : p.b0);
             const int64_t ld = up ? p.ldb1 : p.ldb0;
-            if constexpr (BT) {
-                const int64_t k = (int64_t)ks * 64 + kb0 + g * 16;
-                const int64_t end = (p.n - n0 - cb * 8) * 2;
-                held[GA + g] =
-                    chunk_at(base + k * ld + (n0 + cb * 8) * 2,
-                             whole ? 16 : k < p.kbytes / 2 ? (int)(end < 16 ? end : 16) : 0);
-            } else {
-                const int r = rb0 + (kDual && up ? g - GB / 2 : g) * 8 * W;
-                held[GA + g] = chunk_at(base + (n0 + (r < nrows ? r : nrows - 1)) * ld + at, left);
-            }
+            const int k = kb0 + g * 16 < klast ? kb0 + g * 16 : klast;
+            const char* base =
+                (const char*)(up ? p.b1 : p.b0) + (BT ? (int64_t)ks * 64 : n0) * ld;
+            held[GA + g] = load16(base + (uint64_t)((BT ? (unsigned)(k * ld) : rowb[g]) + ob));
         }
     };
-    auto fetch = [&](int kt) __attribute__((always_inline)) {
-        const int ks = p.parts > 1 && kt >= nks ? kt - nks : kt;
-        if (((int64_t)ks + 1) * kStep <= p.kbytes && (!AT || mrows == BM) && (!BT || nrows == BN))
-            fetch_chunks(kt, std::true_type{});
-        else
-            fetch_chunks(kt, std::false_type{});
+    auto fetch_short = [&](int kt, v4i (&held)[GA + GB]) __attribute__((always_inline)) {
+        const bool second = p.parts > 1 && kt >= nks;
+        const int ks = second ? kt - nks : kt;
+        const int64_t at = (int64_t)ks * kStep + lc * 16;
+#pragma unroll
+        for (int g = 0; g < GA + GB; ++g) {
+            const bool isb = g >= GA;
+            const int gg = isb ? g - GA : g;
+            const bool up = isb && (kDual ? gg >= GB / 2 : second);
+            const bool t = isb ? BT : AT;
+            const int64_t k = (int64_t)ks * 64 + (isb ? kb0 : ka0) + gg * 16;
+            const int r = isb ? rb0 + (kDual && up ? gg - GB / 2 : gg) * 8 * W
+                              : ra0 + row_of(gg * 8 * W, TM * 16);
+            const int rows = isb ? nrows : mrows;
+            const int64_t row = t ? (k < p.kbytes / 2 ? k : 0)
+                                  : (isb ? n0 : m0) + (r < rows ? r : rows - 1);
+            const int64_t w = t ? ((isb ? n0 : m0) + (isb ? cb : ca) * 8) * 2 : at;
+            held[g] = chunk_of_short_row((const char*)(isb ? (up ? p.b1 : p.b0) : p.a) +
+                                             row * (isb ? (up ? p.ldb1 : p.ldb0) : p.lda) +
+                                             (!isb && second ? p.part_a : 0) + w,
+                                         (int)((isb ? lenb : lena) - w));
+        }
     };
-    auto put = [&](int kt) __attribute__((always_inline)) {
+    // ... and to LDS, with zeros in the place of what they miss
+    auto put = [&](int kt, v4i (&held)[GA + GB]) __attribute__((always_inline)) {
+        const bool second = p.parts > 1 && kt >= nks;
+        const int ks = second ? kt - nks : kt;
+        const int64_t at = (int64_t)ks * kStep + lc * 16;
+        if (((int64_t)ks + 1) * kStep > p.kbytes || (AT && mrows < BM) || (BT && nrows < BN)) {
+            const int64_t wa = AT ? (m0 + ca * 8) * 2 : at, wb = BT ? (n0 + cb * 8) * 2 : at;
+            const int pa = (int)(wa - from_row(wa, lena)), pb = (int)(wb - from_row(wb, lenb));
+#pragma unroll
+            for (int g = 0; g < GA + GB; ++g) {
+                const bool isb = g >= GA;
+                const int64_t k = (int64_t)ks * 64 + (isb ? kb0 + (g - GA) * 16 : ka0 + g * 16);
+                if (REG == kAnyAddress)
+                    held[g] = drop(held[g], isb ? pb : pa);
+                if ((isb ? BT : AT) && k >= p.kbytes / 2)
+                    held[g] = v4i{0, 0, 0, 0};
+            }
+        }
 #pragma unroll
         for (int g = 0; g < GA + GB; ++g) {
             const int gg = g >= GA ? g - GA : g;
@@ -269,10 +345,12 @@ product_kernel(const ProductArgs p)
     // what row_of is for), rows of B on the four registers of a result.
     const int q = lane >> 4, l16 = lane & 15;
     if constexpr (REG) {
-        if (kg < nk) {
-            fetch(kg);
-            put(kg);
-        }
+        v4i held[GA + GB];
+        if constexpr (REG == kAnyAddress)
+            fetch(0, held);
+        else
+            fetch_short(0, held);
+        put(0, held);
     } else {
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s)
@@ -325,12 +403,13 @@ product_kernel(const ProductArgs p)
             }
             __syncthreads();
         }
-        if constexpr (REG) {
-            if (kt + WK < nk)
-                fetch(kt + WK);
-        } else if (kt + (NS - 1) * WK < nk) {
+        v4i held[REG ? GA + GB : 1];
+        if constexpr (REG == kAnyAddress)
+            fetch(kt + 1 < nk ? kt + 1 : kt, held);
+        else if constexpr (REG == kShortRows)
+            fetch_short(kt + 1 < nk ? kt + 1 : kt, held);
+        else if (kt + (NS - 1) * WK < nk)
             stage(kt + (NS - 1) * WK);
-        }
         if (WK > 1 && kt >= nk)
             break;     // (the last round: no barrier follows in the loop)
         float sa[TM], sb[2];
@@ -415,8 +494,8 @@ product_kernel(const ProductArgs p)
         if constexpr (SM != kNoScale)
             add(TM - 1);
         if constexpr (REG) {
-            if (kt + WK < nk)
-                put(kt + WK);
+            if (kt + 1 < nk)
+                put(kt + 1, held);
         }
     }
 
@@ -494,7 +573,7 @@ product_kernel(const ProductArgs p)
     }
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, bool REG = false,
+template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG = kAligned,
           bool AT = false, bool BT = false>
 hipError_t run(ProductArgs p, hipStream_t stream)
 {
@@ -567,21 +646,24 @@ hipError_t pick16(const ProductArgs& p, hipStream_t stream)
     const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 | (uintptr_t)p.lda |
                           (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
     if (any & 15) {
+        const int64_t lena = AT ? p.m * 2 : p.kbytes, lenb = BT ? p.n * 2 : p.kbytes;
+        if (lena < 16 || lenb < 16)
+            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kShortRows, AT, BT>(p, stream);
         constexpr Tile tiles[] = {{256, EP == kEpStore ? 256 : 128, 256, 1.9f},
                                   {128, EP == kEpStore ? 128 : 64, 512, 1.2f}};
         if (cheapest(tiles, p.m, p.n) == 0)
-            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, true, AT, BT>(p, stream);
-        return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, true, AT, BT>(p, stream);
+            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, kAnyAddress, AT, BT>(p, stream);
+        return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kAnyAddress, AT, BT>(p, stream);
     }
     if constexpr (EP == kEpStore) {
         constexpr Tile tiles[] = {{256, 256, 256, 1.6f}, {128, 128, 512, 1.06f}, {128, 128, 256, .62f}};
         switch (cheapest(tiles, p.m, p.n)) {
         case 0:
-            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, false, AT, BT>(p, stream);
+            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, kAligned, AT, BT>(p, stream);
         case 1:
-            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, false, AT, BT>(p, stream);
+            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kAligned, AT, BT>(p, stream);
         default:
-            return run<TYPE, 128, 128, 2, 2, 1, 4, EP, kNoScale, false, AT, BT>(p, stream);
+            return run<TYPE, 128, 128, 2, 2, 1, 4, EP, kNoScale, kAligned, AT, BT>(p, stream);
         }
     } else {
         constexpr Tile tiles[] = {{256, 128, 256, 1.6f}, {128, 64, 512, 1.06f}, {128, 64, 256, .62f},
