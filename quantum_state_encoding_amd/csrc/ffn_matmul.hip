@@ -408,8 +408,6 @@ product_kernel(const ProductArgs p)
             fetch(kt + 1 < nk ? kt + 1 : kt, held);
         else if constexpr (REG == kShortRows)
             fetch_short(kt + 1 < nk ? kt + 1 : kt, held);
-        else if (kt + (NS - 1) * WK < nk)
-            stage(kt + (NS - 1) * WK);
         if (WK > 1 && kt >= nk)
             break;     // (the last round: no barrier follows in the loop)
         float sa[TM], sb[2];
@@ -480,6 +478,10 @@ product_kernel(const ProductArgs p)
             if constexpr (SM != kNoScale)
                 if (i > 0)
                     add(i - 1);
+            // (after the first rows' matrix instructions are on their way)
+            if constexpr (!REG)
+                if (i == 0 && kt + (NS - 1) * WK < nk)
+                    stage(kt + (NS - 1) * WK);
             if (i + 1 < TM)
                 __builtin_amdgcn_sched_group_barrier(0x100, AT ? 4 : 2, 0);   // LDS reads
             if constexpr (SM != kNoScale) {
