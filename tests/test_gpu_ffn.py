@@ -222,6 +222,9 @@ MATMUL = [  # m, n, k
     (33, 64, 100), (64, 500, 1000), (65, 128, 128), (128, 130, 2000), (130, 1, 16),
     (257, 255, 640), (300, 1025, 144), (1000, 700, 15), (100, 2100, 513),
     (3600, 3400, 272), (3601, 3399, 1007),
+    # one size for each tile, where it is the cheapest, with ragged edges
+    (700, 4001, 400), (1900, 4000, 260), (500, 3970, 130), (200, 1030, 2100), (20, 16400, 300),
+    (9, 16390, 1111), (31, 777, 8193), (2, 100, 9000),
 ]
 
 
@@ -323,6 +326,9 @@ GATED = [  # m, n, k
     (1, 1, 1), (1, 100, 256), (8, 16, 64), (16, 33, 100), (17, 129, 129), (33, 40, 500),
     (64, 257, 96), (65, 128, 64), (100, 130, 63), (129, 127, 258), (300, 300, 1000),
     (257, 66, 2), (515, 1030, 72), (2100, 3100, 136),
+    # a size for each tile: 64, 128 deep, 128 and 256 wide, aligned and not
+    (60, 4100, 72), (130, 8200, 40), (240, 16400, 24), (70, 16380, 130), (2050, 3001, 77),
+    (33, 300, 7), (150, 5, 3), (20, 16500, 66),
 ]
 
 
@@ -402,7 +408,10 @@ def test_gated_saturated_gates():
 
 
 BACK = [(1, 1, 1), (1, 40, 64), (7, 9, 11), (16, 64, 128), (65, 100, 130), (128, 129, 72),
-        (200, 77, 300), (300, 513, 260), (1030, 700, 515), (2100, 1600, 136)]
+        (200, 77, 300), (300, 513, 260), (1030, 700, 515), (2100, 1600, 136),
+        # each gradient's product with 256-wide tiles, and few columns
+        (2600, 72, 5120), (72, 2056, 4112), (2601, 70, 5121), (70, 2050, 4099), (300, 5, 200),
+        (200, 300, 6)]
 
 
 @pytest.mark.parametrize("m,n,k", BACK)
