@@ -53,9 +53,7 @@ struct ProductArgs {
     const void* dh;         // kEpGateGrad: gradient of C, m x n
     int64_t lddh;
     int act;                // 0 silu, 1 gelu
-    // set by the launcher: four neighbours of c, of dh, at one aligned address
-    int wide_c, wide_dh;
-    int tiles_m, tiles_n;
+    int tiles_m, tiles_n;   // set by the launcher
 };
 
 // Enqueue a product.  type: element type of A and B; row_scales: e4m3 with

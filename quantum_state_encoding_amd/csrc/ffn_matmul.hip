@@ -525,7 +525,7 @@ product_kernel(const ProductArgs p)
     }
 
     // Results: lane l holds rows l % 16 * TM .. of A and four consecutive rows
-    // of B, stored at once where the output's alignment allows.
+    // of B, stored at once.
     const bool bf = p.ctype == kTBf16;
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -560,7 +560,7 @@ product_kernel(const ProductArgs p)
                     v[k] = f * acc[i][j + TN / 2][k];
                 }
             } else if constexpr (EP == kEpGateGrad) {
-                const v4f g = load4(p.dh, m * p.lddh + n0 + nc, bf, cnt, p.wide_dh);
+                const v4f g = load4(p.dh, m * p.lddh + n0 + nc, bf, cnt);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float f, d;
@@ -568,9 +568,9 @@ product_kernel(const ProductArgs p)
                     v[k] = g[k] * acc[i][j + TN / 2][k] * d;
                     u[k] = g[k] * f;
                 }
-                store4(c, at + p.part_c, u, p.ctype, cnt, p.wide_c);
+                store4(c, at + p.part_c, u, p.ctype, cnt);
             }
-            store4(c, at, v, p.ctype, cnt, p.wide_c);
+            store4(c, at, v, p.ctype, cnt);
         }
     }
 }
@@ -582,10 +582,6 @@ hipError_t run(ProductArgs p, hipStream_t stream)
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
     constexpr size_t kLds = WK * NS * (size_t)(BM + BN) * (kStep + (SM != kNoScale ? 4 : 0));
     static_assert(kLds <= 160 * 1024 && (size_t)(WK - 1) * BM * BN * 4 <= kLds, "LDS of a CU");
-    const int64_t csize = p.ctype == kTF32 ? 4 : 2;
-    p.wide_c = (((uintptr_t)p.c | (uintptr_t)p.c1 | (uintptr_t)((p.ldc | p.ldc1 | p.part_c) * csize)) &
-                (4 * csize - 1)) == 0;
-    p.wide_dh = (((uintptr_t)p.dh | (uintptr_t)(p.lddh * 2)) & 7) == 0;
     p.tiles_m = (int)((p.m + BM - 1) / BM);
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
     auto* k = &product_kernel<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT>;
