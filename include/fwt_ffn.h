@@ -79,11 +79,19 @@ int fwt_rotate_quantize(const void* x, fwt_ffn_dtype dtype, int64_t m, int64_t k
  * which keeps all of it, at half the rate.  A row of a
  * or b is read up to k only, whatever its padding holds.  The strides lda
  * and ldb are multiples of 16 below 2^23, a and b 16-byte aligned
- * (FWT_EALIGN; a longer stride FWT_EUNSUPPORTED). */
+ * (FWT_EALIGN; a longer stride FWT_EUNSUPPORTED).
+ *  ws          scratch of fwt_scaled_matmul_workspace bytes (0 for most
+ *              sizes), 16-byte aligned, one for each call that may run at the
+ *              same time: a long contraction with few results is then shared
+ *              by several workgroups, whose sums a second kernel adds in a
+ *              fixed order.  NULL: it is not shared, which takes longer and
+ *              adds in another order. */
+int fwt_scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, fwt_scales b_kind,
+                                fwt_ffn_dtype ctype, size_t* bytes);
 int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const void* b,
                       int64_t ldb, const float* b_scales, fwt_scales b_kind, int64_t m,
                       int64_t n, int64_t k, void* c, fwt_ffn_dtype ctype, int64_t ldc,
-                      hipStream_t stream);
+                      void* ws, size_t ws_bytes, hipStream_t stream);
 
 /* h = act(x gate^T) * (x up^T): x is m x k, gate and up n x k, of one
  * dtype.  bf16 and f16: h has the same dtype, the scales are NULL; any
@@ -91,12 +99,14 @@ int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const v
  * are read faster).  e4m3: x_scales row scales, gate_scales and up_scales
  * tile scales, alignment as for fwt_scaled_matmul, h bf16, f16 or fp32.
  * Both products are summed as fwt_scaled_matmul sums them, in 32 bits, and
- * only h is rounded. */
+ * only h is rounded.  ws: as there, of fwt_gated_ffn_workspace bytes. */
+int fwt_gated_ffn_workspace(fwt_ffn_dtype dtype, int64_t m, int64_t n, int64_t k,
+                            fwt_ffn_dtype htype, size_t* bytes);
 int fwt_gated_ffn(const void* x, int64_t ldx, const float* x_scales, const void* gate,
                   int64_t ldgate, const float* gate_scales, const void* up, int64_t ldup,
                   const float* up_scales, fwt_ffn_dtype dtype, int64_t m, int64_t n, int64_t k,
-                  fwt_activation act, void* h, fwt_ffn_dtype htype, int64_t ldh,
-                  hipStream_t stream);
+                  fwt_activation act, void* h, fwt_ffn_dtype htype, int64_t ldh, void* ws,
+                  size_t ws_bytes, hipStream_t stream);
 
 /* Gradients of fwt_gated_ffn on bf16 or f16 for dh (m x n):
  *   dx = dg gate + du up,  dgate = dg^T x,  dup = du^T x,

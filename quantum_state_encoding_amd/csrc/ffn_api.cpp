@@ -117,9 +117,33 @@ constexpr Array kNone{nullptr, 0, 0, 0, 0, false};
 // 16-bit elements of a row padded to whole 16-byte chunks.
 int64_t pad8(int64_t n) { return (n + 7) & ~(int64_t)7; }
 
+// Scratch that a product's shares of a long contraction need.
+size_t shares_of(int64_t m, int64_t n, int64_t k, int type, int ctype, int epilogue, bool row,
+                 int parts = 1)
+{
+    ProductArgs p{};
+    p.m = m;
+    p.n = n;
+    p.kbytes = k * size_of(type);
+    p.ctype = ctype;
+    p.parts = parts;
+    return qse::product_workspace(p, type, epilogue, row);
+}
+
 // The backward pass's scratch: dg beside du, m rows of 2 pad8(n) 16-bit
-// elements.
-size_t backward_scratch(int64_t m, int64_t n) { return (size_t)m * 4 * (size_t)pad8(n); }
+// elements, and behind it the shares of one product at a time.
+size_t backward_sums(int64_t m, int64_t n)
+{
+    return ((size_t)m * 4 * (size_t)pad8(n) + 255) & ~(size_t)255;
+}
+size_t backward_scratch(int64_t m, int64_t n, int64_t k)
+{
+    size_t most = shares_of(m, n, k, FWT_BF16, FWT_BF16, qse::kEpGateGrad, false);
+    const size_t dx = shares_of(m, k, n, FWT_BF16, FWT_BF16, qse::kEpStore, false, 2);
+    const size_t dw = shares_of(2 * pad8(n), k, m, FWT_BF16, FWT_BF16, qse::kEpStoreT, false);
+    most = most > dx ? most : dx;
+    return backward_sums(m, n) + (most > dw ? most : dw);
+}
 
 }  // namespace
 
@@ -177,16 +201,35 @@ int fwt_rotate_quantize(const void* x, fwt_ffn_dtype dtype, int64_t m, int64_t k
     return status(qse::launch_rotate(a, (int)dtype, tile, transposed != 0, stream));
 }
 
-int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const void* b,
-                      int64_t ldb, const float* b_scales, fwt_scales b_kind, int64_t m,
-                      int64_t n, int64_t k, void* c, fwt_ffn_dtype ctype, int64_t ldc,
-                      hipStream_t stream)
+int fwt_scaled_matmul_workspace(int64_t m, int64_t n, int64_t k, fwt_scales b_kind,
+                                fwt_ffn_dtype ctype, size_t* bytes)
 {
-    if (!dims_ok(m, n, k) || !is_out(ctype) ||
+    if (!bytes || !dims_ok(m, n, k) || !is_out(ctype) ||
         (b_kind != FWT_SCALES_ROW && b_kind != FWT_SCALES_TILE))
         return FWT_EINVAL;
+    *bytes = m == 0 || n == 0 ? 0
+                              : shares_of(m, n, k, FWT_E4M3, ctype, qse::kEpStore,
+                                          b_kind == FWT_SCALES_ROW);
+    return FWT_OK;
+}
+
+int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const void* b,
+                      int64_t ldb, const float* b_scales, fwt_scales b_kind, int64_t m,
+                      int64_t n, int64_t k, void* c, fwt_ffn_dtype ctype, int64_t ldc, void* ws,
+                      size_t ws_bytes, hipStream_t stream)
+{
+    size_t need = 0;
+    const int rc0 = fwt_scaled_matmul_workspace(m, n, k, b_kind, ctype, &need);
+    if (rc0 != FWT_OK)
+        return rc0;
     if (m == 0 || n == 0)
         return FWT_OK;
+    if (!ws)
+        need = 0;
+    if (ws_bytes < need)
+        return FWT_EINVAL;
+    if (need && !aligned16(ws, 0))
+        return FWT_EALIGN;
     if (!a || !b || !c || !a_scales || !b_scales)
         return FWT_EINVAL;
     if (!aligned16(a, lda) || !aligned16(b, ldb))
@@ -200,6 +243,7 @@ int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const v
         {a_scales, blocks(k), m, m, 4, false},
         {b_scales, blocks(k), sbn, sbn, 4, false},
         {c, m, n, ldc, size_of(ctype), true},
+        need ? Array{ws, 1, (int64_t)need, (int64_t)need, 1, true} : kNone,
     };
     const int rc = check_call(arrays, stream);
     if (rc != FWT_OK)
@@ -212,27 +256,50 @@ int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const v
     p.m = m;
     p.n = n;
     p.kbytes = k;
+    p.parts = 1;
     p.sa = a_scales;
     p.sb0 = b_scales;
     p.sb_n = sbn;
     p.c = c;
     p.ldc = ldc;
     p.ctype = (int)ctype;
+    p.may_split = need != 0;
+    p.partial = ws;
     return status(qse::launch_product(p, FWT_E4M3, qse::kEpStore, b_kind == FWT_SCALES_ROW, stream));
+}
+
+int fwt_gated_ffn_workspace(fwt_ffn_dtype dtype, int64_t m, int64_t n, int64_t k,
+                            fwt_ffn_dtype htype, size_t* bytes)
+{
+    const bool f8 = dtype == FWT_E4M3;
+    if (!bytes || !dims_ok(m, n, k) || (!f8 && !is16(dtype)) ||
+        (f8 ? !is_out(htype) : htype != dtype))
+        return FWT_EINVAL;
+    *bytes = m == 0 || n == 0 ? 0 : shares_of(m, n, k, dtype, htype, qse::kEpGate, false);
+    return FWT_OK;
 }
 
 int fwt_gated_ffn(const void* x, int64_t ldx, const float* x_scales, const void* gate,
                   int64_t ldgate, const float* gate_scales, const void* up, int64_t ldup,
                   const float* up_scales, fwt_ffn_dtype dtype, int64_t m, int64_t n, int64_t k,
-                  fwt_activation act, void* h, fwt_ffn_dtype htype, int64_t ldh,
-                  hipStream_t stream)
+                  fwt_activation act, void* h, fwt_ffn_dtype htype, int64_t ldh, void* ws,
+                  size_t ws_bytes, hipStream_t stream)
 {
     const bool f8 = dtype == FWT_E4M3;
-    if (!dims_ok(m, n, k) || (!f8 && !is16(dtype)) || (f8 ? !is_out(htype) : htype != dtype) ||
-        (act != FWT_SILU && act != FWT_GELU))
+    size_t need = 0;
+    const int rc0 = fwt_gated_ffn_workspace(dtype, m, n, k, htype, &need);
+    if (rc0 != FWT_OK)
+        return rc0;
+    if (act != FWT_SILU && act != FWT_GELU)
         return FWT_EINVAL;
     if (m == 0 || n == 0)
         return FWT_OK;
+    if (!ws)
+        need = 0;
+    if (ws_bytes < need)
+        return FWT_EINVAL;
+    if (need && !aligned16(ws, 0))
+        return FWT_EALIGN;
     if (!x || !gate || !up || !h || f8 != (x_scales != nullptr) ||
         f8 != (gate_scales != nullptr) || f8 != (up_scales != nullptr))
         return FWT_EINVAL;
@@ -250,6 +317,7 @@ int fwt_gated_ffn(const void* x, int64_t ldx, const float* x_scales, const void*
         f8 ? Array{x_scales, blocks(k), m, m, 4, false} : kNone,
         f8 ? Array{gate_scales, blocks(k), blocks(n), blocks(n), 4, false} : kNone,
         f8 ? Array{up_scales, blocks(k), blocks(n), blocks(n), 4, false} : kNone,
+        need ? Array{ws, 1, (int64_t)need, (int64_t)need, 1, true} : kNone,
     };
     const int rc = check_call(arrays, stream);
     if (rc != FWT_OK)
@@ -272,6 +340,8 @@ int fwt_gated_ffn(const void* x, int64_t ldx, const float* x_scales, const void*
     p.ldc = ldh;
     p.ctype = (int)htype;
     p.act = (int)act;
+    p.may_split = need != 0;
+    p.partial = ws;
     return status(qse::launch_product(p, (int)dtype, qse::kEpGate, false, stream));
 }
 
@@ -279,7 +349,7 @@ int fwt_gated_ffn_backward_workspace(int64_t m, int64_t n, int64_t k, size_t* by
 {
     if (!bytes || !dims_ok(m, n, k))
         return FWT_EINVAL;
-    *bytes = m == 0 || n == 0 ? 0 : backward_scratch(m, n);
+    *bytes = m == 0 || n == 0 ? 0 : backward_scratch(m, n, k);
     return FWT_OK;
 }
 
@@ -347,6 +417,8 @@ int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t
     p.dh = dh;
     p.lddh = lddh;
     p.act = (int)act;
+    p.may_split = 1;
+    p.partial = (char*)ws + backward_sums(m, n);
     hipError_t e = qse::launch_product(p, (int)dtype, qse::kEpGateGrad, false, stream);
     if (e != hipSuccess)
         return status(e);
@@ -366,6 +438,8 @@ int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t
     d.c = dx;
     d.ldc = lddx;
     d.ctype = (int)dtype;
+    d.may_split = 1;
+    d.partial = p.partial;
     e = qse::launch_product(d, (int)dtype, qse::kEpStore, false, stream);
     if (e != hipSuccess)
         return status(e);
@@ -385,6 +459,8 @@ int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t
     g.ldc = lddgate;
     g.ldc1 = lddup;
     g.ctype = (int)dtype;
+    g.may_split = 1;
+    g.partial = p.partial;
     e = qse::launch_product(g, (int)dtype, qse::kEpStoreT, false, stream);
     return status(e);
 }

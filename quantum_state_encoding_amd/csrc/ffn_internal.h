@@ -53,13 +53,17 @@ struct ProductArgs {
     const void* dh;         // kEpGateGrad: gradient of C, m x n
     int64_t lddh;
     int act;                // 0 silu, 1 gelu
-    int tiles_m, tiles_n;   // set by the launcher
+    int may_split;          // partial has product_workspace bytes
+    void* partial;
+    int tiles_m, tiles_n, splits;   // set by the launcher
 };
 
 // Enqueue a product.  type: element type of A and B; row_scales: e4m3 with
 // a scale for each row of B.
 hipError_t launch_product(const ProductArgs& p, int type, int epilogue, bool row_scales,
                           hipStream_t stream);
+// Bytes of ProductArgs::partial for a product of these sizes (0: none).
+size_t product_workspace(ProductArgs p, int type, int epilogue, bool row_scales);
 // Its form for few rows of A (kEpStore: e4m3 only).
 constexpr int kStripRows = 32;
 hipError_t launch_strip(const ProductArgs& p, int type, int epilogue, bool row_scales,

@@ -122,6 +122,69 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
     }
 }
 
+// From a tile's sums to results: lane l holds rows l % 16 * TM .. of A (AT:
+// every 16th from l % 16) and four consecutive rows of B, stored at once.
+// acc: rows i0, i0 + 1, .. of the wave's BM / WM / 16.
+template <int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN>
+__device__ __forceinline__ void finish_rows(const ProductArgs& p, const v4f (&acc)[NI][TN], int i0,
+                                            int tm, int tn, int wave, int lane)
+{
+    constexpr int TM = BM / WM / 16;
+    constexpr bool kDual = EP != kEpStore;
+    constexpr int BNO = kDual ? BN / 2 : BN, kRowsB = BNO / WN;
+    const int wm = wave / WN, wn = wave % WN, q = lane >> 4, l16 = lane & 15;
+    const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNO;
+    const int mrows = (int)(p.m - m0 < BM ? p.m - m0 : BM);
+    const int nrows = (int)(p.n - n0 < BNO ? p.n - n0 : BNO);
+    const bool bf = p.ctype == kTBf16;
+#pragma unroll
+    for (int i = 0; i < NI; ++i) {
+        const int r = wm * (TM * 16) + (AT ? (i0 + i) * 16 + l16 : l16 * TM + i0 + i);
+        if (r >= mrows)
+            continue;
+        int64_t m = m0 + r;
+        void* c = p.c;
+        int64_t ldc = p.ldc;
+        if (AT && p.split) {      // rows from split on: another matrix
+            if (m >= p.split) {
+                m -= p.split;
+                c = p.c1;
+                ldc = p.ldc1;
+            }
+            if (m >= p.split_rows)
+                continue;
+        }
+#pragma unroll
+        for (int j = 0; j < (kDual ? TN / 2 : TN); ++j) {
+            const int nc = wn * kRowsB + j * 16 + q * 4;
+            if (nc >= nrows)
+                continue;
+            const int64_t at = m * ldc + n0 + nc;
+            const int cnt = nrows - nc < 4 ? nrows - nc : 4;
+            v4f v = acc[i][j], u;
+            if constexpr (EP == kEpGate) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float f, d;
+                    activation(p.act, acc[i][j][k], f, d);
+                    v[k] = f * acc[i][j + TN / 2][k];
+                }
+            } else if constexpr (EP == kEpGateGrad) {
+                const v4f g = load4(p.dh, m * p.lddh + n0 + nc, bf, cnt);
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float f, d;
+                    activation(p.act, acc[i][j][k], f, d);
+                    v[k] = g[k] * acc[i][j + TN / 2][k] * d;
+                    u[k] = g[k] * f;
+                }
+                store4(c, at + p.part_c, u, p.ctype, cnt);
+            }
+            store4(c, at, v, p.ctype, cnt);
+        }
+    }
+}
+
 // REG: the operands' rows need not be 16-byte aligned; they go through
 // registers, loaded before a step's products and stored to LDS after them.
 enum Alignment : int {
@@ -164,9 +227,14 @@ product_kernel(const ProductArgs p)
     const int nrows = (int)(p.n - n0 < BNO ? p.n - n0 : BNO);
 
     static_assert(!REG || (WK == 1 && NS == 2), "REG");
-    static_assert(!(AT || BT) || (SM == kNoScale && !kDual && GA == 4 && GB == 4), "[k][rows]");
+    static_assert(!(AT || BT) || (SM == kNoScale && !kDual && (!AT || GA == 4) && GB == 4), "[k][rows]");
     constexpr int kRowsB = BNO / WN;                 // rows of one projection per wave
     const int nks = (int)((p.kbytes + kStep - 1) / kStep);   // steps of a part
+    const int all = p.parts > 1 ? 2 * nks : nks;
+    // this workgroup's steps: all, or its share of them
+    const int share = (all + p.splits - 1) / p.splits;
+    const int first = (int)blockIdx.y * share;
+    const int nk = first + share < all ? first + share : all;
     // A wave stages 1 KiB at a time, pieces wave, wave + W, ...: 8 LDS rows of
     // an operand, or 64 k / (4 W) rows of k of one that is [k][rows].  Piece g
     // lies a constant number of rows behind the wave's first.  Descriptors
@@ -197,9 +265,9 @@ product_kernel(const ProductArgs p)
         return make_rsrc((const char*)base + (int64_t)ks * 64 * ld + r0 * 2,
                          (uint64_t)((left - 1) * ld + (((rows - r0) * 2 + 15) & ~(int64_t)15)));
     };
-    // step kt = round * WK + group
+    // step kt = first + round * WK + group
     auto buffer_of = [=](int kt) __attribute__((always_inline)) {
-        return (((kt / WK) & (NS - 1)) * WK + kg) * kBuf;
+        return ((((kt - first) / WK) & (NS - 1)) * WK + kg) * kBuf;
     };
     // A step's chunks into registers: where they lie in their row (bytes), and
     // what of it they miss.  [k][rows]: rows of k past the last are zeros.
@@ -333,7 +401,6 @@ product_kernel(const ProductArgs p)
                          base - wave * 1024 + (BM + BN) * kStep + sw * 256, vs);
     };
 
-    const int nk = p.parts > 1 ? 2 * nks : nks;
     v4f acc[TM][TN];
 #pragma unroll
     for (int i = 0; i < TM; ++i)
@@ -347,15 +414,15 @@ product_kernel(const ProductArgs p)
     if constexpr (REG) {
         v4i held[GA + GB];
         if constexpr (REG == kAnyAddress)
-            fetch(0, held);
+            fetch(first, held);
         else
-            fetch_short(0, held);
-        put(0, held);
+            fetch_short(first, held);
+        put(first, held);
     } else {
 #pragma unroll
         for (int s = 0; s < NS - 1; ++s)
-            if (s * WK + kg < nk)
-                stage(s * WK + kg);
+            if (first + s * WK + kg < nk)
+                stage(first + s * WK + kg);
     }
     const int swz = l16 >> 1;
     const int ao = (wm * TM * 16 + l16) * kStep + ((q ^ swz) * 16);
@@ -365,7 +432,7 @@ product_kernel(const ProductArgs p)
     const int sbo = (BM + BN) * kStep + (BM + wn * kRowsB + q * 4) * 4;
     const int ktail = (int)(p.kbytes % kStep);
 
-    for (int kt = kg; kt - kg < nk; kt += WK) {
+    for (int kt = first + kg; kt - kg < nk; kt += WK) {
         // The step's own loads have arrived, those of later steps go on.
         if constexpr (!REG) {
             if (NS > 2 && kt + (NS - 2) * WK < nk)
@@ -376,9 +443,9 @@ product_kernel(const ProductArgs p)
         __syncthreads();
         unsigned char* buf = lds + buffer_of(kt);
         const int k0 = kt - kg;      // the round's first step
-        if (!REG && ktail && (k0 + WK >= nk || (p.parts > 1 && k0 < nks && k0 + WK >= nks))) {
+        if (!REG && ktail && (k0 + WK >= all || (p.parts > 1 && k0 < nks && k0 + WK >= nks))) {
             // Past the end of k both operands are 0, whatever was read there.
-            const bool mine = kt == nk - 1 || kt == nks - 1;
+            const bool mine = kt == all - 1 || kt == nks - 1;
             if constexpr (AT)
                 for (int c = (ktail / 2) * kCa + tid; mine && c < BM * 8; c += 64 * W)
                     *(v4i*)(buf + c * 16) = v4i{0, 0, 0, 0};
@@ -524,61 +591,59 @@ product_kernel(const ProductArgs p)
                     acc[i][j] += sums[((g * TM + i) * TN + j) * 64 * W + tid];
     }
 
-    // Results: lane l holds rows l % 16 * TM .. of A and four consecutive rows
-    // of B, stored at once.
-    const bool bf = p.ctype == kTBf16;
+    if (p.splits > 1) {        // the shares' sums join in join_kernel
+        v4f* out = (v4f*)p.partial +
+                   ((int64_t)blockIdx.y * gridDim.x + blockIdx.x) * (TM * TN * 64 * W) + tid;
 #pragma unroll
-    for (int i = 0; i < TM; ++i) {
-        const int r = wm * (TM * 16) + (AT ? i * 16 + l16 : l16 * TM + i);
-        if (r >= mrows)
-            continue;
-        int64_t m = m0 + r;
-        void* c = p.c;
-        int64_t ldc = p.ldc;
-        if (AT && p.split) {      // rows from split on: another matrix
-            if (m >= p.split) {
-                m -= p.split;
-                c = p.c1;
-                ldc = p.ldc1;
-            }
-            if (m >= p.split_rows)
-                continue;
-        }
+        for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < (kDual ? TN / 2 : TN); ++j) {
-            const int nc = wn * kRowsB + j * 16 + q * 4;
-            if (nc >= nrows)
-                continue;
-            const int64_t at = m * ldc + n0 + nc;
-            const int cnt = nrows - nc < 4 ? nrows - nc : 4;
-            v4f v = acc[i][j], u;
-            if constexpr (EP == kEpGate) {
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float f, d;
-                    activation(p.act, acc[i][j][k], f, d);
-                    v[k] = f * acc[i][j + TN / 2][k];
-                }
-            } else if constexpr (EP == kEpGateGrad) {
-                const v4f g = load4(p.dh, m * p.lddh + n0 + nc, bf, cnt);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float f, d;
-                    activation(p.act, acc[i][j][k], f, d);
-                    v[k] = g[k] * acc[i][j + TN / 2][k] * d;
-                    u[k] = g[k] * f;
-                }
-                store4(c, at + p.part_c, u, p.ctype, cnt);
-            }
-            store4(c, at, v, p.ctype, cnt);
-        }
+            for (int j = 0; j < TN; ++j)
+                out[(i * TN + j) * 64 * W] = acc[i][j];
+        return;
     }
+    finish_rows<BM, BN, WM, WN, EP, AT>(p, acc, 0, tm, tn, wave, lane);
+}
+
+// The shares of a tile's contraction, added in their order: a workgroup for
+// each of a wave's blocks of 16 rows, so that few tiles still spread over the
+// CUs, and four shares' loads in flight.
+template <int BM, int BN, int WM, int WN, int EP, bool AT>
+__global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
+{
+    constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    const int64_t stride = (int64_t)gridDim.x * (TM * TN * 64 * W);
+    const v4f* in = (const v4f*)p.partial + (int64_t)blockIdx.x * (TM * TN * 64 * W) +
+                    (int)blockIdx.y * TN * 64 * W + threadIdx.x;
+    v4f acc[1][TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j)
+        acc[0][j] = in[j * 64 * W];
+    for (int s = 1; s < p.splits; s += 4) {
+        v4f more[4][TN];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+#pragma unroll
+            for (int j = 0; j < TN; ++j)
+                more[u][j] = in[(s + u < p.splits ? s + u : s) * stride + j * 64 * W];
+#pragma unroll
+        for (int u = 0; u < 4; ++u)
+            if (s + u < p.splits)
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[0][j] += more[u][j];
+    }
+    int tm, tn;
+    tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
+    finish_rows<BM, BN, WM, WN, EP, AT>(p, acc, (int)blockIdx.y, tm, tn,
+                                        __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6),
+                                        threadIdx.x & 63);
 }
 
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG = kAligned,
           bool AT = false, bool BT = false>
-hipError_t run(ProductArgs p, hipStream_t stream)
+hipError_t run(ProductArgs p, int splits, hipStream_t stream)
 {
+    p.splits = splits;
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
     constexpr size_t kLds = WK * NS * (size_t)(BM + BN) * (kStep + (SM != kNoScale ? 4 : 0));
     static_assert(kLds <= 160 * 1024 && (size_t)(WK - 1) * BM * BN * 4 <= kLds, "LDS of a CU");
@@ -599,7 +664,15 @@ hipError_t run(ProductArgs p, hipStream_t stream)
         if (e != hipSuccess)
             return e;
     }
-    hipLaunchKernelGGL(k, dim3((unsigned)(p.tiles_m * p.tiles_n)), dim3(64 * WM * WN * WK), kLds, stream, p);
+    const unsigned tiles = (unsigned)(p.tiles_m * p.tiles_n);
+    hipLaunchKernelGGL(k, dim3(tiles, (unsigned)splits), dim3(64 * WM * WN * WK), kLds, stream, p);
+    const hipError_t e = hipGetLastError();
+    if (splits == 1 || e != hipSuccess)
+        return e;
+    if constexpr (BM <= 128 && BN <= 128) {      // (larger tiles are never split)
+        hipLaunchKernelGGL((join_kernel<BM, BN, WM, WN, EP, AT>), dim3(tiles, BM / WM / 16),
+                           dim3(64 * WM * WN), 0, stream, p);
+    }
     return hipGetLastError();
 }
 
@@ -616,132 +689,176 @@ hipError_t run(ProductArgs p, hipStream_t stream)
 // (*) two groups of waves for e4m3, four rounds in LDS for 16 bits.  So m 512
 // n 4096 k 16384 (e4m3) takes 49 us with 64 x 64 tiles and 82 with 128 x 128
 // ones, m 4096 takes 451 and 260, and 227 with 256 x 256 ones.
+//
+// Where the tiles leave half of their slots empty, the workgroups of a tile
+// share its steps and a second kernel adds their sums, for about 5 us: m 300
+// n 200 k 16000 (fp32 out) takes 44 us in one share, 16 in twelve.
 struct Tile {
     int bm, bn, slots;   // bn: output columns
     float step;
+    int area;            // of the sums, 0: not split
+};
+struct Choice {
+    int tile, splits;
+    size_t bytes;        // of ProductArgs::partial
 };
 template <int N>
-int cheapest(const Tile (&tiles)[N], int64_t m, int64_t n)
+Choice cheapest(const Tile (&tiles)[N], const ProductArgs& p)
 {
-    int best = 0;
+    const int64_t steps = (p.kbytes + kStep - 1) / kStep * (p.parts > 1 ? 2 : 1);
+    Choice best{0, 1, 0};
     double least = 0;
     for (int i = 0; i < N; ++i) {
-        const int64_t count = ((m + tiles[i].bm - 1) / tiles[i].bm) *
-                              ((n + tiles[i].bn - 1) / tiles[i].bn);
-        const double cost = (double)((count + tiles[i].slots - 1) / tiles[i].slots) * tiles[i].step;
+        const Tile& t = tiles[i];
+        const int64_t count = ((p.m + t.bm - 1) / t.bm) * ((p.n + t.bn - 1) / t.bn);
+        double cost = (double)((count + t.slots - 1) / t.slots) * t.step * steps;
+        int splits = 1;
+        if (t.area && p.may_split && count * 2 <= t.slots) {
+            int64_t s = t.slots / count < 16 ? t.slots / count : 16;
+            s = s < steps / 4 ? s : steps / 4;
+            // every share has steps, the last one fewer
+            s = s > 1 ? (steps + (steps + s - 1) / s - 1) / ((steps + s - 1) / s) : 1;
+            const double shared = (double)((steps + s - 1) / s) * t.step + 5.0;
+            if (s > 1 && shared < cost) {
+                cost = shared;
+                splits = (int)s;
+            }
+        }
         if (i == 0 || cost < least) {
-            best = i;
             least = cost;
+            best = Choice{i, splits, splits > 1 ? (size_t)splits * count * t.area * 4 : 0};
         }
     }
     return best;
 }
 
+// 16-bit operands at any address; query: the bytes of ProductArgs::partial
+// instead of a launch.
+template <int TYPE, int EP, bool AT, bool BT>
+hipError_t pick_any(const ProductArgs& p, size_t* query, hipStream_t stream)
+{
+    const int64_t lena = AT ? p.m * 2 : p.kbytes, lenb = BT ? p.n * 2 : p.kbytes;
+    constexpr bool dual = EP != kEpStore;
+    constexpr Tile tiles[] = {{256, dual ? 128 : 256, 256, 1.9f, 0},
+                              {128, dual ? 64 : 128, 512, 1.2f, 128 * 128}};
+    const Choice c = cheapest(tiles, p);
+    if (query) {
+        *query = c.bytes;
+        return hipSuccess;
+    }
+    if (lena < 16 || lenb < 16)
+        return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kShortRows, AT, BT>(p, 1, stream);
+    if (c.tile == 0)
+        return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, kAnyAddress, AT, BT>(p, 1, stream);
+    return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kAnyAddress, AT, BT>(p, c.splits, stream);
+}
+
 // 16-bit operands.
 template <int TYPE, int EP, bool AT, bool BT>
-hipError_t pick16(const ProductArgs& p, hipStream_t stream)
+hipError_t pick16(const ProductArgs& p, size_t* query, hipStream_t stream)
 {
-    const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 | (uintptr_t)p.lda |
-                          (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
-    if (any & 15) {
-        const int64_t lena = AT ? p.m * 2 : p.kbytes, lenb = BT ? p.n * 2 : p.kbytes;
-        if (lena < 16 || lenb < 16)
-            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kShortRows, AT, BT>(p, stream);
-        constexpr Tile tiles[] = {{256, EP == kEpStore ? 256 : 128, 256, 1.9f},
-                                  {128, EP == kEpStore ? 128 : 64, 512, 1.2f}};
-        if (cheapest(tiles, p.m, p.n) == 0)
-            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, kAnyAddress, AT, BT>(p, stream);
-        return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kAnyAddress, AT, BT>(p, stream);
-    }
-    if constexpr (EP == kEpStore) {
-        constexpr Tile tiles[] = {{256, 256, 256, 1.6f}, {128, 128, 512, 1.06f}, {128, 128, 256, .62f}};
-        switch (cheapest(tiles, p.m, p.n)) {
-        case 0:
-            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, kAligned, AT, BT>(p, stream);
-        case 1:
-            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kAligned, AT, BT>(p, stream);
-        default:
-            return run<TYPE, 128, 128, 2, 2, 1, 4, EP, kNoScale, kAligned, AT, BT>(p, stream);
-        }
+    size_t any_bytes = 0;
+    if (query) {
+        (void)pick_any<TYPE, EP, AT, BT>(p, &any_bytes, stream);
     } else {
-        constexpr Tile tiles[] = {{256, 128, 256, 1.6f}, {128, 64, 512, 1.06f}, {128, 64, 256, .62f},
-                                  {64, 64, 256, .42f}};
-        switch (cheapest(tiles, p.m, p.n)) {
-        case 0:
-            return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale>(p, stream);
-        case 1:
-            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale>(p, stream);
-        case 2:
-            return run<TYPE, 128, 128, 2, 2, 1, 4, EP, kNoScale>(p, stream);
-        default:
-            return run<TYPE, 64, 128, 1, 4, 1, 4, EP, kNoScale>(p, stream);
-        }
+        const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 |
+                              (uintptr_t)p.lda | (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
+        if (any & 15)
+            return pick_any<TYPE, EP, AT, BT>(p, nullptr, stream);
     }
+    constexpr bool dual = EP != kEpStore;
+    // (A of 64 rows cannot be [k][rows]: a wave stages whole KiB of it)
+    constexpr Tile tiles[] = {{256, dual ? 128 : 256, 256, 1.6f, 0},
+                              {128, dual ? 64 : 128, 512, 1.06f, 0},
+                              {128, dual ? 64 : 128, 256, .62f, 128 * 128},
+                              {64, dual ? 64 : 128, 256, AT ? 1e30f : .42f, 64 * 128}};
+    const Choice c = cheapest(tiles, p);
+    if (query) {
+        *query = any_bytes > c.bytes ? any_bytes : c.bytes;
+        return hipSuccess;
+    }
+    switch (c.tile) {
+    case 0:
+        return run<TYPE, 256, 256, 2, 4, 1, 2, EP, kNoScale, kAligned, AT, BT>(p, 1, stream);
+    case 1:
+        return run<TYPE, 128, 128, 2, 2, 1, 2, EP, kNoScale, kAligned, AT, BT>(p, 1, stream);
+    case 2:
+        return run<TYPE, 128, 128, 2, 2, 1, 4, EP, kNoScale, kAligned, AT, BT>(p, c.splits, stream);
+    }
+    if constexpr (!AT)
+        return run<TYPE, 64, 128, 1, 4, 1, 4, EP, kNoScale, kAligned, AT, BT>(p, c.splits, stream);
+    return hipErrorInvalidValue;
 }
 
 // e4m3 operands.  The widened operands of an fp32 result, or a scale for each
 // row of B, leave no registers for the largest tile.
 template <int TYPE, int EP, int SM>
-hipError_t pick8(const ProductArgs& p, hipStream_t stream)
+hipError_t pick8(const ProductArgs& p, size_t* query, hipStream_t stream)
 {
-    constexpr bool exact = TYPE == kTE4m3Exact;
+    constexpr bool exact = TYPE == kTE4m3Exact, dual = EP != kEpStore;
     constexpr float never = 1e30f;
     constexpr float large = exact || SM == kRowScale ? never : 1.75f;
-    if constexpr (EP == kEpStore) {
-        constexpr Tile tiles[] = {{128, 128, 512, exact ? 2.0f : 1.05f},
-                                  {128, 128, 256, exact ? 1.1f : .65f},
-                                  {64, 64, 512, exact ? .70f : .40f},
-                                  {64, 64, 256, exact ? .36f : .26f},
-                                  {256, 256, 256, large}};
-        switch (cheapest(tiles, p.m, p.n)) {
-        case 0:
-            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM>(p, stream);
-        case 1:
-            return run<TYPE, 128, 128, 2, 2, 2, 2, EP, SM>(p, stream);
-        case 2:
-            return run<TYPE, 64, 64, 2, 2, 2, 2, EP, SM>(p, stream);
-        case 3:
-            // (fp32 results: four groups of waves 10-15 % faster than two
-            // with four rounds in LDS; 16-bit results 5-10 % slower)
-            return run<TYPE, 64, 64, 2, 2, exact ? 4 : 2, exact ? 2 : 4, EP, SM>(p, stream);
-        }
-    } else {
-        constexpr Tile tiles[] = {{128, 64, 512, exact ? 2.0f : 1.05f},
-                                  {128, 64, 256, exact ? 1.1f : .65f},
-                                  {64, 64, 256, exact ? .60f : .40f},
-                                  {256, 128, 256, large}};
-        switch (cheapest(tiles, p.m, p.n)) {
-        case 0:
-            return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM>(p, stream);
-        case 1:
-            return run<TYPE, 128, 128, 2, 2, 2, 2, EP, SM>(p, stream);
-        case 2:
-            return run<TYPE, 64, 128, 1, 4, 3, 2, EP, SM>(p, stream);
-        }
+    constexpr Tile tiles[] = {
+        {256, dual ? 128 : 256, 256, large, 0},
+        {128, dual ? 64 : 128, 512, exact ? 2.0f : 1.05f, 0},
+        {128, dual ? 64 : 128, 256, exact ? 1.1f : .65f, 0},
+        {64, 64, dual ? 256 : 512, dual ? (exact ? .60f : .40f) : exact ? .70f : .40f,
+         dual ? 64 * 128 : 0},
+        {64, 64, 256, dual ? never : exact ? .36f : .26f, 64 * 64}};
+    const Choice c = cheapest(tiles, p);
+    if (query) {
+        *query = c.bytes;
+        return hipSuccess;
+    }
+    switch (c.tile) {
+    case 1:
+        return run<TYPE, 128, 128, 2, 2, 1, 2, EP, SM>(p, 1, stream);
+    case 2:
+        return run<TYPE, 128, 128, 2, 2, 2, 2, EP, SM>(p, 1, stream);
+    case 3:
+        if constexpr (dual)
+            return run<TYPE, 64, 128, 1, 4, 3, 2, EP, SM>(p, c.splits, stream);
+        else
+            return run<TYPE, 64, 64, 2, 2, 2, 2, EP, SM>(p, 1, stream);
+    case 4:
+        // (fp32 results: four groups of waves 10-15 % faster than two with
+        // four rounds in LDS; 16-bit results 5-10 % slower)
+        if constexpr (!dual)
+            return run<TYPE, 64, 64, 2, 2, exact ? 4 : 2, exact ? 2 : 4, EP, SM>(p, c.splits, stream);
     }
     if constexpr (large != never)
-        return run<TYPE, 256, 256, 2, 4, 1, 2, EP, SM>(p, stream);
+        return run<TYPE, 256, 256, 2, 4, 1, 2, EP, SM>(p, 1, stream);
     return hipErrorInvalidValue;
 }
 
 template <int TYPE>
-hipError_t launch16(const ProductArgs& p, int ep, hipStream_t stream)
+hipError_t launch16(const ProductArgs& p, int ep, size_t* query, hipStream_t stream)
 {
     if (ep == kEpGate)
-        return pick16<TYPE, kEpGate, false, false>(p, stream);
+        return pick16<TYPE, kEpGate, false, false>(p, query, stream);
     if (ep == kEpGateGrad)
-        return pick16<TYPE, kEpGateGrad, false, false>(p, stream);
-    return ep == kEpStoreT ? pick16<TYPE, kEpStore, true, true>(p, stream)
-                           : pick16<TYPE, kEpStore, false, true>(p, stream);
+        return pick16<TYPE, kEpGateGrad, false, false>(p, query, stream);
+    return ep == kEpStoreT ? pick16<TYPE, kEpStore, true, true>(p, query, stream)
+                           : pick16<TYPE, kEpStore, false, true>(p, query, stream);
 }
 
 template <int TYPE>
-hipError_t launch8(const ProductArgs& p, int ep, bool row_scales, hipStream_t stream)
+hipError_t launch8(const ProductArgs& p, int ep, bool row_scales, size_t* query, hipStream_t stream)
 {
     if (ep == kEpGate)
-        return pick8<TYPE, kEpGate, kTileScale>(p, stream);
-    return row_scales ? pick8<TYPE, kEpStore, kRowScale>(p, stream)
-                      : pick8<TYPE, kEpStore, kTileScale>(p, stream);
+        return pick8<TYPE, kEpGate, kTileScale>(p, query, stream);
+    return row_scales ? pick8<TYPE, kEpStore, kRowScale>(p, query, stream)
+                      : pick8<TYPE, kEpStore, kTileScale>(p, query, stream);
+}
+
+hipError_t tiles_for(const ProductArgs& p, int type, int ep, bool row_scales, size_t* query,
+                     hipStream_t stream)
+{
+    if (type == kTE4m3)
+        return p.ctype == kTF32 ? launch8<kTE4m3Exact>(p, ep, row_scales, query, stream)
+                                : launch8<kTE4m3>(p, ep, row_scales, query, stream);
+    return type == kTBf16 ? launch16<kTBf16>(p, ep, query, stream)
+                          : launch16<kTF16>(p, ep, query, stream);
 }
 
 // Few rows: the strip kernel, except where 64-row tiles fill the CUs and their
@@ -763,10 +880,16 @@ hipError_t launch_product(const ProductArgs& p, int type, int ep, bool row_scale
 {
     if (strips(p, type, ep))
         return launch_strip(p, type, ep, row_scales, stream);
-    if (type == kTE4m3)
-        return p.ctype == kTF32 ? launch8<kTE4m3Exact>(p, ep, row_scales, stream)
-                                : launch8<kTE4m3>(p, ep, row_scales, stream);
-    return type == kTBf16 ? launch16<kTBf16>(p, ep, stream) : launch16<kTF16>(p, ep, stream);
+    return tiles_for(p, type, ep, row_scales, nullptr, stream);
+}
+
+size_t product_workspace(ProductArgs p, int type, int ep, bool row_scales)
+{
+    size_t bytes = 0;
+    p.may_split = 1;
+    if (!strips(p, type, ep))
+        (void)tiles_for(p, type, ep, row_scales, &bytes, nullptr);
+    return bytes;
 }
 
 }  // namespace qse

@@ -24,7 +24,8 @@ ROTATE_MAX_BITS, ROTATE_MAX_BITS_T = 14, 7   # FWT_ROTATE_MAX_BITS, .._T
 BLOCK = 128                                  # elements of k that share a scale
 
 # Every symbol include/fwt_ffn.h declares.
-FFN_SYMBOLS = ("fwt_rotate_quantize_workspace", "fwt_rotate_quantize", "fwt_scaled_matmul",
+FFN_SYMBOLS = ("fwt_rotate_quantize_workspace", "fwt_rotate_quantize",
+               "fwt_scaled_matmul_workspace", "fwt_scaled_matmul", "fwt_gated_ffn_workspace",
                "fwt_gated_ffn", "fwt_gated_ffn_backward_workspace", "fwt_gated_ffn_backward")
 
 _SCALES = {"row": 0, "tile": 1}
@@ -45,10 +46,12 @@ def _load():
         lib.fwt_rotate_quantize_workspace.argtypes = [i64, i64, i32, i32, i32, psz]
         lib.fwt_rotate_quantize.argtypes = [vp, i32, i64, i64, i64, i32, i32, i32, vp, i64, vp,
                                             vp, sz, vp]
+        lib.fwt_scaled_matmul_workspace.argtypes = [i64, i64, i64, i32, i32, psz]
         lib.fwt_scaled_matmul.argtypes = [vp, i64, vp, vp, i64, vp, i32, i64, i64, i64, vp, i32,
-                                          i64, vp]
+                                          i64, vp, sz, vp]
+        lib.fwt_gated_ffn_workspace.argtypes = [i32, i64, i64, i64, i32, psz]
         lib.fwt_gated_ffn.argtypes = [vp, i64, vp, vp, i64, vp, vp, i64, vp, i32, i64, i64, i64,
-                                      i32, vp, i32, i64, vp]
+                                      i32, vp, i32, i64, vp, sz, vp]
         lib.fwt_gated_ffn_backward_workspace.argtypes = [i64, i64, i64, psz]
         lib.fwt_gated_ffn_backward.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, i32, i64, i64,
                                                i64, i32, vp, i64, vp, i64, vp, i64, vp, sz, vp]
@@ -141,6 +144,12 @@ def _scratch(nbytes, like):
     return ws, ws.data_ptr()
 
 
+def _may_share(m, n, k):
+    """Whether a product of these sizes could want scratch: only where few
+    tiles (of 64 x 64 and more) have many steps."""
+    return m > 16 and k >= 512 and m * n <= 1 << 21
+
+
 def _current():
     """The current device, or the reason that there is none."""
     try:
@@ -199,12 +208,19 @@ def scaled_matmul(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=Non
     _scales_of(a_scales, "a_scales", dev, nblocks, m, ("row",))
     kind = _scales_of(b_scales, "b_scales", dev, nblocks, n, ("tile", "row"))
     dtype = _out_dtype(out_dtype, out)
+    need = 0
+    if _may_share(m, n, k):
+        size = ctypes.c_size_t(0)
+        _raise(lib.fwt_scaled_matmul_workspace(m, n, k, _SCALES[kind], _types[dtype],
+                                               ctypes.byref(size)), "fwt_scaled_matmul_workspace")
+        need = size.value
     handle, where = _on(stream, dev)
     with where:
         c, ldc = _result(out, "out", dev, m, n, dtype, a)
+        ws, wp = _scratch(need, a)
     _raise(lib.fwt_scaled_matmul(a.data_ptr(), lda, a_scales.data_ptr(), b.data_ptr(), ldb,
                                  b_scales.data_ptr(), _SCALES[kind], m, n, k, c.data_ptr(),
-                                 _types[dtype], ldc, handle), "fwt_scaled_matmul")
+                                 _types[dtype], ldc, wp, need, handle), "fwt_scaled_matmul")
     return c
 
 
@@ -241,12 +257,20 @@ def gated_ffn(x, gate, up, act="silu", x_scales=None, gate_scales=None, up_scale
         if dtype is not x.dtype:
             raise ValueError("the output has the operands' dtype")
     code = _act(act)
+    need = 0
+    if _may_share(m, n, k):
+        size = ctypes.c_size_t(0)
+        _raise(lib.fwt_gated_ffn_workspace(_types[x.dtype], m, n, k, _types[dtype],
+                                           ctypes.byref(size)), "fwt_gated_ffn_workspace")
+        need = size.value
     handle, where = _on(stream, dev)
     with where:
         h, ldh = _result(out, "out", dev, m, n, dtype, x)
+        ws, wp = _scratch(need, x)
     _raise(lib.fwt_gated_ffn(x.data_ptr(), ldx, sp[0], gate.data_ptr(), ldg, sp[1],
                              up.data_ptr(), ldu, sp[2], _types[x.dtype], m, n, k, code,
-                             h.data_ptr(), _types[dtype], ldh, handle), "fwt_gated_ffn")
+                             h.data_ptr(), _types[dtype], ldh, wp, need, handle),
+           "fwt_gated_ffn")
     return h
 
 

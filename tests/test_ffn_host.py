@@ -68,8 +68,9 @@ def test_rotate_workspace(L):
 
 
 def matmul(L, a=P, lda=256, sa=2 * P, b=3 * P, ldb=256, sb=4 * P, kind=0, m=4, n=8, k=256,
-           c=5 * P, ctype=BF16, ldc=8):
-    return L.fwt_scaled_matmul(a, lda, sa, b, ldb, sb, kind, m, n, k, c, ctype, ldc, None)
+           c=5 * P, ctype=BF16, ldc=8, ws=None, wsb=0):
+    return L.fwt_scaled_matmul(a, lda, sa, b, ldb, sb, kind, m, n, k, c, ctype, ldc, ws, wsb,
+                               None)
 
 
 def test_matmul_refusals(L):
@@ -85,9 +86,9 @@ def test_matmul_refusals(L):
 
 
 def gated(L, x=P, ldx=64, xs=None, g=2 * P, ldg=64, gs=None, u=3 * P, ldu=64, us=None,
-          dtype=BF16, m=4, n=8, k=64, act=0, h=4 * P, htype=BF16, ldh=8):
+          dtype=BF16, m=4, n=8, k=64, act=0, h=4 * P, htype=BF16, ldh=8, ws=None, wsb=0):
     return L.fwt_gated_ffn(x, ldx, xs, g, ldg, gs, u, ldu, us, dtype, m, n, k, act, h, htype,
-                           ldh, None)
+                           ldh, ws, wsb, None)
 
 
 def test_gated_refusals(L):
@@ -126,6 +127,40 @@ def test_backward_refusals(L):
     assert L.fwt_gated_ffn_backward_workspace(0, 8, 64, ctypes.byref(out)) == OK
     assert out.value == 0
     assert L.fwt_gated_ffn_backward_workspace(4, 8, 0, ctypes.byref(out)) == EINVAL
+
+
+def test_workspaces_of_shared_contractions(L):
+    def size(fn, *a):
+        out = ctypes.c_size_t(77)
+        return fn(*a, ctypes.byref(out)), out.value
+    mm, gf = L.fwt_scaled_matmul_workspace, L.fwt_gated_ffn_workspace
+    # few tiles with many steps; not: few rows, few steps, many tiles
+    for dtype in (BF16, F16, F32):
+        st, n = size(mm, 300, 200, 16000, 0, dtype)
+        assert st == OK and 0 < n <= 16 << 20
+    assert size(mm, 4, 200, 16000, 0, BF16) == (OK, 0)
+    assert size(mm, 300, 200, 256, 1, BF16) == (OK, 0)
+    assert size(mm, 4096, 4096, 16384, 1, BF16) == (OK, 0)
+    assert size(mm, 0, 200, 16000, 1, BF16) == (OK, 0)
+    assert size(mm, 300, 200, 0, 1, BF16)[0] == EINVAL
+    assert size(mm, 300, 200, 16000, 3, BF16)[0] == EINVAL
+    assert size(mm, 300, 200, 16000, 0, E4M3)[0] == EINVAL
+    assert mm(1, 1, 1, 0, BF16, None) == EINVAL
+    st, n = size(gf, BF16, 64, 64, 8016, BF16)
+    assert st == OK and 0 < n <= 16 << 20
+    assert size(gf, E4M3, 300, 128, 16384, F32)[1] > 0
+    assert size(gf, BF16, 64, 64, 8016, F16)[0] == EINVAL
+    assert gf(BF16, 1, 1, 1, BF16, None) == EINVAL
+    # a workspace that is given has to be whole and aligned
+    big = dict(m=300, n=200, k=16000, lda=16000, ldb=16000, ldc=200)
+    far = {n: (i + 1) << 28 for i, n in enumerate(("a", "sa", "b", "sb", "c", "ws"))}
+    assert matmul(L, **big, **dict(far, wsb=16)) == EINVAL
+    assert matmul(L, **big, **dict(far, ws=far["ws"] + 4, wsb=1 << 24)) == EALIGN
+    assert matmul(L, **big, **dict(far, ws=far["a"], wsb=1 << 24)) == EINVAL
+    far = {n: (i + 1) << 28 for i, n in enumerate(("x", "g", "u", "h", "ws"))}
+    big = dict(m=64, n=64, k=8016, ldx=8016, ldg=8016, ldu=8016, ldh=64)
+    assert gated(L, **big, **dict(far, wsb=16)) == EINVAL
+    assert gated(L, **big, **dict(far, ws=far["ws"] + 8, wsb=1 << 24)) == EALIGN
 
 
 def test_host_tensors_are_refused(L):

@@ -225,6 +225,8 @@ MATMUL = [  # m, n, k
     # one size for each tile, where it is the cheapest, with ragged edges
     (700, 4001, 400), (1900, 4000, 260), (500, 3970, 130), (200, 1030, 2100), (20, 16400, 300),
     (9, 16390, 1111), (31, 777, 8193), (2, 100, 9000),
+    # few results of a long contraction, which several workgroups share
+    (300, 200, 16001), (65, 70, 9100), (33, 129, 30000),
 ]
 
 
@@ -329,6 +331,8 @@ GATED = [  # m, n, k
     # a size for each tile: 64, 128 deep, 128 and 256 wide, aligned and not
     (60, 4100, 72), (130, 8200, 40), (240, 16400, 24), (70, 16380, 130), (2050, 3001, 77),
     (33, 300, 7), (150, 5, 3), (20, 16500, 66),
+    # contractions that are shared
+    (64, 64, 8016), (300, 128, 8200), (100, 70, 6001), (40, 300, 12345),
 ]
 
 
@@ -411,7 +415,9 @@ BACK = [(1, 1, 1), (1, 40, 64), (7, 9, 11), (16, 64, 128), (65, 100, 130), (128,
         (200, 77, 300), (300, 513, 260), (1030, 700, 515), (2100, 1600, 136),
         # each gradient's product with 256-wide tiles, and few columns
         (2600, 72, 5120), (72, 2056, 4112), (2601, 70, 5121), (70, 2050, 4099), (300, 5, 200),
-        (200, 300, 6)]
+        (200, 300, 6),
+        # each product's contraction shared
+        (16, 64, 8016), (64, 4100, 200), (4000, 40, 72), (70, 2051, 133), (3001, 33, 41)]
 
 
 @pytest.mark.parametrize("m,n,k", BACK)
@@ -586,6 +592,8 @@ def test_captured_and_replayed():
     g = gen(22)
     w, q = block_weights(g, 512, 1024, 9, 10)
     wb = [t.bfloat16() for t in w]
+    wide = torch.randn(48, 9000, generator=g, device="cuda").bfloat16()   # shared contractions
+    wq = qse.rotate_quantize(wide)
     x = torch.randn(130, 512, generator=g, device="cuda").bfloat16()
     one = torch.randn(1, 512, generator=g, device="cuda").bfloat16()
     grad = torch.randn(130, 1024, generator=g, device="cuda").bfloat16()
@@ -594,7 +602,9 @@ def test_captured_and_replayed():
         return (block_8bit(x, *q, 9, 10), block_8bit(one, *q, 9, 10),
                 qse.gated_ffn(x, wb[0], wb[1], act="gelu"),
                 *qse.gated_ffn_backward(x, wb[0], wb[1], grad),
-                *[t.float() for t in qse.rotate_quantize(wb[2], bits=10, scales="tile")])
+                *[t.float() for t in qse.rotate_quantize(wb[2], bits=10, scales="tile")],
+                qse.gated_ffn(wide, wide, wide), qse.scaled_matmul(*wq, *wq),
+                *qse.gated_ffn_backward(wide, wide, wide, grad[:48, :48]))
     side = torch.cuda.Stream()
     side.wait_stream(torch.cuda.current_stream())
     with torch.cuda.stream(side):
