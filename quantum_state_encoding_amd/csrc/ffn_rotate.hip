@@ -109,12 +109,11 @@ __device__ __forceinline__ void wave_stages(float (&v)[16], int bits, int lane)
 template <int N>
 __device__ __forceinline__ unsigned block_max(const float (&v)[N])
 {
-    unsigned m = 0;
+    float f = 0.0f;      // (the maximum that hands NaN on)
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-        const unsigned u = __float_as_uint(v[i]) & 0x7fffffffu;
-        m = m > u ? m : u;
-    }
+    for (int i = 0; i < N; ++i)
+        f = __builtin_elementwise_maximum(f, __builtin_fabsf(v[i]));
+    unsigned m = __float_as_uint(f) & 0x7fffffffu;
     unsigned o = lane_partner_u32<0>(m);
     m = m > o ? m : o;
     o = lane_partner_u32<1>(m);
@@ -213,19 +212,22 @@ __global__ __launch_bounds__(256) void rows_kernel(const RotateArgs p, float nor
     finish<MODE>(p, v, norm, !(p.bits & 1), row, kb, lane & 7, live);
 }
 
-// Rotations of 2^11 to 2^14: a workgroup of 2^b / 32 threads for each, all
-// stages on 32 registers a thread, in three layouts with LDS between them:
+// Rotations of 2^11 to 2^14: a workgroup of 2^b / 32 threads for each, in
+// three layouts with LDS between them:
 //   A  bits 10 .. b-1 and 0 .. 14-b: 2^(15-b) neighbours of every 1024
-//   B  bits 5 .. 9: every 32nd of a 1024
-//   C  bits 15-b .. 4: 32 neighbours, a quarter of a block
-// (A lane stage costs two instructions an element, a register stage one, and
-// the vector instructions are what comes closest to the memory's time: about
-// 20 an element, 68 us of the 78 that 8192 x 16384 bf16 take from memory.)
+//   B  bits 5 .. 9: every 32nd of a 1024, register stages
+//   C  bits 15-b .. 4: 32 neighbours, a quarter of a block, register stages
+// A is H_32 times 32 inputs: for 16-bit inputs, as they come from memory, on
+// the matrix cores (products by +-1 are exact, sums are fp32), for fp32
+// register stages.  A lane stage costs two instructions an element, a register
+// stage one, and the vector instructions are what comes closest to the
+// memory's time: 8192 x 16384 bf16 take 78 us from memory and 95 with A in
+// registers (25 instructions an element), 90 with A on the matrix cores (20).
 //
-// Element i stands in LDS at i ^ (bits 6-8 of i at 2-4) ^ (bit 10 at 5): so
-// the 16-byte accesses of C (16 lanes, 32 elements apart) and the 4-byte ones
-// of B (two runs of 32) take all banks.  Each layout's addresses are a few
-// lane values and constants that are added.
+// Element i stands in LDS at i ^ (bits 6-8 of i at 2-4) ^ (bits 10 + 11 at 5):
+// so the 16-byte accesses of C (16 lanes, 32 elements apart), the 4-byte ones
+// of B (two runs of 32) and A's take all banks.  Each layout's addresses are a
+// few lane values and constants that are added.
 // Stages on register bits [LO, HI) of 32 values.
 template <int LO, int HI>
 __device__ __forceinline__ void stages32(float (&v)[32])
@@ -238,11 +240,104 @@ __device__ __forceinline__ void stages32(float (&v)[32])
                 butterfly(v[i], v[i | (1 << b)]);
 }
 
+// Layout A, from memory to LDS.
+template <int BITS>
+__device__ __forceinline__ void layout_a32(const float* x, float* lds, int t)
+{
+    constexpr int kNear = 1 << (15 - BITS), kSegs = 1 << (BITS - 10);
+    struct __attribute__((packed)) Near {
+        float w[kNear];
+    };
+    typedef float v2f __attribute__((ext_vector_type(2)));
+    float v[32];
+#pragma unroll
+    for (int g = 0; g < kSegs; ++g) {
+        const Near n = *(const Near*)(x + t * kNear + g * 1024);
+#pragma unroll
+        for (int i = 0; i < kNear; ++i)
+            v[g * kNear + i] = n.w[i];
+    }
+    stages32<0, 5>(v);
+    const int a0 = t * kNear, am = ((a0 >> 6) & 7) << 2;
+#pragma unroll
+    for (int i = 0; i < kNear; i += 2) {
+        float* const even = lds + ((a0 + i) ^ am);
+        float* const odd = lds + ((a0 + i) ^ am ^ 32);
+#pragma unroll
+        for (int g = 0; g < kSegs; ++g)
+            *(v2f*)(((g ^ (g >> 1)) & 1 ? odd : even) + g * 1024) =
+                v2f{v[g * kNear + i], v[g * kNear + i + 1]};
+    }
+}
+
+// The same for 16-bit inputs: 16 places at a time, the second operand's lane
+// (q, l) holds inputs 8 q .. 8 q + 7 of place l, the first one's those of row l
+// (and 16 + l) of H_32: (-1)^popcount(row AND input).
+template <int TYPE, int BITS>
+__device__ __forceinline__ void layout_a16(const unsigned short* x, float* lds, int t)
+{
+    constexpr int kNear = 1 << (15 - BITS);
+    constexpr int kRun = kNear < 8 ? kNear : 8;     // neighbours of a load
+    const int lane = t & 63, q = lane >> 4, l16 = lane & 15, place0 = t - lane;
+    v4i in[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const unsigned short* at = x + (place0 + c * 16 + l16) * kNear + q * 8 / kNear * 1024 +
+                                   q * 8 % kNear;
+        struct __attribute__((packed)) Run {
+            unsigned short w[kRun];
+        };
+        struct All {
+            Run r[8 / kRun];
+        } all;
+#pragma unroll
+        for (int r = 0; r < 8 / kRun; ++r)
+            all.r[r] = *(const Run*)(at + r * 1024);
+        in[c] = __builtin_bit_cast(v4i, all);
+    }
+    // signs of two inputs at a time: bits 0-2 of the input are in the word
+    const unsigned one = TYPE == kTBf16 ? 0x3f803f80u : 0x3c003c00u;
+    const auto sign = [](int bit) { return bit ? 0x80008000u : 0u; };
+    const unsigned w0 = one ^ sign((l16 >> 3) & q & 1) ^ (l16 & 1 ? 0x80000000u : 0u);
+    const unsigned s1 = sign(l16 & 2), s2 = sign(l16 & 4);
+    v4i h[2];
+    h[0] = v4i{(int)w0, (int)(w0 ^ s1), (int)(w0 ^ s2), (int)(w0 ^ s1 ^ s2)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[1][i] = (int)((unsigned)h[0][i] ^ sign(q >> 1));
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            v4f d = v4f{0.f, 0.f, 0.f, 0.f};
+            if constexpr (TYPE == kTBf16)
+                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, h[e]),
+                                                            __builtin_bit_cast(v8bf, in[c]), d, 0, 0, 0);
+            else
+                d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, h[e]),
+                                                           __builtin_bit_cast(v8h, in[c]), d, 0, 0, 0);
+            // rows 16 e + 4 q .. + 3: neighbours within kNear, then segments
+            constexpr int kWide = kNear < 4 ? kNear : 4;
+            typedef float Piece __attribute__((ext_vector_type(kWide)));
+#pragma unroll
+            for (int r = 0; r < 4; r += kWide) {
+                const int out = e * 16 + q * 4 + r;
+                const int seg = out / kNear;
+                const int i = (place0 + c * 16 + l16) * kNear + out % kNear;
+                float* at = lds + seg * 1024 +
+                            (i ^ (((i >> 6) & 7) << 2) ^ (((seg ^ (seg >> 1)) & 1) << 5));
+                Piece w;
+#pragma unroll
+                for (int k = 0; k < kWide; ++k)
+                    w[k] = d[r + k];
+                *(Piece*)at = w;
+            }
+        }
+}
+
 template <int TYPE, int MODE, int BITS>
 __global__ __launch_bounds__(1 << (BITS - 5)) void long_kernel(const RotateArgs p, float norm)
 {
-    constexpr int kNear = 1 << (15 - BITS);     // neighbours of layout A
-    constexpr int kSegs = 1 << (BITS - 10);
     __shared__ __align__(16) float lds[1 << BITS];
     const int t = threadIdx.x;
     const int64_t per = p.k >> BITS;
@@ -256,38 +351,15 @@ __global__ __launch_bounds__(1 << (BITS - 5)) void long_kernel(const RotateArgs 
     }
     const int64_t row = w / per;
     const int64_t k0 = (w - row * per) << BITS;
-    const int64_t x0 = row * p.ldx + k0 + t * kNear;
     float v[32];
-    // kNear elements at one address
-    using Word = typename std::conditional<TYPE == kTF32, float, unsigned short>::type;
-    struct __attribute__((packed)) Near {
-        Word w[kNear];
-    };
-#pragma unroll
-    for (int g = 0; g < kSegs; ++g) {
-        const Near n = *(const Near*)((const Word*)p.x + x0 + g * 1024);
-#pragma unroll
-        for (int i = 0; i < kNear; ++i) {
-            if constexpr (TYPE == kTF32)
-                v[g * kNear + i] = n.w[i];
-            else
-                v[g * kNear + i] = from16(n.w[i], TYPE == kTBf16);
-        }
-    }
-    stages32<0, 5>(v);
-    typedef float v2f __attribute__((ext_vector_type(2)));
-    const int a0 = t * kNear, am = ((a0 >> 6) & 7) << 2;
-#pragma unroll
-    for (int i = 0; i < kNear; i += 2) {
-        float* const even = lds + ((a0 + i) ^ am);
-        float* const odd = lds + ((a0 + i) ^ am ^ 32);
-#pragma unroll
-        for (int g = 0; g < kSegs; ++g)
-            *(v2f*)((g & 1 ? odd : even) + g * 1024) = v2f{v[g * kNear + i], v[g * kNear + i + 1]};
-    }
+    if constexpr (TYPE != kTF32)
+        layout_a16<TYPE, BITS>((const unsigned short*)p.x + row * p.ldx + k0, lds, t);
+    else
+        layout_a32<BITS>((const float*)p.x + row * p.ldx + k0, lds, t);
     __syncthreads();
     // i = bit 5 (e), bits 6-8 (j), bit 9 (h): where bits 2-5 come out
-    const int b0 = (t >> 5) * 1024 + ((t & 31) ^ (t & 32));
+    const int odd = ((t >> 5) ^ (t >> 6)) & 1;
+    const int b0 = (t >> 5) * 1024 + ((t & 31) ^ (odd << 5));
     float* at[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j)
@@ -300,7 +372,7 @@ __global__ __launch_bounds__(1 << (BITS - 5)) void long_kernel(const RotateArgs 
     for (int i = 0; i < 32; ++i)
         at[i & 15][(i >> 4) * 512] = v[i];
     __syncthreads();
-    const float* const c0 = lds + ((t * 32) ^ (t & 32));
+    const float* const c0 = lds + ((t * 32) ^ (odd << 5));
     const int cm = ((t >> 1) & 7) << 2;
 #pragma unroll
     for (int i = 0; i < 32; i += 4) {
@@ -440,13 +512,13 @@ tile_t16_kernel(const RotateArgs p, float norm)
             lane_stage<4>(v, lane);
         if constexpr (BITS > 6)
             lane_stage<5>(v, lane);
-        unsigned m = 0;
+        float f = 0.0f;
 #pragma unroll
         for (int i = 0; i < 32; ++i) {
             v[i] *= norm;
-            const unsigned u = __float_as_uint(v[i]) & 0x7fffffffu;
-            m = m > u ? m : u;
+            f = __builtin_elementwise_maximum(f, __builtin_fabsf(v[i]));
         }
+        unsigned m = __float_as_uint(f) & 0x7fffffffu;
 #pragma unroll
         for (int d = 16; d < 64; d *= 2) {
             const unsigned o = (unsigned)__shfl_xor((int)m, d);

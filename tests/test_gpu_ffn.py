@@ -136,6 +136,41 @@ def test_rotate_of_activations(m, k, bits, transpose, scales, dtype):
     assert bool(((q.double() - r).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("bits", [0, 5, 7, 10, 11, 12, 13, 14])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rotate_keeps_subnormal_inputs(bits, dtype):
+    # Integers times the type's smallest magnitude: every sum is exact, so the
+    # 16-bit input and the same numbers in fp32 give the same bits.
+    say("rotate subnormal", bits, dtype)
+    x = torch.randint(-8, 9, (3, max(256, 1 << bits)), generator=gen(bits), device="cuda")
+    x = x.float() * 2.0 ** (-24 if dtype == "f16" else -133)
+    q, s = qse.rotate_quantize(x.to(DT[dtype]), bits=bits)
+    q2, s2 = qse.rotate_quantize(x, bits=bits)
+    assert torch.equal(x.to(DT[dtype]).float(), x)
+    assert torch.equal(s, s2) and torch.equal(q.float(), q2.float())
+    assert dtype == "bf16" or bool((q.float() != 0).any())
+
+
+@pytest.mark.parametrize("bits", [11, 12, 13, 14])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_long_rotations_of_views(bits, dtype):
+    # rows that begin at any even address, and a value that is not finite: it
+    # reaches its own rotation and no other
+    say("rotate views", bits, dtype)
+    k = 1 << bits
+    big = torch.randn(9, 2 * k + 7, generator=gen(bits), device="cuda").to(DT[dtype])
+    big[4, 3 + k + 77] = float("inf")
+    for lo in (0, 1, 3, 7):
+        view = big[:, lo:lo + 2 * k]
+        q, s = qse.rotate_quantize(view, bits=bits)
+        q2, s2 = qse.rotate_quantize(view.contiguous(), bits=bits)
+        assert torch.equal(q.view(torch.uint8), q2.view(torch.uint8))
+        assert torch.equal(torch.isnan(s), torch.isnan(s2))
+        bad = torch.isnan(q.float())
+        assert bool(bad[4, k:].all()) and not bool(bad[4, :k].any())
+        assert not bool(bad[[0, 1, 2, 3, 5, 6, 7, 8]].any())
+
+
 def test_rotate_strided_and_unaligned_inputs():
     say("rotate strided")
     g = gen(1)
