@@ -20,7 +20,9 @@
  * owns, on the calling thread's current device; the stream is one of that
  * device; all arguments are checked on the host before anything is enqueued
  * (FWT_EINVAL for a null pointer, a size or stride out of range, buffers
- * that overlap or are not device memory of the needed size); nothing is
+ * that are not device memory of the needed size, and one that is written
+ * and lies, from its first element to its last, across another's; inputs
+ * may be the same); nothing is
  * allocated and nothing synchronises, so every call may be captured into a
  * HIP graph.  Results do not depend on what else runs: sums have a fixed
  * order.  Strides are in elements, last dimensions are contiguous.  Sizes of
@@ -63,7 +65,9 @@ typedef enum { FWT_SILU = 0, FWT_GELU = 1 } fwt_activation;
  * The stages run in fp32, strides 1, 2, 4, ... within the 2^bits elements,
  * the factor after them: a sum past the fp32 range counts as not finite.
  * FWT_EALIGN: codes, ldcodes or ws misaligned; FWT_EINVAL: bits out of
- * range or k not a multiple of 2^bits. */
+ * range or k not a multiple of 2^bits; FWT_EUNSUPPORTED: 2^29 blocks of 128
+ * or more, or of a transposed input or with tile scales more than 65535 * 128
+ * rows or 2^22 blocks in one. */
 int fwt_rotate_quantize_workspace(int64_t m, int64_t k, int bits, fwt_scales scales,
                                   int transposed, size_t* bytes);
 int fwt_rotate_quantize(const void* x, fwt_ffn_dtype dtype, int64_t m, int64_t k, int64_t ldx,
@@ -79,7 +83,8 @@ int fwt_rotate_quantize(const void* x, fwt_ffn_dtype dtype, int64_t m, int64_t k
  * which keeps all of it, at half the rate.  A row of a
  * or b is read up to k only, whatever its padding holds.  The strides lda
  * and ldb are multiples of 16 below 2^23, a and b 16-byte aligned
- * (FWT_EALIGN; a longer stride FWT_EUNSUPPORTED).
+ * (FWT_EALIGN; a longer stride, or more than 2^22 tiles of 128 x 64 results,
+ * FWT_EUNSUPPORTED).
  *  ws          scratch of fwt_scaled_matmul_workspace bytes (0 for most
  *              sizes), 16-byte aligned, one for each call that may run at the
  *              same time: a long contraction with few results is then shared
@@ -96,7 +101,7 @@ int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const v
 /* h = act(x gate^T) * (x up^T): x is m x k, gate and up n x k, of one
  * dtype.  bf16 and f16: h has the same dtype, the scales are NULL; any
  * alignment (operands whose addresses and strides are multiples of 16 bytes
- * are read faster).  e4m3: x_scales row scales, gate_scales and up_scales
+ * are read faster) and strides below 2^22.  e4m3: x_scales row scales, gate_scales and up_scales
  * tile scales, alignment as for fwt_scaled_matmul, h bf16, f16 or fp32.
  * Both products are summed as fwt_scaled_matmul sums them, in 32 bits, and
  * only h is rounded.  ws: as there, of fwt_gated_ffn_workspace bytes. */
@@ -113,7 +118,8 @@ int fwt_gated_ffn(const void* x, int64_t ldx, const float* x_scales, const void*
  *   dg = dh * up' * act'(g),  du = dh * act(g),  g = x gate^T, up' = x up^T.
  * g and up' are computed again in 32 bits, not stored by the forward pass;
  * dg and du are rounded to the dtype for the matrix products.  All arrays
- * have the dtype.  ws: scratch of fwt_gated_ffn_backward_workspace bytes,
+ * have the dtype; ldx, ldgate and ldup are below 2^22, n below 2^21 and the
+ * three products have fewer than 2^22 tiles (FWT_EUNSUPPORTED).  ws: scratch of fwt_gated_ffn_backward_workspace bytes,
  * 16-byte aligned, one for each call that may run at the same time. */
 int fwt_gated_ffn_backward_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);
 int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t ldgate,

@@ -35,15 +35,26 @@ struct Array {
 
 constexpr int64_t kMaxDim = (int64_t)1 << 30;
 
-// The array must have a sane stride and lie in one device allocation.
-int check_array(const Array& a)
+// Whether a product has too many tiles of 128 x 64 for one launch (larger and
+// smaller tiles are chosen where theirs fit).
+bool too_many(int64_t m, int64_t n)
+{
+    return ((m + 127) / 128) * ((n + 63) / 64) >= qse::kFfnMaxTiles;
+}
+
+// The array must have a sane stride, ...
+int check_stride(const Array& a)
 {
     if (!a.p || a.ld < a.cols)
         return FWT_EINVAL;
     if (a.ld > ((int64_t)1 << 40) || (a.rows > 1 && a.ld > INT64_MAX / 8 / a.rows))
         return FWT_EINVAL;
-    if ((uintptr_t)a.p & (uintptr_t)(a.size - 1))
-        return FWT_EALIGN;
+    return (uintptr_t)a.p & (uintptr_t)(a.size - 1) ? FWT_EALIGN : FWT_OK;
+}
+
+// ... and lie in one device allocation.
+int check_memory(const Array& a)
+{
     hipDeviceptr_t base = nullptr;
     size_t size = 0;
     const hipError_t e = hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)a.p);
@@ -67,20 +78,23 @@ bool overlap(const Array& a, const Array& b)
     return x < y + b.span() && y < x + a.span();
 }
 
-// Every array on its own, and what is written against all others; then the
-// stream.
+// Every array's stride, what is written against all others, the memory; then
+// the stream.  (size 0: an array that this call does not have)
 template <int N>
 int check_call(const Array (&arrays)[N], hipStream_t stream)
 {
+    for (const Array& a : arrays) {
+        const int rc = a.size ? check_stride(a) : FWT_OK;
+        if (rc != FWT_OK)
+            return rc;
+    }
     for (const Array& a : arrays)
-        if (a.p && a.written)
+        if (a.size && a.written)
             for (const Array& b : arrays)
-                if (&a != &b && b.p && overlap(a, b))
+                if (&a != &b && b.size && overlap(a, b))
                     return FWT_EINVAL;
     for (const Array& a : arrays) {
-        if (a.size == 0)
-            continue;   // an array that this call does not have
-        const int rc = check_array(a);
+        const int rc = a.size ? check_memory(a) : FWT_OK;
         if (rc != FWT_OK)
             return rc;
     }
@@ -172,12 +186,14 @@ int fwt_rotate_quantize(const void* x, fwt_ffn_dtype dtype, int64_t m, int64_t k
         return FWT_EINVAL;
     if (m == 0)
         return FWT_OK;
+    const bool tile = scales == FWT_SCALES_TILE;
     if (!x || !codes || !s || (need && (!ws || ws_bytes < need)))
         return FWT_EINVAL;
     if (!aligned16(codes, ldcodes) || (need && !aligned16(ws, 0)))
         return FWT_EALIGN;
-    const bool tile = scales == FWT_SCALES_TILE;
-    if (blocks(m) > 65535 || m * blocks(k) / 32 >= ((int64_t)1 << 30))
+    // threads of a launch: 8 a block, or 1024 for 128 rows of one
+    if (m * blocks(k) >= ((int64_t)1 << 29) ||
+        ((tile || transposed) && (blocks(m) > 65535 || blocks(k) >= ((int64_t)1 << 22))))
         return FWT_EUNSUPPORTED;
     const Array arrays[] = {
         {x, transposed ? k : m, transposed ? m : k, ldx, size_of(dtype), false},
@@ -234,7 +250,7 @@ int fwt_scaled_matmul(const void* a, int64_t lda, const float* a_scales, const v
         return FWT_EINVAL;
     if (!aligned16(a, lda) || !aligned16(b, ldb))
         return FWT_EALIGN;
-    if (lda >= qse::kFfnMaxStride || ldb >= qse::kFfnMaxStride)
+    if (lda >= qse::kFfnMaxStride || ldb >= qse::kFfnMaxStride || too_many(m, n))
         return FWT_EUNSUPPORTED;
     const int64_t sbn = b_kind == FWT_SCALES_ROW ? n : blocks(n);
     const Array arrays[] = {
@@ -307,7 +323,7 @@ int fwt_gated_ffn(const void* x, int64_t ldx, const float* x_scales, const void*
     if (f8 && (!aligned16(x, ldx) || !aligned16(gate, ldgate) || !aligned16(up, ldup)))
         return FWT_EALIGN;
     if (ldx * sz >= qse::kFfnMaxStride || ldgate * sz >= qse::kFfnMaxStride ||
-        ldup * sz >= qse::kFfnMaxStride)
+        ldup * sz >= qse::kFfnMaxStride || too_many(m, n))
         return FWT_EUNSUPPORTED;
     const Array arrays[] = {
         {x, m, k, ldx, sz, false},
@@ -376,7 +392,8 @@ int fwt_gated_ffn_backward(const void* x, int64_t ldx, const void* gate, int64_t
     if (sums && !aligned16(ws, 0))
         return FWT_EALIGN;
     if (ldx * 2 >= qse::kFfnMaxStride || ldgate * 2 >= qse::kFfnMaxStride ||
-        ldup * 2 >= qse::kFfnMaxStride || pad8(n) * 4 >= qse::kFfnMaxStride)
+        ldup * 2 >= qse::kFfnMaxStride || pad8(n) * 4 >= qse::kFfnMaxStride ||
+        too_many(m, n) || too_many(m, k) || too_many(2 * pad8(n), k))
         return FWT_EUNSUPPORTED;
     const Array arrays[] = {
         sums ? Array{x, m, k, ldx, 2, false} : kNone,

@@ -20,6 +20,10 @@ enum FfnType : int { kTBf16 = 0, kTF16 = 1, kTF32 = 2, kTE4m3 = 3, kTE4m3Exact =
 // stay within a 32-bit offset of its first one.
 constexpr int64_t kFfnMaxStride = (int64_t)1 << 23;
 
+// Workgroups of a launch stay below this: of at most 1024 threads each,
+// they have fewer than 2^32 threads, which is a launch's limit.
+constexpr int64_t kFfnMaxTiles = (int64_t)1 << 22;
+
 // What a product's epilogue does with its accumulators.
 enum FfnEpilogue : int {
     kEpStore = 0,     // C = A B^T; 16-bit operands: with B stored [k][n]

@@ -711,7 +711,9 @@ Choice cheapest(const Tile (&tiles)[N], const ProductArgs& p)
     for (int i = 0; i < N; ++i) {
         const Tile& t = tiles[i];
         const int64_t count = ((p.m + t.bm - 1) / t.bm) * ((p.n + t.bn - 1) / t.bn);
-        double cost = (double)((count + t.slots - 1) / t.slots) * t.step * steps;
+        double cost = count >= kFfnMaxTiles
+                          ? 1e300
+                          : (double)((count + t.slots - 1) / t.slots) * t.step * steps;
         int splits = 1;
         if (t.area && p.may_split && count * 2 <= t.slots) {
             int64_t s = t.slots / count < 16 ? t.slots / count : 16;
@@ -870,7 +872,7 @@ bool strips(const ProductArgs& p, int type, int ep)
     if (p.m > kStripRows || ep == kEpGateGrad || (ep != kEpGate && type != kTE4m3))
         return false;
     const bool fills = (p.n + 63) / 64 >= 256;
-    return !fills || (ep == kEpGate && p.m <= 16);
+    return !fills || (ep == kEpGate && p.m <= 16 && (p.n + 15) / 16 < kFfnMaxTiles);
 }
 
 }  // namespace

@@ -205,8 +205,9 @@ __global__ __launch_bounds__(256) void rows_kernel(const RotateArgs p, float nor
     // maxima has read last and the last-level cache may hold (4096 x 16384
     // fp32, b = 10, tile scales: 117 us from the front, 112 from the end).
     const int64_t wg = MODE == kTileGiven ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-    const int64_t g = (wg * 256 + threadIdx.x) >> 3;
-    const int64_t row = g / kbs, kb = g - row * kbs;
+    const unsigned g = (unsigned)(wg * 32 + (threadIdx.x >> 3));   // (at most 2^29)
+    const unsigned r = g / (unsigned)kbs;
+    const int64_t row = r, kb = g - r * (unsigned)kbs;
     const bool live = row < p.m;
     const int64_t k0 = kb * kFfnBlock + (lane & 7) * 16;
     const int left = live ? (int)(p.k - k0 < 16 ? p.k - k0 : 16) : 0;

@@ -14,6 +14,7 @@ Example (one feed-forward block of a served model; weights prepared once)::
 """
 import contextlib
 import ctypes
+import operator
 
 import quantum_state_encoding_amd as _qse
 
@@ -171,11 +172,14 @@ def rotate_quantize(x, bits=0, scales="row", transpose=False, stream=None):
     lib = _lib or _load()
     if scales not in _SCALES:
         raise ValueError("scales must be 'row' or 'tile'")
+    bits = operator.index(bits)
+    if not 0 <= bits <= ROTATE_MAX_BITS:
+        _raise(_qse.FWT_EINVAL, "rotate_quantize: bits %d" % bits)
     dev = _current()
     m, k, ld = _matrix(x, "x", _floats, dev)
     if transpose:
         m, k = k, m
-    kind, bits, t = _SCALES[scales], int(bits), 1 if transpose else 0
+    kind, t = _SCALES[scales], 1 if transpose else 0
     need = 0
     if kind and bits > ROTATE_MAX_BITS_T:
         size = ctypes.c_size_t(0)

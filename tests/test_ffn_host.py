@@ -47,6 +47,13 @@ def test_rotate_refusals(L):
         assert rotate(L, **bad) == EINVAL, bad
     for bad in (dict(q=P + 8), dict(ldq=264), dict(bits=8, scales=1, ws=P + 4, wsb=1 << 20)):
         assert rotate(L, **bad) == EALIGN, bad
+    far = dict(x=1 << 40, q=1 << 42, s=1 << 44)
+    for bad in (dict(m=1 << 29, k=128, ldx=128, ldq=128), dict(m=1 << 20, k=1 << 16, bits=0),
+                dict(m=(65535 * 128) + 1, scales=1), dict(m=(65535 * 128) + 1, t=1, ldx=1 << 30),
+                dict(m=1, k=1 << 29, scales=1)):
+        assert rotate(L, **dict(far, **bad)) == EUNSUPPORTED, bad
+    for ldx in (-1, 255, (1 << 40) + 1, (1 << 63) - 1, -(1 << 63)):
+        assert rotate(L, **dict(far, ldx=ldx)) == EINVAL
     # written arrays that overlap, or overlap what is read
     assert rotate(L, q=P, s=P + 64) == EINVAL
     assert rotate(L, x=P, q=P) == EINVAL
@@ -83,6 +90,12 @@ def test_matmul_refusals(L):
         assert matmul(L, **bad) == EALIGN, bad
     assert matmul(L, lda=1 << 23) == EUNSUPPORTED
     assert matmul(L, ldb=1 << 23) == EUNSUPPORTED
+    assert matmul(L, m=1 << 20, n=1 << 15, ldc=1 << 15) == EUNSUPPORTED
+    assert matmul(L, m=1 << 29, n=1) == EUNSUPPORTED
+    for ld in (-16, 240, -(1 << 63)):
+        assert matmul(L, lda=ld) == EINVAL
+    for ld in (7, -8, (1 << 63) - 1):
+        assert matmul(L, ldc=ld) == EINVAL
 
 
 def gated(L, x=P, ldx=64, xs=None, g=2 * P, ldg=64, gs=None, u=3 * P, ldu=64, us=None,
@@ -103,6 +116,7 @@ def test_gated_refusals(L):
     assert gated(L, **dict(f8, ldu=72)) == EALIGN
     assert gated(L, ldx=1 << 22) == EUNSUPPORTED
     assert gated(L, ldg=1 << 22) == EUNSUPPORTED
+    assert gated(L, m=1 << 20, n=1 << 15, ldh=1 << 15) == EUNSUPPORTED
 
 
 def backward(L, x=P, ldx=64, g=2 * P, ldg=64, u=3 * P, ldu=64, dh=4 * P, lddh=8, dtype=BF16,
@@ -121,6 +135,8 @@ def test_backward_refusals(L):
         assert backward(L, **bad) == EINVAL, bad
     assert backward(L, ws=8 * P + 8) == EALIGN
     assert backward(L, ldx=1 << 22) == EUNSUPPORTED
+    assert backward(L, m=1 << 20, k=1 << 15, ldx=1 << 15, wsb=1 << 40) == EUNSUPPORTED
+    assert backward(L, n=1 << 21, wsb=1 << 40) == EUNSUPPORTED
     out = ctypes.c_size_t()
     assert L.fwt_gated_ffn_backward_workspace(4, 8, 64, ctypes.byref(out)) == OK
     assert out.value > 0 and out.value % 2 == 0
@@ -177,3 +193,8 @@ def test_host_tensors_are_refused(L):
         qse.scaled_matmul(q, torch.zeros(1, 4), q, torch.zeros(1, 4))
     with pytest.raises(ValueError):
         qse.rotate_quantize(x, scales="column")
+    for bits in (-1, 15, 1 << 32, (1 << 32) + 3):     # (no wrap to a valid number)
+        with pytest.raises(qse.FwtError):
+            qse.rotate_quantize(x, bits=bits)
+    with pytest.raises(TypeError):
+        qse.rotate_quantize(x, bits=2.5)

@@ -590,6 +590,30 @@ def test_block_together(m, k, n, bits_in, bits_mid):
     assert bool(((h.double() - f * u).abs() <= tol).all())
 
 
+@pytest.mark.parametrize("m,n,k", [(300, 200, 16000), (64, 130, 8016)])
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+def test_without_scratch_a_contraction_is_not_shared(m, n, k, out):
+    # Integers below 4 and scales that are powers of two: every sum is exact
+    # (below 16 k < 2^18), so the shared contraction, the one in one piece
+    # (no workspace at the C entry point) and the 64-bit product agree in
+    # fp32, and after one rounding in bf16.
+    say("no scratch", m, n, k, out)
+    g = gen(m + n)
+    a, b = (torch.randint(-4, 5, (r, k), generator=g, device="cuda").float().to(F8)
+            for r in (m, n))
+    sa = torch.full((-(-k // BLOCK), m), 0.5, device="cuda")
+    sb = torch.full((-(-k // BLOCK), n), 2.0, device="cuda")
+    want = (a.double() @ b.double().t()).float().to(DT[out])
+    assert torch.equal(qse.scaled_matmul(a, sa, b, sb, out_dtype=DT[out]), want)
+    c = torch.zeros(m, n, dtype=DT[out], device="cuda")
+    lib = qse.ffn._load()
+    status = lib.fwt_scaled_matmul(a.data_ptr(), k, sa.data_ptr(), b.data_ptr(), k, sb.data_ptr(),
+                                   0, m, n, k, c.data_ptr(), {"bf16": 0, "f32": 2}[out], n, None,
+                                   0, torch.cuda.current_stream().cuda_stream)
+    assert status == 0
+    assert torch.equal(c, want)
+
+
 def test_side_stream_and_two_streams_at_once():
     say("streams")
     g = gen(21)
