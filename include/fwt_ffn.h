@@ -62,8 +62,8 @@ typedef enum { FWT_SILU = 0, FWT_GELU = 1 } fwt_activation;
  *  ws          scratch of fwt_rotate_quantize_workspace bytes (0 except for
  *              tile scales with bits > 7), 16-byte aligned; two calls that
  *              may run at the same time need one each.
- * The stages run in fp32, strides 1, 2, 4, ... within the 2^bits elements,
- * the factor after them: a sum past the fp32 range counts as not finite.
+ * Sums are in fp32, in an order that dtype and bits fix, the factor comes
+ * after them: a sum past the fp32 range counts as not finite.
  * FWT_EALIGN: codes, ldcodes or ws misaligned; FWT_EINVAL: bits out of
  * range or k not a multiple of 2^bits; FWT_EUNSUPPORTED: 2^29 blocks of 128
  * or more, or of a transposed input or with tile scales more than 65535 * 128

@@ -5,11 +5,19 @@
 // s = max(max |y| / 448, 2^-126), q = e4m3(y / s), rounded to nearest even.
 // A block with a value that is not finite gets a NaN scale and NaN codes.
 //
-// Layout: 8 consecutive lanes hold a block of 128, each 16 consecutive
-// elements.  So bits 0-3 of a rotation are register stages, bits 4-6 cross
-// the 8 lanes, bits 7-9 the 8 blocks of a wave, and bits 10-13 the waves of a
-// workgroup (through LDS); the block's maximum is three lane steps, and a
-// lane stores its 16 codes at once.
+// It is a pass over memory: what is read and written takes 0.2 us a MB at a large
+// copy's rate (5.15 TB/s), and the add/subtract stages have to stay under that.  A stage
+// on register bits costs a vector instruction an element, one across lanes
+// two and more, and the first five of a 16-bit input nothing on the matrix
+// cores (H_32, +-1).  So there is a kernel for each way to lay out 2^b:
+//   rows_kernel      b <= 10 (16 bits: <= 7): 16 elements a lane, 8 lanes a
+//                    block: bits 0-3 in registers, the others across lanes
+//   mid_kernel       16 bits, b = 8 .. 10: matrix cores, registers
+//   long_kernel      b = 11 .. 14: three layouts with LDS between them
+//   tile_kernel      b <= 7, tile scales or transposed fp32: a 128 x 128 tile
+//   tile_t16_kernel  b <= 7, transposed 16 bits
+// Tile scales of longer rotations need two passes: a 128-row tile of 2^b
+// columns does not fit a CU, so the blocks' maxima are found first.
 #include <hip/hip_runtime.h>
 
 #include "ffn_device.h"
@@ -275,9 +283,39 @@ __device__ __forceinline__ void layout_a32(const float* x, float* lds, int t)
     }
 }
 
-// The same for 16-bit inputs: 16 places at a time, the second operand's lane
-// (q, l) holds inputs 8 q .. 8 q + 7 of place l, the first one's those of row l
-// (and 16 + l) of H_32: (-1)^popcount(row AND input).
+// H_32 as the first operand of two 16-bit matrix instructions (rows 0 .. 15 and
+// 16 .. 31): lane (q, l) holds inputs 8 q .. 8 q + 7 of row l (and 16 + l),
+// (-1)^popcount(row AND input).  Products by +-1 are exact, sums are fp32.
+template <int TYPE>
+__device__ __forceinline__ void hadamard32(int lane, v4i (&h)[2])
+{
+    const int q = lane >> 4, l16 = lane & 15;
+    // signs of two inputs at a time: bits 0-2 of the input are in the word
+    const unsigned one = TYPE == kTBf16 ? 0x3f803f80u : 0x3c003c00u;
+    const auto sign = [](int bit) { return bit ? 0x80008000u : 0u; };
+    const unsigned w0 = one ^ sign((l16 >> 3) & q & 1) ^ (l16 & 1 ? 0x80000000u : 0u);
+    const unsigned s1 = sign(l16 & 2), s2 = sign(l16 & 4);
+    h[0] = v4i{(int)w0, (int)(w0 ^ s1), (int)(w0 ^ s2), (int)(w0 ^ s1 ^ s2)};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        h[1][i] = (int)((unsigned)h[0][i] ^ sign(q >> 1));
+}
+
+// Their products with 32 inputs of 16 places: lane (q, l) holds inputs 8 q ..
+// of place l, and gets rows 4 q .. 4 q + 3 of it.
+template <int TYPE>
+__device__ __forceinline__ v4f times(v4i h, v4i in)
+{
+    const v4f zero = v4f{0.f, 0.f, 0.f, 0.f};
+    if constexpr (TYPE == kTBf16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, h),
+                                                       __builtin_bit_cast(v8bf, in), zero, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, h),
+                                                      __builtin_bit_cast(v8h, in), zero, 0, 0, 0);
+}
+
+// The same for 16-bit inputs, 16 places at a time.
 template <int TYPE, int BITS>
 __device__ __forceinline__ void layout_a16(const unsigned short* x, float* lds, int t)
 {
@@ -300,27 +338,13 @@ __device__ __forceinline__ void layout_a16(const unsigned short* x, float* lds, 
             all.r[r] = *(const Run*)(at + r * 1024);
         in[c] = __builtin_bit_cast(v4i, all);
     }
-    // signs of two inputs at a time: bits 0-2 of the input are in the word
-    const unsigned one = TYPE == kTBf16 ? 0x3f803f80u : 0x3c003c00u;
-    const auto sign = [](int bit) { return bit ? 0x80008000u : 0u; };
-    const unsigned w0 = one ^ sign((l16 >> 3) & q & 1) ^ (l16 & 1 ? 0x80000000u : 0u);
-    const unsigned s1 = sign(l16 & 2), s2 = sign(l16 & 4);
     v4i h[2];
-    h[0] = v4i{(int)w0, (int)(w0 ^ s1), (int)(w0 ^ s2), (int)(w0 ^ s1 ^ s2)};
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-        h[1][i] = (int)((unsigned)h[0][i] ^ sign(q >> 1));
+    hadamard32<TYPE>(lane, h);
 #pragma unroll
     for (int c = 0; c < 4; ++c)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-            v4f d = v4f{0.f, 0.f, 0.f, 0.f};
-            if constexpr (TYPE == kTBf16)
-                d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, h[e]),
-                                                            __builtin_bit_cast(v8bf, in[c]), d, 0, 0, 0);
-            else
-                d = __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, h[e]),
-                                                           __builtin_bit_cast(v8h, in[c]), d, 0, 0, 0);
+            const v4f d = times<TYPE>(h[e], in[c]);
             // rows 16 e + 4 q .. + 3: neighbours within kNear, then segments
             constexpr int kWide = kNear < 4 ? kNear : 4;
             typedef float Piece __attribute__((ext_vector_type(kWide)));
@@ -338,6 +362,100 @@ __device__ __forceinline__ void layout_a16(const unsigned short* x, float* lds, 
                 *(Piece*)at = w;
             }
         }
+}
+
+// Layout B, N stages from bit 5, in place.
+template <int N>
+__device__ __forceinline__ void layout_b(float* lds, int t)
+{
+    float v[32];
+    // i = bit 5 (e), bits 6-8 (j), bit 9 (h): where bits 2-5 come out
+    const int odd = ((t >> 5) ^ (t >> 6)) & 1;
+    const int b0 = (t >> 5) * 1024 + ((t & 31) ^ (odd << 5));
+    float* at[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j)
+        at[j] = lds + (b0 ^ ((j >> 1) << 2) ^ ((j & 1) << 5)) + (j >> 1) * 64;
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        v[i] = at[i & 15][(i >> 4) * 512];
+    stages32<0, N>(v);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+        at[i & 15][(i >> 4) * 512] = v[i];
+}
+
+// Layout C, from LDS to registers.
+__device__ __forceinline__ void layout_c(const float* lds, int t, float (&v)[32])
+{
+    const int odd = ((t >> 5) ^ (t >> 6)) & 1;
+    const float* const c0 = lds + ((t * 32) ^ (odd << 5));
+    const int cm = ((t >> 1) & 7) << 2;
+#pragma unroll
+    for (int i = 0; i < 32; i += 4) {
+        const v4f c = *(const v4f*)(c0 + (i ^ cm));
+        v[i] = c[0];
+        v[i + 1] = c[1];
+        v[i + 2] = c[2];
+        v[i + 3] = c[3];
+    }
+}
+
+// Rotations of 2^8 to 2^10 of 16-bit inputs: a wave takes 2048 elements, 2^(11-b)
+// rotations in the order of the rows.  Bits 0-4 are the matrix cores' H_32
+// (32 neighbours are a place), the others layout B's register stages, and
+// layout C hands a lane its quarter of a block.  What it saves are lane
+// stages: 8192 x 4096 bf16, b = 10, takes 29.4 us with lane stages and 19.5
+// here, where its bytes take 19.7 at a large copy's rate.
+template <int TYPE, int MODE, int BITS>
+__global__ __launch_bounds__(64) void mid_kernel(const RotateArgs p, float norm)
+{
+    constexpr int kUnits = 2048 >> BITS;
+    __shared__ __align__(16) float lds[2048];
+    const int t = threadIdx.x, q = t >> 4, l16 = t & 15;
+    const unsigned per = (unsigned)(p.k >> BITS);
+    const unsigned w = MODE == kTileGiven ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
+    const unsigned u0 = w * (unsigned)kUnits;
+    const unsigned row0 = u0 / per, rem = u0 - row0 * per;
+    // row and first column of rotation u0 + d
+    const auto unit = [=](unsigned d, int64_t& row, int64_t& k0) __attribute__((always_inline)) {
+        const unsigned v = rem + d;
+        const unsigned more = per >= kUnits ? (v >= per ? 1u : 0u) : v / per;
+        row = row0 + more;
+        k0 = (int64_t)(v - more * per) << BITS;
+        return row < p.m;
+    };
+    struct __attribute__((packed)) Any {
+        v4i w;
+    };
+    v4i in[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int i = (c * 16 + l16) * 32 + q * 8;
+        int64_t row, k0;
+        unit((unsigned)i >> BITS, row, k0);
+        row = row < p.m ? row : p.m - 1;     // past the last: any that is there
+        in[c] = ((const Any*)((const unsigned short*)p.x + row * p.ldx + k0 +
+                              (i & ((1 << BITS) - 1))))->w;
+    }
+    v4i h[2];
+    hadamard32<TYPE>(t, h);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const int i = (c * 16 + l16) * 32 + e * 16 + q * 4;
+            *(v4f*)(lds + (i ^ (((i >> 6) & 7) << 2) ^ ((c >> 1) << 5))) = times<TYPE>(h[e], in[c]);
+        }
+    __syncthreads();
+    layout_b<BITS - 5>(lds, t);
+    __syncthreads();
+    float v[32];
+    layout_c(lds, t, v);
+    int64_t row, k0;
+    const bool live = unit((unsigned)(t * 32) >> BITS, row, k0);
+    k0 += t * 32 & ((1 << BITS) - 1);
+    finish<MODE>(p, v, norm, !(BITS & 1), row, k0 / kFfnBlock, t & 3, live);
 }
 
 template <int TYPE, int MODE, int BITS>
@@ -363,31 +481,9 @@ __global__ __launch_bounds__(1 << (BITS - 5)) void long_kernel(const RotateArgs 
     else
         layout_a32<BITS>((const float*)p.x + row * p.ldx + k0, lds, t);
     __syncthreads();
-    // i = bit 5 (e), bits 6-8 (j), bit 9 (h): where bits 2-5 come out
-    const int odd = ((t >> 5) ^ (t >> 6)) & 1;
-    const int b0 = (t >> 5) * 1024 + ((t & 31) ^ (odd << 5));
-    float* at[16];
-#pragma unroll
-    for (int j = 0; j < 16; ++j)
-        at[j] = lds + (b0 ^ ((j >> 1) << 2) ^ ((j & 1) << 5)) + (j >> 1) * 64;
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = at[i & 15][(i >> 4) * 512];
-    stages32<0, 5>(v);
-#pragma unroll
-    for (int i = 0; i < 32; ++i)
-        at[i & 15][(i >> 4) * 512] = v[i];
+    layout_b<5>(lds, t);
     __syncthreads();
-    const float* const c0 = lds + ((t * 32) ^ (odd << 5));
-    const int cm = ((t >> 1) & 7) << 2;
-#pragma unroll
-    for (int i = 0; i < 32; i += 4) {
-        const v4f c = *(const v4f*)(c0 + (i ^ cm));
-        v[i] = c[0];
-        v[i + 1] = c[1];
-        v[i + 2] = c[2];
-        v[i + 3] = c[3];
-    }
+    layout_c(lds, t, v);
     stages32<15 - BITS, 5>(v);
     finish<MODE>(p, v, norm, !(BITS & 1), row, k0 / kFfnBlock + (t >> 2), t & 3, true);
 }
@@ -600,9 +696,26 @@ template <int TYPE, int MODE>
 hipError_t rows(const RotateArgs& p, float norm, hipStream_t stream)
 {
     const int64_t kbs = (p.k + kFfnBlock - 1) / kFfnBlock;
+    if constexpr (TYPE != kTF32) {
+        const int64_t rotations = p.m * (p.k >> p.bits);
+        const dim3 grid((unsigned)(((rotations << p.bits) + 2047) / 2048));
+        switch (p.bits) {
+        case 8:
+            hipLaunchKernelGGL((mid_kernel<TYPE, MODE, 8>), grid, dim3(64), 0, stream, p, norm);
+            return hipGetLastError();
+        case 9:
+            hipLaunchKernelGGL((mid_kernel<TYPE, MODE, 9>), grid, dim3(64), 0, stream, p, norm);
+            return hipGetLastError();
+        case 10:
+            hipLaunchKernelGGL((mid_kernel<TYPE, MODE, 10>), grid, dim3(64), 0, stream, p, norm);
+            return hipGetLastError();
+        }
+    }
     if (p.bits <= 10) {
-        hipLaunchKernelGGL((rows_kernel<TYPE, MODE>), dim3((unsigned)((p.m * kbs + 31) / 32)),
-                           dim3(256), 0, stream, p, norm);
+        if constexpr (TYPE == kTF32 || MODE == kRowScales) {   // (else bits is above 7)
+            hipLaunchKernelGGL((rows_kernel<TYPE, MODE>), dim3((unsigned)((p.m * kbs + 31) / 32)),
+                               dim3(256), 0, stream, p, norm);
+        }
     } else {
         const dim3 grid((unsigned)(p.m * (p.k >> p.bits)));
         const dim3 block(1u << (p.bits - 5));

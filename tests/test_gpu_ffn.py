@@ -74,6 +74,9 @@ ROTATE = [  # m, k, bits, transpose
     (1, 128, 7, True), (130, 256, 7, True), (37, 100, 2, True), (257, 33, 0, True),
     (64, 192, 6, True), (5, 1, 0, True), (128, 96, 5, True), (200, 304, 4, True),
     (1000, 24, 3, True), (130, 4096, 12, False), (129, 32768, 14, False),
+    # rotations that end inside a wave's 2048 elements, in rows of one to many
+    (1, 256, 8, False), (5, 4352, 8, False), (77, 512, 9, False), (9, 6656, 9, False),
+    (6, 11264, 10, False), (300, 256, 8, False),
 ]
 
 
