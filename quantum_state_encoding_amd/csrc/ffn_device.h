@@ -158,9 +158,9 @@ __device__ __forceinline__ void store4(void* c, int64_t at, v4f v, int type, int
 }
 
 // Four 16-bit values from p[at ..], 0 past cnt.
-__device__ __forceinline__ v4f load4(const void* p, int64_t at, bool bf, int cnt)
+typedef unsigned short v4h __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ v4h load4(const void* p, int64_t at, int cnt)
 {
-    typedef unsigned short v4h __attribute__((ext_vector_type(4)));
     struct __attribute__((packed)) Any {
         v4h v;
     };
@@ -174,7 +174,7 @@ __device__ __forceinline__ v4f load4(const void* p, int64_t at, bool bf, int cnt
             if (k < cnt)
                 h[k] = s[k];
     }
-    return v4f{from16(h[0], bf), from16(h[1], bf), from16(h[2], bf), from16(h[3], bf)};
+    return h;
 }
 
 // act(g) and its derivative in 32 bits.  silu: g s and s (1 + g (1 - s))

@@ -125,22 +125,53 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 // From a tile's sums to results: lane l holds rows l % 16 * TM .. of A (AT:
 // every 16th from l % 16) and four consecutive rows of B, stored at once.
 // acc: rows i0, i0 + 1, .. of the wave's BM / WM / 16.
-template <int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN>
-__device__ __forceinline__ void finish_rows(const ProductArgs& p, const v4f (&acc)[NI][TN], int i0,
-                                            int tm, int tn, int wave, int lane)
+//
+// A tile runs this once, as straight code, and its time is mostly that of
+// fetching the code: so a whole tile has a path of its own without bounds, and
+// each activation too (EPIGAIN).
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN, int ACT,
+          bool WHOLE>
+__device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (&acc)[NI][TN],
+                                               int i0, int tm, int tn, int wave, int lane)
 {
     constexpr int TM = BM / WM / 16;
     constexpr bool kDual = EP != kEpStore;
-    constexpr int BNO = kDual ? BN / 2 : BN, kRowsB = BNO / WN;
+    constexpr int BNO = kDual ? BN / 2 : BN, kRowsB = BNO / WN, TJ = kDual ? TN / 2 : TN;
     const int wm = wave / WN, wn = wave % WN, q = lane >> 4, l16 = lane & 15;
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNO;
-    const int mrows = (int)(p.m - m0 < BM ? p.m - m0 : BM);
-    const int nrows = (int)(p.n - n0 < BNO ? p.n - n0 : BNO);
-    const bool bf = p.ctype == kTBf16;
+    const int mrows = WHOLE || p.m - m0 > BM ? BM : (int)(p.m - m0);
+    const int nrows = WHOLE || p.n - n0 > BNO ? BNO : (int)(p.n - n0);
+    const int ctype = TYPE == kTE4m3Exact ? (int)kTF32
+                      : TYPE != kTE4m3    ? TYPE
+                      : p.ctype == kTBf16 ? (int)kTBf16
+                                          : (int)kTF16;
+    const int act = ACT < 0 ? p.act : ACT;
+    const auto row_at = [=](int i) __attribute__((always_inline)) {
+        return wm * (TM * 16) + (AT ? (i0 + i) * 16 + l16 : l16 * TM + i0 + i);
+    };
+    const auto column_at = [=](int j) __attribute__((always_inline)) {
+        return wn * kRowsB + j * 16 + q * 4;
+    };
+    const auto count_at = [=](int nc) __attribute__((always_inline)) {
+        return WHOLE || nrows - nc > 4 ? 4 : nrows - nc;
+    };
+    // All of dh before the first store (a load behind a store that may be to
+    // the same address waits for memory each time).
+    v4h dh[EP == kEpGateGrad ? NI : 1][TJ];
+    if constexpr (EP == kEpGateGrad) {
+#pragma unroll
+        for (int i = 0; i < NI; ++i)
+#pragma unroll
+            for (int j = 0; j < TJ; ++j) {
+                const int r = WHOLE || row_at(i) < mrows ? row_at(i) : mrows - 1;
+                const int nc = column_at(j);
+                dh[i][j] = load4(p.dh, (m0 + r) * p.lddh + n0 + nc, count_at(nc));
+            }
+    }
 #pragma unroll
     for (int i = 0; i < NI; ++i) {
-        const int r = wm * (TM * 16) + (AT ? (i0 + i) * 16 + l16 : l16 * TM + i0 + i);
-        if (r >= mrows)
+        const int r = row_at(i);
+        if (!WHOLE && r >= mrows)
             continue;
         int64_t m = m0 + r;
         void* c = p.c;
@@ -155,34 +186,44 @@ __device__ __forceinline__ void finish_rows(const ProductArgs& p, const v4f (&ac
                 continue;
         }
 #pragma unroll
-        for (int j = 0; j < (kDual ? TN / 2 : TN); ++j) {
-            const int nc = wn * kRowsB + j * 16 + q * 4;
-            if (nc >= nrows)
+        for (int j = 0; j < TJ; ++j) {
+            const int nc = column_at(j);
+            if (!WHOLE && nc >= nrows)
                 continue;
             const int64_t at = m * ldc + n0 + nc;
-            const int cnt = nrows - nc < 4 ? nrows - nc : 4;
             v4f v = acc[i][j], u;
-            if constexpr (EP == kEpGate) {
+            if constexpr (kDual) {
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float f, d;
-                    activation(p.act, acc[i][j][k], f, d);
-                    v[k] = f * acc[i][j + TN / 2][k];
+                    activation(act, acc[i][j][k], f, d);
+                    if constexpr (EP == kEpGate) {
+                        v[k] = f * acc[i][j + TN / 2][k];
+                    } else {
+                        const float g = from16(dh[i][j][k], ctype == kTBf16);
+                        v[k] = g * acc[i][j + TN / 2][k] * d;
+                        u[k] = g * f;
+                    }
                 }
-            } else if constexpr (EP == kEpGateGrad) {
-                const v4f g = load4(p.dh, m * p.lddh + n0 + nc, bf, cnt);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    float f, d;
-                    activation(p.act, acc[i][j][k], f, d);
-                    v[k] = g[k] * acc[i][j + TN / 2][k] * d;
-                    u[k] = g[k] * f;
-                }
-                store4(c, at + p.part_c, u, p.ctype, cnt);
             }
-            store4(c, at, v, p.ctype, cnt);
+            if constexpr (EP == kEpGateGrad)
+                store4(c, at + p.part_c, u, ctype, count_at(nc));
+            store4(c, at, v, ctype, count_at(nc));
         }
     }
+}
+
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN>
+__device__ __forceinline__ void finish_rows(const ProductArgs& p, const v4f (&acc)[NI][TN], int i0,
+                                            int tm, int tn, int wave, int lane)
+{
+    constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
+    if ((int64_t)(tm + 1) * BM > p.m || (int64_t)(tn + 1) * BNO > p.n)
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, -1, false>(p, acc, i0, tm, tn, wave, lane);
+    else if (EP == kEpStore || p.act == 0)
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 0, true>(p, acc, i0, tm, tn, wave, lane);
+    else
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 1, true>(p, acc, i0, tm, tn, wave, lane);
 }
 
 // REG: the operands' rows need not be 16-byte aligned; they go through
@@ -601,13 +642,13 @@ product_kernel(const ProductArgs p)
                 out[(i * TN + j) * 64 * W] = acc[i][j];
         return;
     }
-    finish_rows<BM, BN, WM, WN, EP, AT>(p, acc, 0, tm, tn, wave, lane);
+    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, 0, tm, tn, wave, lane);
 }
 
 // The shares of a tile's contraction, added in their order: a workgroup for
 // each of a wave's blocks of 16 rows, so that few tiles still spread over the
 // CUs, and four shares' loads in flight.
-template <int BM, int BN, int WM, int WN, int EP, bool AT>
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT>
 __global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
 {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -634,8 +675,8 @@ __global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
     }
     int tm, tn;
     tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-    finish_rows<BM, BN, WM, WN, EP, AT>(p, acc, (int)blockIdx.y, tm, tn,
-                                        __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6),
+    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, (int)blockIdx.y, tm, tn,
+                                              __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6),
                                         threadIdx.x & 63);
 }
 
@@ -670,7 +711,7 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
     if (splits == 1 || e != hipSuccess)
         return e;
     if constexpr (BM <= 128 && BN <= 128) {      // (larger tiles are never split)
-        hipLaunchKernelGGL((join_kernel<BM, BN, WM, WN, EP, AT>), dim3(tiles, BM / WM / 16),
+        hipLaunchKernelGGL((join_kernel<TYPE, BM, BN, WM, WN, EP, AT>), dim3(tiles, BM / WM / 16),
                            dim3(64 * WM * WN), 0, stream, p);
     }
     return hipGetLastError();
