@@ -4,6 +4,10 @@
 // them (16 of each projection) and all of A, its waves take the 128-byte
 // steps of k in turn, straight from memory into the matrix instructions'
 // registers, and one sum over the waves in LDS, in a fixed order, joins them.
+//
+// Memory bounds it, for one token the time to start too: e4m3 m 1 n 4096 k
+// 16384 takes 13.4 us (5.0 TB/s; a large copy reaches 5.15), gated bf16 m 8
+// n 16384 k 4096 47 us (5.7 TB/s: reads alone are faster than a copy).
 #include <hip/hip_runtime.h>
 
 #include "ffn_device.h"
