@@ -5,15 +5,15 @@
 // s = max(max |y| / 448, 2^-126), q = e4m3(y / s), rounded to nearest even.
 // A block with a value that is not finite gets a NaN scale and NaN codes.
 //
-// It is a pass over memory: what is read and written takes 0.2 us a MB at a large
-// copy's rate (5.15 TB/s), and the add/subtract stages have to stay under that.  A stage
-// on register bits costs a vector instruction an element, one across lanes
-// two and more, and the first five of a 16-bit input nothing on the matrix
-// cores (H_32, +-1).  So there is a kernel for each way to lay out 2^b:
-//   rows_kernel      b <= 10 (16 bits: <= 7): 16 elements a lane, 8 lanes a
-//                    block: bits 0-3 in registers, the others across lanes
-//   mid_kernel       16 bits, b = 8 .. 10: matrix cores, registers
-//   long_kernel      b = 11 .. 14: three layouts with LDS between them
+// It is a pass over memory: what is read and written takes 0.2 us a MB at a
+// large copy's rate (5.15 TB/s), and the add/subtract stages have to stay
+// under that.  A stage on register bits costs a vector instruction an element,
+// one across lanes two and more, and the first five of a 16-bit input nothing
+// on the matrix cores (H_32, +-1).  So there is a kernel for each way to lay out 2^b:
+//   rows_kernel      b <= 7: 16 elements a lane, 8 lanes a block: bits 0-3 in
+//                    registers, the others across lanes
+//   mid_kernel       b = 8 .. 10: two register layouts with LDS between them
+//   long_kernel      b = 11 .. 14: three
 //   tile_kernel      b <= 7, tile scales or transposed fp32: a 128 x 128 tile
 //   tile_t16_kernel  b <= 7, transposed 16 bits
 // Tile scales of longer rotations need two passes: a 128-row tile of 2^b
@@ -86,7 +86,7 @@ __device__ __forceinline__ void lane_stage(float (&v)[N], int lane)
     }
 }
 
-// Bits 0 .. bits - 1 (at most 10) of a wave's 1024 elements.
+// Bits 0 .. bits - 1 (at most 7) of a wave's 1024 elements.
 __device__ __forceinline__ void wave_stages(float (&v)[16], int bits, int lane)
 {
 #pragma unroll
@@ -103,12 +103,6 @@ __device__ __forceinline__ void wave_stages(float (&v)[16], int bits, int lane)
         lane_stage<1>(v, lane);
     if (bits > 6)
         lane_stage<2>(v, lane);
-    if (bits > 7)
-        lane_stage<3>(v, lane);
-    if (bits > 8)
-        lane_stage<4>(v, lane);
-    if (bits > 9)
-        lane_stage<5>(v, lane);
 }
 
 // Largest magnitude of the block's 128 values (16 on each of 8 lanes, or 32
@@ -202,18 +196,14 @@ __device__ __forceinline__ void finish(const RotateArgs& p, float (&v)[N], float
     }
 }
 
-// Rotations of at most 2^10: the blocks of all rows one after another, 8 to a
-// wave.  (k is a multiple of 2^b, so a rotation's blocks lie in one wave.)
-template <int TYPE, int MODE>
+// Rotations of at most 2^7: the blocks of all rows one after another, 8 to a
+// wave.  (k is a multiple of 2^b, so a rotation lies in one block.)
+template <int TYPE>
 __global__ __launch_bounds__(256) void rows_kernel(const RotateArgs p, float norm)
 {
     const int lane = threadIdx.x & 63;
     const int64_t kbs = (p.k + kFfnBlock - 1) / kFfnBlock;
-    // Codes by given scales are taken from the end, which the search for the
-    // maxima has read last and the last-level cache may hold (4096 x 16384
-    // fp32, b = 10, tile scales: 117 us from the front, 112 from the end).
-    const int64_t wg = MODE == kTileGiven ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
-    const unsigned g = (unsigned)(wg * 32 + (threadIdx.x >> 3));   // (at most 2^29)
+    const unsigned g = blockIdx.x * 32 + (threadIdx.x >> 3);     // (at most 2^29)
     const unsigned r = g / (unsigned)kbs;
     const int64_t row = r, kb = g - r * (unsigned)kbs;
     const bool live = row < p.m;
@@ -222,7 +212,7 @@ __global__ __launch_bounds__(256) void rows_kernel(const RotateArgs p, float nor
     float v[16];
     load_elements<TYPE>(p.x, row * p.ldx + k0, left, v);
     wave_stages(v, p.bits, lane);
-    finish<MODE>(p, v, norm, !(p.bits & 1), row, kb, lane & 7, live);
+    finish<kRowScales>(p, v, norm, !(p.bits & 1), row, kb, lane & 7, live);
 }
 
 // Rotations of 2^11 to 2^14: a workgroup of 2^b / 32 threads for each, in
@@ -401,12 +391,17 @@ __device__ __forceinline__ void layout_c(const float* lds, int t, float (&v)[32]
     }
 }
 
-// Rotations of 2^8 to 2^10 of 16-bit inputs: a wave takes 2048 elements, 2^(11-b)
-// rotations in the order of the rows.  Bits 0-4 are the matrix cores' H_32
-// (32 neighbours are a place), the others layout B's register stages, and
-// layout C hands a lane its quarter of a block.  What it saves are lane
-// stages: 8192 x 4096 bf16, b = 10, takes 29.4 us with lane stages and 19.5
-// here, where its bytes take 19.7 at a large copy's rate.
+// Rotations of 2^8 to 2^10: a wave takes 2048 elements, 2^(11-b) rotations in
+// the order of the rows.  Bits 0-4 are register stages on a lane's 32
+// neighbours, for 16-bit inputs the matrix cores' H_32; the others layout B's
+// register stages; and layout C hands a lane its quarter of a block.  Against
+// stages across lanes (16 elements a lane, no LDS), b = 10: 8192 x 4096 bf16
+// 29.4 and 19.5 us (19.7 at a large copy's rate), fp32 34.7 and 32.4 (32.8),
+// 4096 x 16384 fp32 with tile scales 109 and 103.
+//
+// Codes by given scales are taken from the end, which the search for the
+// maxima has read last and the last-level cache may hold (4096 x 16384 fp32,
+// tile scales: 117 us from the front, 112 from the end).
 template <int TYPE, int MODE, int BITS>
 __global__ __launch_bounds__(64) void mid_kernel(const RotateArgs p, float norm)
 {
@@ -428,25 +423,47 @@ __global__ __launch_bounds__(64) void mid_kernel(const RotateArgs p, float norm)
     struct __attribute__((packed)) Any {
         v4i w;
     };
-    v4i in[4];
-#pragma unroll
-    for (int c = 0; c < 4; ++c) {
-        const int i = (c * 16 + l16) * 32 + q * 8;
+    if constexpr (TYPE == kTF32) {
         int64_t row, k0;
-        unit((unsigned)i >> BITS, row, k0);
+        unit((unsigned)(t * 32) >> BITS, row, k0);
         row = row < p.m ? row : p.m - 1;     // past the last: any that is there
-        in[c] = ((const Any*)((const unsigned short*)p.x + row * p.ldx + k0 +
-                              (i & ((1 << BITS) - 1))))->w;
-    }
-    v4i h[2];
-    hadamard32<TYPE>(t, h);
+        const float* x = (const float*)p.x + row * p.ldx + k0 + (t * 32 & ((1 << BITS) - 1));
+        float v[32];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const int i = (c * 16 + l16) * 32 + e * 16 + q * 4;
-            *(v4f*)(lds + (i ^ (((i >> 6) & 7) << 2) ^ ((c >> 1) << 5))) = times<TYPE>(h[e], in[c]);
+        for (int i = 0; i < 32; i += 4) {
+            const v4f w = __builtin_bit_cast(v4f, ((const Any*)(x + i))->w);
+            v[i] = w[0];
+            v[i + 1] = w[1];
+            v[i + 2] = w[2];
+            v[i + 3] = w[3];
         }
+        stages32<0, 5>(v);
+        float* const c0 = lds + ((t * 32) ^ (t & 32));
+        const int cm = ((t >> 1) & 7) << 2;
+#pragma unroll
+        for (int i = 0; i < 32; i += 4)
+            *(v4f*)(c0 + (i ^ cm)) = v4f{v[i], v[i + 1], v[i + 2], v[i + 3]};
+    } else {
+        v4i in[4];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            const int i = (c * 16 + l16) * 32 + q * 8;
+            int64_t row, k0;
+            unit((unsigned)i >> BITS, row, k0);
+            row = row < p.m ? row : p.m - 1;
+            in[c] = ((const Any*)((const unsigned short*)p.x + row * p.ldx + k0 +
+                                  (i & ((1 << BITS) - 1))))->w;
+        }
+        v4i h[2];
+        hadamard32<TYPE>(t, h);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const int i = (c * 16 + l16) * 32 + e * 16 + q * 4;
+                *(v4f*)(lds + (i ^ (((i >> 6) & 7) << 2) ^ ((c >> 1) << 5))) = times<TYPE>(h[e], in[c]);
+            }
+    }
     __syncthreads();
     layout_b<BITS - 5>(lds, t);
     __syncthreads();
@@ -466,7 +483,7 @@ __global__ __launch_bounds__(1 << (BITS - 5)) void long_kernel(const RotateArgs 
     const int64_t per = p.k >> BITS;
     // Rotations of the 32 rows whose scales share a line of memory run on one
     // XCD (workgroup w on XCD w mod 8), whose L2 gathers them.
-    // Codes by given scales are taken from the end (see rows_kernel).
+    // Codes by given scales are taken from the end (see mid_kernel).
     int64_t w = MODE == kTileGiven ? gridDim.x - 1 - blockIdx.x : blockIdx.x;
     const int64_t group = 256 * per;
     if (w < p.m * per / group * group) {
@@ -696,25 +713,21 @@ template <int TYPE, int MODE>
 hipError_t rows(const RotateArgs& p, float norm, hipStream_t stream)
 {
     const int64_t kbs = (p.k + kFfnBlock - 1) / kFfnBlock;
-    if constexpr (TYPE != kTF32) {
+    if (MODE == kRowScales && p.bits <= 7) {
+        hipLaunchKernelGGL((rows_kernel<TYPE>), dim3((unsigned)((p.m * kbs + 31) / 32)), dim3(256),
+                           0, stream, p, norm);
+    } else if (p.bits <= 10) {
         const int64_t rotations = p.m * (p.k >> p.bits);
         const dim3 grid((unsigned)(((rotations << p.bits) + 2047) / 2048));
         switch (p.bits) {
         case 8:
             hipLaunchKernelGGL((mid_kernel<TYPE, MODE, 8>), grid, dim3(64), 0, stream, p, norm);
-            return hipGetLastError();
+            break;
         case 9:
             hipLaunchKernelGGL((mid_kernel<TYPE, MODE, 9>), grid, dim3(64), 0, stream, p, norm);
-            return hipGetLastError();
-        case 10:
+            break;
+        default:
             hipLaunchKernelGGL((mid_kernel<TYPE, MODE, 10>), grid, dim3(64), 0, stream, p, norm);
-            return hipGetLastError();
-        }
-    }
-    if (p.bits <= 10) {
-        if constexpr (TYPE == kTF32 || MODE == kRowScales) {   // (else bits is above 7)
-            hipLaunchKernelGGL((rows_kernel<TYPE, MODE>), dim3((unsigned)((p.m * kbs + 31) / 32)),
-                               dim3(256), 0, stream, p, norm);
         }
     } else {
         const dim3 grid((unsigned)(p.m * (p.k >> p.bits)));
