@@ -687,6 +687,87 @@ def test_captured_and_replayed():
             assert torch.equal(a, b), i
 
 
+# ---- arrays past 4 GiB ------------------------------------------------------
+# The last rows (and the last results) of an operand that is larger than 2^32
+# bytes against the same rows alone; small integers, so every sum is exact and
+# the two agree bit for bit whatever tiles they take.
+
+def small_integers(rows, cols, dtype, seed):
+    t = torch.empty(rows, cols, dtype=torch.int8, device="cuda")
+    t.random_(-4, 5, generator=gen(seed))
+    out = torch.empty(rows, cols, dtype=dtype, device="cuda")
+    for lo in range(0, rows, 1 << 14):
+        out[lo:lo + (1 << 14)] = t[lo:lo + (1 << 14)].to(dtype)
+    return out
+
+
+@pytest.mark.parametrize("bits,scales", [(5, "row"), (8, "tile"), (13, "row")])
+def test_rotate_past_32_bits(bits, scales):
+    say("large rotate", bits, scales)
+    x = small_integers(70016, 65536, torch.bfloat16, bits)    # 9 GB, codes 4.6 GB
+    q, s = qse.rotate_quantize(x, bits=bits, scales=scales)
+    for rows in (slice(0, 128), slice(70016 - 128, 70016)):
+        q2, s2 = qse.rotate_quantize(x[rows], bits=bits, scales=scales)
+        assert torch.equal(q[rows].view(torch.uint8), q2.view(torch.uint8))
+        at = slice(rows.start // BLOCK, rows.stop // BLOCK) if scales == "tile" else rows
+        assert torch.equal(s[:, at], s2)
+
+
+def test_rotate_transposed_past_32_bits():
+    say("large rotate, transposed")
+    x = small_integers(65536, 35008, torch.bfloat16, 1)       # k x m, 4.6 GB
+    q, s = qse.rotate_quantize(x, bits=7, transpose=True)
+    q2, s2 = qse.rotate_quantize(x[-256:], bits=7, transpose=True)
+    assert torch.equal(q[:, -256:].float(), q2.float()) and torch.equal(s[-2:], s2)
+
+
+@pytest.mark.parametrize("m", [3, 70, 600])
+def test_matmul_past_32_bits(m):
+    say("large matmul", m)
+    n, k = 70016, 65536                                       # codes of 4.6 GB
+    a, b = small_integers(m, k, F8, 2), small_integers(n, k, F8, 3)
+    sa, sb = torch.ones(k // BLOCK, m, device="cuda"), torch.ones(k // BLOCK, n, device="cuda")
+    for out in (torch.float32, torch.bfloat16):
+        c = qse.scaled_matmul(a, sa, b, sb, out_dtype=out)
+        for rows in (slice(0, 200), slice(n - 200, n)):
+            want = qse.scaled_matmul(a, sa, b[rows], sb[:, rows].contiguous(), out_dtype=out)
+            assert torch.equal(c[:, rows], want)
+    del b
+    # and results past them, from a short contraction
+    m, n = 50000, 49999
+    a, b = small_integers(m, 128, F8, 4), small_integers(n, 128, F8, 5)
+    sa, sb = torch.ones(1, m, device="cuda"), torch.ones(1, n, device="cuda")
+    c = qse.scaled_matmul(a, sa, b, sb)
+    for i, j in ((0, n - 300), (m - 300, 0), (m - 300, n - 300)):
+        want = a[i:i + 300].float() @ b[j:j + 300].float().t()
+        assert torch.equal(c[i:i + 300, j:j + 300], want.bfloat16())
+
+
+@pytest.mark.parametrize("m", [5, 200])
+def test_gated_past_32_bits(m):
+    say("large gated", m)
+    n, k = 140032, 16384                                      # 4.6 GB each
+    x = small_integers(m, k, torch.bfloat16, 6) * 0.0625
+    wg, wu = (small_integers(n, k, torch.bfloat16, seed) for seed in (7, 8))
+    h = qse.gated_ffn(x, wg, wu)
+    for rows in (slice(0, 200), slice(n - 200, n)):
+        assert torch.equal(h[:, rows], qse.gated_ffn(x, wg[rows], wu[rows]))
+
+
+def test_gated_backward_past_32_bits():
+    # one token's gradient is not zero: each weight gradient is one product
+    say("large backward")
+    m, n, k = 140032, 32, 16384                               # x and dx of 4.6 GB
+    x = small_integers(m, k, torch.bfloat16, 9)
+    wg, wu = (small_integers(n, k, torch.bfloat16, seed) * 0.0625 for seed in (10, 11))
+    dh = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+    dh[-3] = 1.0
+    dx, dg, du = qse.gated_ffn_backward(x, wg, wu, dh)
+    sx, sg, su = qse.gated_ffn_backward(x[-128:], wg, wu, dh[-128:])
+    assert torch.equal(dx[-128:], sx) and torch.equal(dg, sg) and torch.equal(du, su)
+    assert float(dx[:-3].abs().max()) == 0.0 and float(dx[-3].abs().max()) > 0.0
+
+
 def test_results_do_not_change_between_runs():
     say("determinism")
     g = gen(23)
