@@ -104,6 +104,51 @@ __device__ __forceinline__ v4f matrix_step(const v4i* a, const v4i* b, v4f acc)
     }
 }
 
+// Sixteen bytes at any address.
+__device__ __forceinline__ v4i load16(const char* p)
+{
+    struct __attribute__((packed)) Any {
+        v4i v;
+    };
+    return ((const Any*)p)->v;
+}
+
+// A 16-byte chunk of 16-bit elements that ends `past` bytes behind its row is
+// read `past` bytes earlier, from the row's last 16: moved to its place, with
+// zeros behind the row.
+__device__ __forceinline__ v4i drop(v4i v, int past)
+{
+    if (past & 8)
+        v = v4i{v[2], v[3], 0, 0};
+    if (past & 4)
+        v = v4i{v[1], v[2], v[3], 0};
+    if (past & 2)
+        v = v4i{(int)__builtin_amdgcn_alignbyte((unsigned)v[1], (unsigned)v[0], 2),
+                (int)__builtin_amdgcn_alignbyte((unsigned)v[2], (unsigned)v[1], 2),
+                (int)__builtin_amdgcn_alignbyte((unsigned)v[3], (unsigned)v[2], 2),
+                (int)((unsigned)v[3] >> 16)};
+    return past >= 16 ? v4i{0, 0, 0, 0} : v;
+}
+
+// The same of a row of fewer than 16 bytes, element by element.
+__device__ __forceinline__ v4i chunk_of_short_row(const char* p, int left)
+{
+    v4i v = v4i{0, 0, 0, 0};
+#pragma unroll 1
+    for (int e = 0; 2 * e < left; ++e) {
+        const int u = (int)((unsigned)((const unsigned short*)p)[e] << (16 * (e & 1)));
+        if (e < 2)
+            v[0] |= u;
+        else if (e < 4)
+            v[1] |= u;
+        else if (e < 6)
+            v[2] |= u;
+        else
+            v[3] |= u;
+    }
+    return v;
+}
+
 // Round to nearest even in 16 bits; the type is uniform.
 __device__ __forceinline__ unsigned short to16(float v, bool bf)
 {

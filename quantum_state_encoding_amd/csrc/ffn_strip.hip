@@ -17,26 +17,27 @@ namespace {
 
 constexpr int kStep = 128;   // bytes of k per step
 
-// Sixteen bytes at any address.
-__device__ __forceinline__ v4i load16(const char* p)
+// Sixteen bytes at `at` of a row of len bytes, 0 past its end.  e4m3 rows are
+// 16-byte aligned, so a chunk that holds a byte of the row is in its page;
+// those of 16-bit types are read from the row's last 16 bytes.
+template <int TYPE>
+__device__ __forceinline__ v4i load16_tail(const char* row, int64_t at, int64_t len)
 {
-    struct __attribute__((packed)) Any {
-        v4i v;
-    };
-    return ((const Any*)p)->v;
-}
-
-// The same, of a row that ends `left` bytes on: 0 from there.
-__device__ __forceinline__ v4i load16_tail(const char* p, int left)
-{
-    if (left >= 16)
-        return load16(p);
-    v4i v = v4i{0, 0, 0, 0};
+    if constexpr (TYPE == kTBf16 || TYPE == kTF16) {
+        if (len < 16)
+            return chunk_of_short_row(row, at == 0 ? (int)len : 0);
+        const int64_t from = at < len - 16 ? at : len - 16;
+        return drop(load16(row + from), (int)(at - from));
+    } else {
+        v4i v = load16(row + (at < len ? at : (len - 1) & ~(int64_t)15));
+        const int left = (int)(len - at);
 #pragma unroll
-    for (int b = 0; b < 16; ++b)
-        if (b < left)
-            v[b >> 2] |= (int)((unsigned)(unsigned char)p[b] << (8 * (b & 3)));
-    return v;
+        for (int w = 0; w < 4; ++w) {
+            const int b = left - 4 * w;
+            v[w] = b >= 4 ? v[w] : b <= 0 ? 0 : v[w] & ((1 << (8 * b)) - 1);
+        }
+        return v;
+    }
 }
 
 template <int TYPE, int MT, int W, int U, int EP, int SM>
@@ -134,15 +135,14 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
     }
     for (; kt * kStep < p.kbytes; kt += W) {
         Step t;
-        const int left = (int)(p.kbytes - kt * kStep < kStep ? p.kbytes - kt * kStep : kStep) - q * 16;
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
 #pragma unroll
             for (int j = 0; j < P; ++j)
-                t.b[j][h] = load16_tail(bp[j] + kt * kStep + h * 64, left - h * 64);
+                t.b[j][h] = load16_tail<TYPE>(bp[j] - q * 16, kt * kStep + h * 64 + q * 16, p.kbytes);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
-                t.a[i][h] = load16_tail(ap[i] + kt * kStep + h * 64, left - h * 64);
+                t.a[i][h] = load16_tail<TYPE>(ap[i] - q * 16, kt * kStep + h * 64 + q * 16, p.kbytes);
         }
         load_scales(t, kt);
         add(t);

@@ -371,6 +371,8 @@ GATED = [  # m, n, k
     (33, 300, 7), (150, 5, 3), (20, 16500, 66),
     # contractions that are shared
     (64, 64, 8016), (300, 128, 8200), (100, 70, 6001), (40, 300, 12345),
+    # few rows, long and odd
+    (28, 115, 1215), (5, 33, 4099), (1, 20, 9), (16, 16, 1001), (3, 40, 8), (32, 18, 5),
 ]
 
 
