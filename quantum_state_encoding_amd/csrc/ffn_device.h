@@ -113,6 +113,33 @@ __device__ __forceinline__ v4i load16(const char* p)
     return ((const Any*)p)->v;
 }
 
+// The same of 16-bit elements at odd addresses too: a load that is not
+// 4-byte aligned takes three times as long, so the words around it are loaded,
+// w and the one that holds its last element, and moved by `by` = address & 2
+// later.  For a strip's operands (gated bf16 m 8: n 8000 k 4097 68 us with
+// such loads, 33 so; k 4098 28); in the tiles, whose loads share the CU with
+// more, the second load costs more than it saves (f16 m 1021 n 5501 k 2047:
+// 75 and 84 us).
+struct Around {
+    v4i w;
+    unsigned last;
+};
+__device__ __forceinline__ Around load_around(const char* p)
+{
+    struct __attribute__((packed, aligned(4))) Words {
+        v4i v;
+    };
+    const uintptr_t at = (uintptr_t)p & ~(uintptr_t)3;
+    return Around{((const Words*)at)->v, *(const unsigned*)(at + 12 + 2 * ((uintptr_t)p & 2))};
+}
+__device__ __forceinline__ v4i moved(const Around& a, int by)
+{
+    return v4i{(int)__builtin_amdgcn_alignbyte((unsigned)a.w[1], (unsigned)a.w[0], by),
+               (int)__builtin_amdgcn_alignbyte((unsigned)a.w[2], (unsigned)a.w[1], by),
+               (int)__builtin_amdgcn_alignbyte((unsigned)a.w[3], (unsigned)a.w[2], by),
+               (int)__builtin_amdgcn_alignbyte(a.last, (unsigned)a.w[3], by)};
+}
+
 // A 16-byte chunk of 16-bit elements that ends `past` bytes behind its row is
 // read `past` bytes earlier, from the row's last 16: moved to its place, with
 // zeros behind the row.

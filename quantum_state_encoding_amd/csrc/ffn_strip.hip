@@ -27,7 +27,8 @@ __device__ __forceinline__ v4i load16_tail(const char* row, int64_t at, int64_t 
         if (len < 16)
             return chunk_of_short_row(row, at == 0 ? (int)len : 0);
         const int64_t from = at < len - 16 ? at : len - 16;
-        return drop(load16(row + from), (int)(at - from));
+        const int by = (int)((uintptr_t)(row + from) & 2);
+        return drop(moved(load_around(row + from), by), (int)(at - from));
     } else {
         v4i v = load16(row + (at < len ? at : (len - 1) & ~(int64_t)15));
         const int left = (int)(len - at);
@@ -40,7 +41,8 @@ __device__ __forceinline__ v4i load16_tail(const char* row, int64_t at, int64_t 
     }
 }
 
-template <int TYPE, int MT, int W, int U, int EP, int SM>
+// ODD: 16-bit rows at addresses that are not multiples of 4.
+template <int TYPE, int MT, int W, int U, int EP, int SM, bool ODD>
 __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
 {
     constexpr int P = EP == kEpStore ? 1 : 2;    // projections
@@ -79,7 +81,17 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
     // are issued before the first is used.
     struct Step {
         v4i b[P][2], a[MT][2];
+        unsigned blast[ODD ? P : 1][2], alast[ODD ? MT : 1][2];
         float sb[SM ? P : 1][SM == 2 ? 4 : 1], sa[SM ? MT : 1];
+    };
+    auto fetch = [](v4i& v, unsigned& last, const char* at) __attribute__((always_inline)) {
+        if constexpr (ODD) {
+            const Around a = load_around(at);
+            v = a.w;
+            last = a.last;
+        } else {
+            v = load16(at);
+        }
     };
     auto load_scales = [&](Step& t, int64_t kt) __attribute__((always_inline)) {
         if constexpr (SM != 0) {
@@ -120,18 +132,34 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
             for (int j = 0; j < P; ++j)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    t[u].b[j][h] = load16(bp[j] + (kt + u * W) * kStep + h * 64);
+                    fetch(t[u].b[j][h], t[u].blast[ODD ? j : 0][h],
+                          bp[j] + (kt + u * W) * kStep + h * 64);
             load_scales(t[u], kt + u * W);
 #pragma unroll
             for (int i = 0; i < MT; ++i)
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
-                    t[u].a[i][h] = load16(ap[i] + (kt + u * W) * kStep + h * 64);
+                    fetch(t[u].a[i][h], t[u].alast[ODD ? i : 0][h],
+                          ap[i] + (kt + u * W) * kStep + h * 64);
         }
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-        for (int u = 0; u < U; ++u)
+        for (int u = 0; u < U; ++u) {
+            if constexpr (ODD) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int j = 0; j < P; ++j)
+                        t[u].b[j][h] = moved(Around{t[u].b[j][h], t[u].blast[j][h]},
+                                             (int)(uintptr_t)bp[j] & 2);
+#pragma unroll
+                    for (int i = 0; i < MT; ++i)
+                        t[u].a[i][h] = moved(Around{t[u].a[i][h], t[u].alast[i][h]},
+                                             (int)(uintptr_t)ap[i] & 2);
+                }
+            }
             add(t[u]);
+        }
     }
     for (; kt * kStep < p.kbytes; kt += W) {
         Step t;
@@ -186,13 +214,13 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
     }
 }
 
-template <int TYPE, int MT, int W, int U, int EP, int SM>
+template <int TYPE, int MT, int W, int U, int EP, int SM, bool ODD = false>
 hipError_t run(const ProductArgs& p, hipStream_t stream)
 {
     constexpr int P = EP == kEpStore ? 1 : 2;
     constexpr size_t kLds = (size_t)W * P * MT * 4 * 64 * 4;
     static_assert(kLds <= 65536, "dynamic LDS without an attribute");
-    hipLaunchKernelGGL((strip_kernel<TYPE, MT, W, U, EP, SM>), dim3((unsigned)((p.n + 15) / 16)),
+    hipLaunchKernelGGL((strip_kernel<TYPE, MT, W, U, EP, SM, ODD>), dim3((unsigned)((p.n + 15) / 16)),
                        dim3(64 * W), kLds, stream, p);
     return hipGetLastError();
 }
@@ -204,6 +232,13 @@ hipError_t run(const ProductArgs& p, hipStream_t stream)
 template <int TYPE, int EP, int SM>
 hipError_t pick(const ProductArgs& p, hipStream_t stream)
 {
+    if constexpr (SM == 0) {
+        const uintptr_t any = (uintptr_t)p.a | (uintptr_t)p.b0 | (uintptr_t)p.b1 |
+                              (uintptr_t)p.lda | (uintptr_t)p.ldb0 | (uintptr_t)p.ldb1;
+        if (any & 3)
+            return p.m > 16 ? run<TYPE, 2, 8, 2, EP, SM, true>(p, stream)
+                            : run<TYPE, 1, 8, 4, EP, SM, true>(p, stream);
+    }
     if (p.m > 16)
         return run<TYPE, 2, 8, 2, EP, SM>(p, stream);
     if constexpr (EP == kEpStore && SM == 1 && TYPE == kTE4m3) {
