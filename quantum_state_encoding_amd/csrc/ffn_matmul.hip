@@ -92,7 +92,8 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 
 // From a tile's sums to results: lane l holds rows l % 16 * TM .. of A (AT:
 // every 16th from l % 16) and four consecutive rows of B, stored at once.
-// acc: rows i0, i0 + 1, .. of the wave's BM / WM / 16.
+// acc: rows i0, i0 + 1, .. of the wave's BM / WM / 16, and the 16-row blocks
+// of B from j0 on (dual: gate's, then up's).
 //
 // A tile runs this once, as straight code, and its time is mostly that of
 // fetching the code: so a whole tile has a path of its own without bounds, and
@@ -101,11 +102,12 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN, int ACT,
           bool WHOLE>
 __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (&acc)[NI][TN],
-                                               int i0, int tm, int tn, int wave, int lane)
+                                               int i0, int j0, int tm, int tn, int wave, int lane)
 {
     constexpr int TM = BM / WM / 16;
     constexpr bool kDual = EP != kEpStore;
     constexpr int BNO = kDual ? BN / 2 : BN, kRowsB = BNO / WN, TJ = kDual ? TN / 2 : TN;
+    // (TN: the blocks that acc has)
     const int wm = wave / WN, wn = wave % WN, q = lane >> 4, l16 = lane & 15;
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNO;
     const int mrows = WHOLE || p.m - m0 > BM ? BM : (int)(p.m - m0);
@@ -119,7 +121,7 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (
         return wm * (TM * 16) + (AT ? (i0 + i) * 16 + l16 : l16 * TM + i0 + i);
     };
     const auto column_at = [=](int j) __attribute__((always_inline)) {
-        return wn * kRowsB + j * 16 + q * 4;
+        return wn * kRowsB + (j0 + j) * 16 + q * 4;
     };
     const auto count_at = [=](int nc) __attribute__((always_inline)) {
         return WHOLE || nrows - nc > 4 ? 4 : nrows - nc;
@@ -184,15 +186,15 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (
 
 template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN>
 __device__ __forceinline__ void finish_rows(const ProductArgs& p, const v4f (&acc)[NI][TN], int i0,
-                                            int tm, int tn, int wave, int lane)
+                                            int j0, int tm, int tn, int wave, int lane)
 {
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
     if ((int64_t)(tm + 1) * BM > p.m || (int64_t)(tn + 1) * BNO > p.n)
-        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, -1, false>(p, acc, i0, tm, tn, wave, lane);
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, -1, false>(p, acc, i0, j0, tm, tn, wave, lane);
     else if (EP == kEpStore || p.act == 0)
-        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 0, true>(p, acc, i0, tm, tn, wave, lane);
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 0, true>(p, acc, i0, j0, tm, tn, wave, lane);
     else
-        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 1, true>(p, acc, i0, tm, tn, wave, lane);
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 1, true>(p, acc, i0, j0, tm, tn, wave, lane);
 }
 
 // REG: the operands' rows need not be 16-byte aligned; they go through
@@ -611,42 +613,47 @@ product_kernel(const ProductArgs p)
                 out[(i * TN + j) * 64 * W] = acc[i][j];
         return;
     }
-    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, 0, tm, tn, wave, lane);
+    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, 0, 0, tm, tn, wave, lane);
 }
 
 // The shares of a tile's contraction, added in their order: a workgroup for
-// each of a wave's blocks of 16 rows, so that few tiles still spread over the
-// CUs, and four shares' loads in flight.
+// each 16 x 16 block of its waves (gated: gate's and up's), so that few tiles
+// still spread over the CUs, and eight shares' loads in flight (f16 m 862 n
+// 15195 k 67, gradients: the join of 7 tiles in 16 shares takes 4.9 us, 7.3
+// with 16 rows of A and all of B to a workgroup).
 template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT>
 __global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
 {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
+    constexpr int P = EP != kEpStore ? 2 : 1, TJ = TN / P;
+    constexpr int kAhead = 8;
     const int64_t stride = (int64_t)gridDim.x * (TM * TN * 64 * W);
+    const int i = (int)blockIdx.y, j = (int)blockIdx.z;
     const v4f* in = (const v4f*)p.partial + (int64_t)blockIdx.x * (TM * TN * 64 * W) +
-                    (int)blockIdx.y * TN * 64 * W + threadIdx.x;
-    v4f acc[1][TN];
+                    (i * TN + j) * 64 * W + threadIdx.x;
+    v4f acc[1][P];
 #pragma unroll
-    for (int j = 0; j < TN; ++j)
-        acc[0][j] = in[j * 64 * W];
-    for (int s = 1; s < p.splits; s += 4) {
-        v4f more[4][TN];
+    for (int h = 0; h < P; ++h)
+        acc[0][h] = in[h * TJ * 64 * W];
+    for (int s = 1; s < p.splits; s += kAhead) {
+        v4f more[kAhead][P];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < kAhead; ++u)
 #pragma unroll
-            for (int j = 0; j < TN; ++j)
-                more[u][j] = in[(s + u < p.splits ? s + u : s) * stride + j * 64 * W];
+            for (int h = 0; h < P; ++h)
+                more[u][h] = in[(s + u < p.splits ? s + u : s) * stride + h * TJ * 64 * W];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < kAhead; ++u)
             if (s + u < p.splits)
 #pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    acc[0][j] += more[u][j];
+                for (int h = 0; h < P; ++h)
+                    acc[0][h] += more[u][h];
     }
     int tm, tn;
     tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, (int)blockIdx.y, tm, tn,
+    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, i, j, tm, tn,
                                               __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6),
-                                        threadIdx.x & 63);
+                                              threadIdx.x & 63);
 }
 
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG = kAligned,
@@ -680,8 +687,9 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
     if (splits == 1 || e != hipSuccess)
         return e;
     if constexpr (BM <= 128 && BN <= 128) {      // (larger tiles are never split)
-        hipLaunchKernelGGL((join_kernel<TYPE, BM, BN, WM, WN, EP, AT>), dim3(tiles, BM / WM / 16),
-                           dim3(64 * WM * WN), 0, stream, p);
+        const dim3 grid(tiles, BM / WM / 16, BNO / WN / 16);
+        hipLaunchKernelGGL((join_kernel<TYPE, BM, BN, WM, WN, EP, AT>), grid, dim3(64 * WM * WN), 0,
+                           stream, p);
     }
     return hipGetLastError();
 }
@@ -702,7 +710,8 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
 //
 // Where the tiles leave half of their slots empty, the workgroups of a tile
 // share its steps and a second kernel adds their sums, for about 5 us: m 300
-// n 200 k 16000 (fp32 out) takes 44 us in one share, 16 in twelve.
+// n 200 k 16000 (fp32 out) takes 44 us in one share, 16 in twelve.  At most
+// 32 shares (gradients of bf16 m 862 n 15195 k 67: 16 115 us, 32 99).
 struct Tile {
     int bm, bn, slots;   // bn: output columns
     float step;
@@ -726,7 +735,7 @@ Choice cheapest(const Tile (&tiles)[N], const ProductArgs& p)
                           : (double)((count + t.slots - 1) / t.slots) * t.step * steps;
         int splits = 1;
         if (t.area && p.may_split && count * 2 <= t.slots) {
-            int64_t s = t.slots / count < 16 ? t.slots / count : 16;
+            int64_t s = t.slots / count < 32 ? t.slots / count : 32;
             s = s < steps / 4 ? s : steps / 4;
             // every share has steps, the last one fewer
             s = s > 1 ? (steps + (steps + s - 1) / s - 1) / ((steps + s - 1) / s) : 1;
