@@ -157,12 +157,13 @@ __device__ __forceinline__ v4i drop(v4i v, int past)
     return past >= 16 ? v4i{0, 0, 0, 0} : v;
 }
 
-// The same of a row of fewer than 16 bytes, element by element.
+// A chunk `left` bytes before its row's end element by element, which rows of
+// fewer than 16 bytes need.
 __device__ __forceinline__ v4i chunk_of_short_row(const char* p, int left)
 {
     v4i v = v4i{0, 0, 0, 0};
 #pragma unroll 1
-    for (int e = 0; 2 * e < left; ++e) {
+    for (int e = 0; 2 * e < left && e < 8; ++e) {
         const int u = (int)((unsigned)((const unsigned short*)p)[e] << (16 * (e & 1)));
         if (e < 2)
             v[0] |= u;

@@ -457,7 +457,9 @@ BACK = [(1, 1, 1), (1, 40, 64), (7, 9, 11), (16, 64, 128), (65, 100, 130), (128,
         (2600, 72, 5120), (72, 2056, 4112), (2601, 70, 5121), (70, 2050, 4099), (300, 5, 200),
         (200, 300, 6),
         # each product's contraction shared
-        (16, 64, 8016), (64, 4100, 200), (4000, 40, 72), (70, 2051, 133), (3001, 33, 41)]
+        (16, 64, 8016), (64, 4100, 200), (4000, 40, 72), (70, 2051, 133), (3001, 33, 41),
+        # rows of fewer than 16 bytes beside longer ones
+        (1, 9, 7), (4, 40, 7), (5, 7, 40), (7, 5, 41), (3, 300, 1), (6, 1, 300), (40, 9, 8)]
 
 
 @pytest.mark.parametrize("m,n,k", BACK)
@@ -486,7 +488,7 @@ def test_gated_backward(m, n, k, act, dtype):
         want = sum(a @ b for a, b, _ in terms)
         tol = sum(e @ b.abs() + count * 2 * U * ((a.abs() + e) @ b.abs()) for a, b, e in terms)
         tol = tol + half(dt) * (want.abs() + tol) + tiny
-        bad = (got.double() - want).abs() > tol
+        bad = ~((got.double() - want).abs() <= tol)      # (NaN is bad)
         assert got.dtype == dt and got.shape == want.shape
         assert not bool(bad.any()), (name, int(bad.sum()))
     check("dx", got[0], [(dg, gd, e_dg), (du, ud, e_du)], 2 * n + 2)
@@ -689,11 +691,6 @@ def test_captured_and_replayed():
             assert torch.equal(a, b), i
 
 
-# ---- arrays past 4 GiB ------------------------------------------------------
-# The last rows (and the last results) of an operand that is larger than 2^32
-# bytes against the same rows alone; small integers, so every sum is exact and
-# the two agree bit for bit whatever tiles they take.
-
 def small_integers(rows, cols, dtype, seed):
     t = torch.empty(rows, cols, dtype=torch.int8, device="cuda")
     t.random_(-4, 5, generator=gen(seed))
@@ -702,6 +699,50 @@ def small_integers(rows, cols, dtype, seed):
         out[lo:lo + (1 << 14)] = t[lo:lo + (1 << 14)].to(dtype)
     return out
 
+
+def nan_framed(t, off):
+    """t as a view of an array that is NaN all around it."""
+    big = torch.full((t.shape[0] + 2, t.shape[1] + 24), float("nan"), device="cuda").to(t.dtype)
+    view = big[1:-1, off:off + t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("m", [1, 5, 17, 40, 300])
+@pytest.mark.parametrize("n,k", [(33, 37), (50, 129), (20, 1001), (130, 64), (9, 7)])
+def test_nothing_around_a_view_is_used(m, n, k):
+    # small integers: sums are exact and the two calls agree whatever path
+    # their alignment gives them
+    say("framed", m, n, k)
+    x, wg, wu = (small_integers(r, k, torch.bfloat16, seed) * 0.5
+                 for r, seed in ((m, 1), (n, 2), (n, 3)))
+    dh = small_integers(m, n, torch.bfloat16, 4)
+    want = qse.gated_ffn(x, wg, wu)
+    whole = qse.rotate_quantize(x)
+    for off in (0, 1, 2, 8, 11):
+        fx, fg, fu, fd = (nan_framed(t, off) for t in (x, wg, wu, dh))
+        assert torch.equal(qse.gated_ffn(fx, fg, fu), want)
+        assert all(bool(torch.isfinite(t).all()) for t in qse.gated_ffn_backward(fx, fg, fu, fd))
+        q, s = qse.rotate_quantize(fx)
+        assert torch.equal(q.float(), whole[0].float()) and torch.equal(s, whole[1])
+        qt, st = qse.rotate_quantize(fx, transpose=True)
+        assert bool(torch.isfinite(qt.float()).all()) and bool(torch.isfinite(st).all())
+    # codes in rows of a multiple of 16 bytes: NaN codes between and around them
+    a = small_integers(m, k, F8, 5)
+    b = small_integers(n, k, F8, 6)
+    fa, fb = (torch.full((len(t) + 1, -(-k // 16) * 16 + 16), float("nan"), device="cuda").to(F8)
+              for t in (a, b))
+    fa[:m, :k], fb[:n, :k] = a, b
+    ones = [torch.ones(-(-k // BLOCK), r, device="cuda") for r in (m, n)]
+    for out in (torch.float32, torch.bfloat16):
+        c = qse.scaled_matmul(fa[:m, :k], ones[0], fb[:n, :k], ones[1], out_dtype=out)
+        assert torch.equal(c, (a.float() @ b.float().t()).to(out))
+
+
+# ---- arrays past 4 GiB ------------------------------------------------------
+# The last rows (and the last results) of an operand that is larger than 2^32
+# bytes against the same rows alone; small integers, so every sum is exact and
+# the two agree bit for bit whatever tiles they take.
 
 @pytest.mark.parametrize("bits,scales", [(5, "row"), (8, "tile"), (13, "row")])
 def test_rotate_past_32_bits(bits, scales):
