@@ -252,7 +252,13 @@ product_kernel(const ProductArgs p)
     // lies a constant number of rows behind the wave's first.  Descriptors
     // end with the last row's last chunk (a 16-byte aligned chunk that holds
     // a valid byte lies in that byte's page).  What lies past the operand's
-    // last row is past its descriptor; it feeds results that are not stored.
+    // last row is past its descriptor: it reads as 0 and feeds results that
+    // are not stored.  The range check of a raw buffer compares the lane's
+    // offset with the descriptor's size less the scalar offset; a scalar offset
+    // past the size would wrap that difference, so none may be: a piece that
+    // begins behind the last row begins at the last row instead (piece_a; a
+    // lane then reads that row or is out of range), or, where a step's rows are
+    // those of k, its offset is cut to the size (within).
     const int64_t kround = (p.kbytes + 15) & ~(int64_t)15;
     const int lr = lane >> 3, lc = slot(wave * 8 + (lane >> 3), lane & 7);
     const int ra0 = row_of(wave * 8 + lr, TM * 16);
@@ -387,6 +393,22 @@ product_kernel(const ProductArgs p)
     if (SM == kTileScale && sw * 64 >= BM)
         sat /= kFfnBlock;
     const unsigned vs = (unsigned)(sat < sn ? sat : sn - 1) * 4;
+    const auto within = [](unsigned off, v4i rsrc) __attribute__((always_inline)) {
+        return off < (unsigned)rsrc[2] ? off : (unsigned)rsrc[2];
+    };
+    unsigned piece_a[GA], piece_b[GB];       // where the pieces' rows begin
+#pragma unroll
+    for (int g = 0; g < GA; ++g) {
+        const int row = row_of(g * 8 * W, TM * 16);
+        piece_a[g] = AT ? (unsigned)(g * 16 * p.lda)
+                        : (unsigned)((row < mrows ? row : mrows - 1) * p.lda);
+    }
+#pragma unroll
+    for (int g = 0; g < GB; ++g) {
+        const bool up = kDual && g >= GB / 2;
+        const int row = (up ? g - GB / 2 : g) * 8 * W;
+        piece_b[g] = (unsigned)((row < nrows ? row : nrows - 1) * (up ? p.ldb1 : p.ldb0));
+    }
     auto stage = [=](int kt) __attribute__((always_inline)) {
         const bool second = BT && p.parts > 1 && kt >= nks;
         const int ks = second ? kt - nks : kt;
@@ -398,15 +420,14 @@ product_kernel(const ProductArgs p)
 #pragma unroll
         for (int g = 0; g < GA; ++g)
             load_to_lds(da, base + g * W * 1024, va,
-                        AT ? (unsigned)(g * 16 * p.lda)
-                           : so + (second ? (unsigned)p.part_a : 0u) +
-                                 (unsigned)(row_of(g * 8 * W, TM * 16) * p.lda));
+                        AT ? within(piece_a[g], da)
+                           : so + (second ? (unsigned)p.part_a : 0u) + piece_a[g]);
 #pragma unroll
         for (int g = 0; g < GB; ++g) {
             const bool up = kDual && g >= GB / 2;
             load_to_lds(up ? ru : db, base + (BM + g * 8 * W) * kStep, up || second ? vu : vb,
-                        BT ? (unsigned)(g * 16 * (second ? p.ldb1 : p.ldb0))
-                           : so + (unsigned)((up ? g - GB / 2 : g) * 8 * W * (up ? p.ldb1 : p.ldb0)));
+                        BT ? within((unsigned)(g * 16 * (second ? p.ldb1 : p.ldb0)), db)
+                           : so + piece_b[g]);
         }
         if constexpr (SM != kNoScale)
             load4_to_lds(make_rsrc(sbase + (int64_t)ks * sn, (uint64_t)sn * 4),
