@@ -38,7 +38,7 @@ __device__ __forceinline__ void load_to_lds(v4i rsrc, unsigned lds, unsigned vof
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, %3 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc), "s"(soff)
-                 : "memory");
+                 : "memory", "m0");
 }
 // The same, four bytes a lane.
 __device__ __forceinline__ void load4_to_lds(v4i rsrc, unsigned lds, unsigned voff)
@@ -46,7 +46,7 @@ __device__ __forceinline__ void load4_to_lds(v4i rsrc, unsigned lds, unsigned vo
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dword %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(voff), "s"(rsrc)
-                 : "memory");
+                 : "memory", "m0");
 }
 // Waits until at most the last N memory operations of the wave are unfinished.
 template <int N>
