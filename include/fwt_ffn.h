@@ -117,8 +117,13 @@ int fwt_gated_ffn(const void* x, int64_t ldx, const float* x_scales, const void*
  *   dx = dg gate + du up,  dgate = dg^T x,  dup = du^T x,
  *   dg = dh * up' * act'(g),  du = dh * act(g),  g = x gate^T, up' = x up^T.
  * g and up' are computed again in 32 bits, not stored by the forward pass;
- * dg and du are rounded to the dtype for the matrix products.  All arrays
- * have the dtype; ldx, ldgate and ldup are below 2^22, n below 2^21 and the
+ * dg and du are rounded to the dtype once for the matrix products, as a
+ * program that stores them would (bf16: the gradients' error in norm is about
+ * sqrt(2) of their own rounding's).  f16: where the largest finite one is above
+ * 65504 or below 2^-12 both are stored times a power of two that the products
+ * take out again, so they lose bits only below 2^-29 of the largest (otherwise
+ * below 2^-14) and the gradients overflow only where they are past the type's
+ * range themselves.  All arrays have the dtype; ldx, ldgate and ldup are below 2^22, n below 2^21 and the
  * three products have fewer than 2^22 tiles (FWT_EUNSUPPORTED).  ws: scratch of fwt_gated_ffn_backward_workspace bytes,
  * 16-byte aligned, one for each call that may run at the same time. */
 int fwt_gated_ffn_backward_workspace(int64_t m, int64_t n, int64_t k, size_t* bytes);

@@ -230,6 +230,36 @@ __device__ __forceinline__ void store4(void* c, int64_t at, v4f v, int type, int
     }
 }
 
+// f16 gradients between two products.  dg and du are rounded to f16 for the
+// matrix cores, whose range (65504 down to steps of 2^-24) the products' results
+// need not share: where the largest of them is past it, or so small that half a
+// step is more than 2^-13 of it, both are stored times 2^-e with the largest
+// near 2^14, and the products that read them multiply their sums by 2^e (both
+// exact).  Otherwise e is 0.
+constexpr float kRangeHigh = 65504.0f, kRangeLow = 0x1p-12f;
+
+// A lane's largest finite magnitude (bits, not 0) into the range.
+__device__ __forceinline__ void note_range(GradRange* r, unsigned top)
+{
+    // most store one and the same word; a maximum has no order
+    if (top >= __float_as_uint(kRangeLow) && top <= __float_as_uint(kRangeHigh))
+        r->within = 1;
+    else
+        atomicMax(&r->top, top);
+}
+__device__ __forceinline__ int range_exponent(const GradRange* r)
+{
+    const unsigned top = r->top;
+    if (top == 0 || (top <= __float_as_uint(kRangeHigh) && r->within))
+        return 0;
+    const int e = (int)(top >> 23) - 127 - 14;      // (a subnormal: -141)
+    return e > -100 ? e : -100;
+}
+__device__ __forceinline__ float power_of_two(int e)
+{
+    return __uint_as_float((unsigned)(e + 127) << 23);
+}
+
 // Four 16-bit values from p[at ..], 0 past cnt.
 typedef unsigned short v4h __attribute__((ext_vector_type(4)));
 __device__ __forceinline__ v4h load4(const void* p, int64_t at, int cnt)

@@ -32,6 +32,14 @@ enum FfnEpilogue : int {
     kEpStoreT = 3,    // 16-bit operands: kEpStore with A stored [k][m] too
 };
 
+// The largest finite magnitude of dg and du in f16, as far as it matters (the
+// factor that they are stored with goes by it): a bit pattern, of values above
+// the type's range or below kRangeLow only, and whether there are others.
+struct GradRange {
+    uint32_t top;
+    uint32_t within;
+};
+
 // One product A B^T (A: m x k, B: n x k, both with k contiguous), or two
 // that share A.  Strides of a and b in bytes, of the others in elements.
 struct ProductArgs {
@@ -57,6 +65,9 @@ struct ProductArgs {
     const void* dh;         // kEpGateGrad: gradient of C, m x n
     int64_t lddh;
     int act;                // 0 silu, 1 gelu
+    GradRange* range;       // f16 gradients: of dg and du (kEpGateGrad sets
+                            // it, the products that read them go by it)
+    int again;              // kEpGateGrad: only where range asks for a factor
     int may_split;          // partial has product_workspace bytes
     void* partial;
     int tiles_m, tiles_n, splits;   // set by the launcher

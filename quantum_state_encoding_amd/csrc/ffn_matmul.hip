@@ -126,6 +126,17 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (
     const auto count_at = [=](int nc) __attribute__((always_inline)) {
         return WHOLE || nrows - nc > 4 ? 4 : nrows - nc;
     };
+    // f16 gradients: the factor that dg and du are stored with, or that the
+    // sums of what was stored so are multiplied by
+    constexpr bool kGrad16 = EP == kEpGateGrad && TYPE == kTF16;
+    float factor = 1.0f;
+    if constexpr (TYPE == kTF16 && EP != kEpGate) {
+        if (EP == kEpStore)
+            factor = power_of_two(range_exponent(p.range));
+        else if (p.again)
+            factor = power_of_two(-range_exponent(p.range));
+    }
+    float top = 0.0f;      // the largest finite magnitude
     // All of dh before the first store (a load behind a store that may be to
     // the same address waits for memory each time).
     v4h dh[EP == kEpGateGrad ? NI : 1][TJ];
@@ -174,13 +185,30 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (
                         const float g = from16(dh[i][j][k], ctype == kTBf16);
                         v[k] = g * acc[i][j + TN / 2][k] * d;
                         u[k] = g * f;
+                        if constexpr (kGrad16) {
+                            // (past the last column g is 0)
+                            const float a = __builtin_fabsf(v[k]), b = __builtin_fabsf(u[k]);
+                            top = __builtin_fmaxf(top, a < __builtin_inff() ? a : 0.0f);
+                            top = __builtin_fmaxf(top, b < __builtin_inff() ? b : 0.0f);
+                            v[k] *= factor;
+                            u[k] *= factor;
+                        }
                     }
                 }
+            } else if constexpr (TYPE == kTF16) {
+                v *= factor;
             }
             if constexpr (EP == kEpGateGrad)
                 store4(c, at + p.part_c, u, ctype, count_at(nc));
             store4(c, at, v, ctype, count_at(nc));
         }
+        // (rows side by side would need more registers than there are)
+        if constexpr (kGrad16)
+            __builtin_amdgcn_sched_barrier(0);
+    }
+    if constexpr (kGrad16) {
+        if (!p.again && top != 0.0f)
+            note_range(p.range, __float_as_uint(top));
     }
 }
 
@@ -227,6 +255,10 @@ product_kernel(const ProductArgs p)
     static_assert(BM % (8 * W) == 0 && BNO % (8 * W) == 0, "whole 8-row groups per wave");
     extern __shared__ __align__(16) unsigned char lds[];
 
+    if constexpr (TYPE == kTF16 && EP == kEpGateGrad) {
+        if (p.again && range_exponent(p.range) == 0)
+            return;
+    }
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(((int)threadIdx.x >> 6) % W);
     const int kg = __builtin_amdgcn_readfirstlane((int)threadIdx.x / (64 * W));
@@ -648,6 +680,10 @@ __global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
     constexpr int P = EP != kEpStore ? 2 : 1, TJ = TN / P;
     constexpr int kAhead = 8;
+    if constexpr (TYPE == kTF16 && EP == kEpGateGrad) {
+        if (p.again && range_exponent(p.range) == 0)
+            return;
+    }
     const int64_t stride = (int64_t)gridDim.x * (TM * TN * 64 * W);
     const int i = (int)blockIdx.y, j = (int)blockIdx.z;
     const v4f* in = (const v4f*)p.partial + (int64_t)blockIdx.x * (TM * TN * 64 * W) +
@@ -703,8 +739,11 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
             return e;
     }
     const unsigned tiles = (unsigned)(p.tiles_m * p.tiles_n);
-    hipLaunchKernelGGL(k, dim3(tiles, (unsigned)splits), dim3(64 * WM * WN * WK), kLds, stream, p);
-    const hipError_t e = hipGetLastError();
+    hipError_t e = hipSuccess;
+    if (splits == 1 || !p.again) {           // (the shares' sums are still there)
+        hipLaunchKernelGGL(k, dim3(tiles, (unsigned)splits), dim3(64 * WM * WN * WK), kLds, stream, p);
+        e = hipGetLastError();
+    }
     if (splits == 1 || e != hipSuccess)
         return e;
     if constexpr (BM <= 128 && BN <= 128) {      // (larger tiles are never split)

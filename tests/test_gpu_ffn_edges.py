@@ -75,3 +75,125 @@ def test_rows_behind_an_operand_are_not_used(m, n, k):
         assert torch.equal(qse.gated_ffn(fx, fg, fu), h)
         got = qse.gated_ffn_backward(fx, fg, fu, before_nan(dh, n + 3, 2))
         assert all(torch.equal(p, q) for p, q in zip(got, grads))
+
+
+# ---- the range of f16 gradients --------------------------------------------
+
+def act64(name, g):
+    if name == "silu":
+        p = torch.sigmoid(g)
+        return g * p, p + g * p * (1 - p)
+    p = 0.5 * torch.special.erfc(-g / math.sqrt(2))
+    return g * p, p + g * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi)
+
+
+# standard deviations of x, gate, up and dh: dg up to about 1e6 beside gradients
+# of some thousands; dg and du below 1e-5 beside gradients of about 1e-4
+RANGES = {"high": (1e-3, 1e-3, 3e4, 1e4), "low": (1e3, 1e-3, 1e-3, 2.0 ** -22)}
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 1, 70), (16, 64, 8016), (65, 100, 130), (5, 7, 40),
+                                   (300, 512, 256), (64, 4100, 200), (1030, 700, 515),
+                                   (2100, 1600, 136), (2600, 72, 5120), (70, 2051, 133)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("span", ["high", "low"])
+def test_f16_gradients_past_the_range_of_dg(m, n, k, act, span):
+    say("f16 range", m, n, k, act, span)
+    g = gen(m + n + k)
+    sx, sg, su, sh = RANGES[span]
+    dt = torch.float16
+    if span == "high":
+        su = su / math.sqrt(k)
+    else:
+        sg, su = sg / math.sqrt(k), su / math.sqrt(k)
+    x, wg, wu = ((torch.randn(r, k, generator=g, device="cuda") * s).to(dt)
+                 for r, s in ((m, sx), (n, sg), (n, su)))
+    dh = (torch.randn(m, n, generator=g, device="cuda") * sh).to(dt)
+    got = qse.gated_ffn_backward(x, wg, wu, dh, act=act)
+    xd, gd, ud, hd = (t.double() for t in (x, wg, wu, dh))
+    gg, u = xd @ gd.t(), xd @ ud.t()
+    eg, eu = ((k + 2) * 2 * U * (xd.abs() @ w.abs().t()) for w in (gd, ud))
+    f, d = act64(act, gg)
+    dg, du = hd * u * d, hd * f
+    top = float(torch.maximum(dg.abs().max(), du.abs().max()))
+    # as in test_gated_backward (|act''| <= 0.8, |act'| <= 1.13, 2^-21 (|g| + 1)
+    # for the activation); |g| is small, where |f| <= |g| keeps that relative
+    ea = 2.0 ** -21 * (gg.abs() + 1)
+    ef = 1.13 * eg + torch.minimum(ea, 2.0 ** -20 * gg.abs())
+    e_dg = hd.abs() * (eu * (d.abs() + ea) + u.abs() * (0.8 * eg + ea))
+    e_du = hd.abs() * ef
+    # half a step of f16, or of the smallest one: 2^-25, with a factor that puts
+    # the largest value above 2^14 2^-39 of that value
+    tiny = 2.0 ** -25 if 2.0 ** -12 * 1.01 < top < 65504 * 0.99 else 2.0 ** -39 * top * 1.01
+    e_dg = e_dg + (half(dt) + 4 * U) * (dg.abs() + e_dg) + tiny
+    e_du = e_du + (half(dt) + 4 * U) * (du.abs() + e_du) + tiny
+
+    def check(name, out, terms, count):
+        want = sum(a @ b for a, b, _ in terms)
+        tol = sum(e @ b.abs() + count * 2 * U * ((a.abs() + e) @ b.abs()) for a, b, e in terms)
+        tol = tol + half(dt) * (want.abs() + tol) + 2.0 ** -25
+        assert float((want.abs() + tol).max()) < 65504, name
+        assert bool(((out.double() - want).abs() <= tol).all()), name
+        return float(want.abs().max())
+    check("dx", got[0], [(dg, gd, e_dg), (du, ud, e_du)], 2 * n + 2)
+    most = check("dgate", got[1], [(dg.t(), xd, e_dg.t())], m + 2)
+    check("dup", got[2], [(du.t(), xd, e_du.t())], m + 2)
+    if m * n > 1000:      # the case is what it stands for
+        assert top > 65520 if span == "high" else top < 2.0 ** -14 < most * 16
+    again = qse.gated_ffn_backward(x, wg, wu, dh, act=act)
+    assert all(torch.equal(a, b) for a, b in zip(got, again))
+
+
+def bits(t):
+    return t.view(torch.int16)
+
+
+def test_f16_gradients_beside_infinite_ones():
+    # A dh that is infinite makes its own row of dx and of the weights'
+    # gradients not finite, and no factor: the other rows keep their bits.
+    # (3e4 times a normal value is past the type in some places already, and
+    # with up thirty times as large dg is past it)
+    say("f16 infinite dh")
+    g = gen(5)
+    x, wg, wu = (torch.randn(r, 136, generator=g, device="cuda").half() * 0.1 for r in (150, 90, 90))
+    for scale, more in ((1.0, 1), (3e4, 1), (5e3, 30)):
+        dh = (torch.randn(150, 90, generator=g, device="cuda") * scale).half()
+        want = qse.gated_ffn_backward(x, wg, wu * more, dh)
+        assert scale == 3e4 or bool(torch.isfinite(want[1]).all())
+        dh[7, 5] = float("inf")
+        dx, dg, du = qse.gated_ffn_backward(x, wg, wu * more, dh)
+        keep = [i for i in range(150) if i != 7]
+        assert torch.equal(bits(dx[keep]), bits(want[0][keep]))
+        assert not bool(torch.isfinite(dx[7]).all())
+        keep = [i for i in range(90) if i != 5]
+        assert torch.equal(bits(dg[keep]), bits(want[1][keep]))
+        assert torch.equal(bits(du[keep]), bits(want[2][keep]))
+        assert not bool(torch.isfinite(dg[5]).all()) and not bool(torch.isfinite(du[5]).all())
+
+
+def test_f16_range_in_a_graph():
+    # one graph, replayed on gradients of each range in turn
+    say("f16 range graph")
+    g = gen(6)
+    x = (torch.randn(70, 256, generator=g, device="cuda") * 1e-3).half()
+    wg = (torch.randn(96, 256, generator=g, device="cuda") * 1e-3).half()
+    wu = (torch.randn(96, 256, generator=g, device="cuda") * 2e3).half()
+    dh = torch.randn(70, 96, generator=g, device="cuda").half()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        qse.gated_ffn_backward(x, wg, wu, dh)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = qse.gated_ffn_backward(x, wg, wu, dh)
+    seen = set()
+    for scale in (1.0, 1e4, 1e-6, 1.0, 3e4, 0.0, 1e-6):
+        dh.copy_(torch.randn(70, 96, generator=g, device="cuda") * scale)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = qse.gated_ffn_backward(x, wg, wu, dh)
+        torch.cuda.synchronize()
+        assert all(torch.equal(bits(a), bits(b)) for a, b in zip(out, want)), scale
+        seen.add(float(out[1].float().norm()))
+    assert len(seen) == 7
