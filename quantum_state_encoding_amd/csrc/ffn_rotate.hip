@@ -156,6 +156,20 @@ __device__ __forceinline__ v4i encode(const float* v, float s, float inv)
     return out;
 }
 
+// Sixteen codes at p, the first `left` of which are the row's: the others are
+// its padding, 0 whatever the block's scale (0 / NaN would be NaN).
+__device__ __forceinline__ void put_codes(uint8_t* p, v4i c, int64_t left)
+{
+    if (left < 16) {
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+            const int b = (int)left - 4 * w;
+            c[w] = b >= 4 ? c[w] : b <= 0 ? 0 : c[w] & ((1 << (8 * b)) - 1);
+        }
+    }
+    *(v4i*)p = c;
+}
+
 // What follows a rotation, whose factor `norm` (exact: a power of two) is
 // still to come: maximum, scale and codes of block kb of a row.  `part` of the
 // block's 128 / N lanes has N of its elements.  A power of two moves into the
@@ -191,8 +205,11 @@ __device__ __forceinline__ void finish(const RotateArgs& p, float (&v)[N], float
 #pragma unroll
     for (int h = 0; h < N; h += 16) {
         const v4i c = encode(v + h, sv, inv);
-        if (live && kb * kFfnBlock + part * N + h < p.k)
-            *(v4i*)(p.q + row * p.ldq + kb * kFfnBlock + part * N + h) = c;
+        const int64_t k = kb * kFfnBlock + part * N + h;
+        if (live && k < p.k) {
+            // (rotations of more than a block have rows of whole ones)
+            put_codes(p.q + row * p.ldq + k, c, N == 16 ? p.k - k : 16);
+        }
     }
 }
 
@@ -560,7 +577,7 @@ __global__ __launch_bounds__(1024) void tile_kernel(const RotateArgs p, float no
             p.s[kb * ((p.m + kFfnBlock - 1) / kFfnBlock) + mb] = s;
         const v4i c = encode(v, s, 1.0f / s);
         if (live && k0 < p.k)
-            *(v4i*)(p.q + row * p.ldq + k0) = c;
+            put_codes(p.q + row * p.ldq + k0, c, p.k - k0);
     }
 }
 
@@ -655,7 +672,7 @@ tile_t16_kernel(const RotateArgs p, float norm)
             const int64_t k = kb * 128 + q * 32 + e * 16;
             const v4i code = encode(v + e * 16, s, inv);
             if (row < p.m && k < p.k)
-                *(v4i*)(p.q + row * p.ldq + k) = code;
+                put_codes(p.q + row * p.ldq + k, code, p.k - k);
         }
     };
     if constexpr (!TILE) {

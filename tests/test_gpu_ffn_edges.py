@@ -197,3 +197,26 @@ def test_f16_range_in_a_graph():
         assert all(torch.equal(bits(a), bits(b)) for a, b in zip(out, want)), scale
         seen.add(float(out[1].float().norm()))
     assert len(seen) == 7
+
+
+# ---- padding ----------------------------------------------------------------
+
+@pytest.mark.parametrize("k", [1, 7, 15, 17, 127, 130, 200, 1000])
+@pytest.mark.parametrize("scales", ["row", "tile"])
+@pytest.mark.parametrize("transpose", [False, True])
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_padding_is_zeros_beside_values_that_are_not_finite(k, scales, transpose, dtype):
+    say("padding", k, scales, transpose, dtype)
+    m = 131
+    for bits in range(4):
+        if k % (1 << bits):
+            break
+        x = torch.randn(m, k, generator=gen(k), device="cuda").to(DT[dtype])
+        x[3, k - 1], x[130, 0], x[64, k // 2] = float("nan"), float("inf"), -float("inf")
+        arg = x.t().contiguous() if transpose else x
+        q, s = qse.rotate_quantize(arg, bits=bits, scales=scales, transpose=transpose)
+        ld = q.stride(0)
+        assert ld == cdiv(k, 16) * 16
+        whole = torch.as_strided(q.view(torch.uint8), (m, ld), (ld, 1))
+        assert bool((whole[:, k:] == 0).all())
+        assert bool(torch.isnan(q[3, k - 1].float())) and bool(torch.isnan(s).any())
