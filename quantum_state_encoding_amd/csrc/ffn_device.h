@@ -284,8 +284,10 @@ __device__ __forceinline__ v4h load4(const void* p, int64_t at, int cnt)
 // with s = 1 / (1 + e^-g); for e^-g past the fp32 range s is 0.  gelu: g P
 // and P + g e^(-g^2/2) / sqrt(2 pi) with P the normal distribution
 // function, from erfc so that the lower tail keeps its relative precision.
-// The hardware's exponential and reciprocal (about one unit in the last
-// place of fp32) are far below the 16-bit rounding of the result.
+// The hardware's exponential and reciprocal (about one unit in the last place
+// of fp32, of an argument that is rounded: 2^-23 |g| or g^2 of the result) are
+// far below the 16-bit rounding of the result; an fp32 result takes
+// activation_exact.
 __device__ __forceinline__ void activation(int act, float g, float& f, float& d)
 {
     if (act == 0) {
@@ -298,6 +300,25 @@ __device__ __forceinline__ void activation(int act, float g, float& f, float& d)
         f = g * p;
         d = p + g * 0.39894228f * __builtin_amdgcn_exp2f(g * g * -0.72134752f);
     }
+}
+
+// act(g) to a few units in the last place of fp32 at any g.  silu: with
+// z = e^-|g|, which does not overflow, s is 1 / (1 + z) or z / (1 + z).  gelu:
+// the argument of erfc is rounded to t, and r is what that lost; near t erfc
+// changes by -2 / sqrt(pi) e^(-t^2) r, which in the lower tail is 2 t r of it.
+__device__ __forceinline__ float activation_exact(int act, float g)
+{
+    if (act == 0) {
+        const float z = expf(-__builtin_fabsf(g));
+        return g * ((g < 0.0f ? z : 1.0f) / (1.0f + z));
+    }
+    constexpr float kHigh = 0.707106769f, kLow = 1.21016171e-8f;   // their sum: 2^(-1/2)
+    const float t = g * -kHigh;
+    float p = erfcf(t);
+    const float r = __builtin_fmaf(g, -kHigh, -t) - g * kLow;
+    if (t > 0.0f && t < 20.0f)
+        p -= 1.12837917f * expf(-t * t) * r;
+    return g * (0.5f * p);
 }
 
 }  // namespace

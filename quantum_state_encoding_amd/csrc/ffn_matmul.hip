@@ -178,7 +178,10 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
                     float f, d;
-                    activation(act, acc[i][j][k], f, d);
+                    if constexpr (TYPE == kTE4m3Exact)
+                        f = activation_exact(act, acc[i][j][k]);
+                    else
+                        activation(act, acc[i][j][k], f, d);
                     if constexpr (EP == kEpGate) {
                         v[k] = f * acc[i][j + TN / 2][k];
                     } else {

@@ -203,7 +203,10 @@ __global__ __launch_bounds__(64 * W) void strip_kernel(const ProductArgs p)
         float v = s[0];
         if constexpr (EP == kEpGate) {
             float d;
-            activation(p.act, s[0], v, d);
+            if constexpr (TYPE == kTE4m3Exact)
+                v = activation_exact(p.act, s[0]);
+            else
+                activation(p.act, s[0], v, d);
             v *= s[P - 1];
         }
         const int64_t o = mm * p.ldc + n;

@@ -220,3 +220,92 @@ def test_padding_is_zeros_beside_values_that_are_not_finite(k, scales, transpose
         whole = torch.as_strided(q.view(torch.uint8), (m, ld), (ld, 1))
         assert bool((whole[:, k:] == 0).all())
         assert bool(torch.isnan(q[3, k - 1].float())) and bool(torch.isnan(s).any())
+
+
+# ---- the activations, relative to their values ------------------------------
+
+def gates(act):
+    """Gates a + b / 16 (exact in e4m3, bf16 and f16 products), down to where
+    act underflows fp32 and up to where it is the gate."""
+    low = -104 if act == "silu" else -14
+    a = [8.0 * i for i in range(low // 8, 3)] if act == "silu" else []
+    a += [float(i) for i in range(-15, 16)]
+    return [(c, b) for c in a for b in range(0, 16, 1 if abs(c) < 16 else 5) if c + b / 16 >= low]
+
+
+def act_relative(act, g, exact):
+    """The activation's error relative to its value.  Hardware exponential and
+    reciprocal: a unit (2 U) each, three roundings, and the argument's rounding
+    and its constant's, 1.25 U each, times |g| (silu) or g^2 (2 t^2 = g^2 of
+    erfc).  Library functions: exp 3 units, erfc 16; the argument of erfc is
+    corrected."""
+    if exact:
+        return (6 * 2 * U if act == "silu" else 20 * 2 * U) + 0 * g
+    if act == "silu":
+        return (8 + 1.25 * g.abs()) * U
+    return (16 * 2 + 4 + 2.5 * g * g) * U
+
+
+def gate_case(act, dtype, k):
+    """x, gate (one row), up (one row) with x gate^T the gates and x up^T = 7."""
+    ab = torch.tensor(gates(act), device="cuda")
+    x = torch.zeros(len(ab), k, device="cuda")
+    x[:, :2], x[:, 2] = ab, 1
+    gate, up = torch.zeros(1, k, device="cuda"), torch.zeros(1, k, device="cuda")
+    gate[0, 0], gate[0, 1], up[0, 2] = 1, 1 / 16, 7
+    g = ab[:, 0].double() + ab[:, 1].double() / 16
+    out = [t.to(dtype) for t in (x, gate, up)]
+    assert all(torch.equal(t.float(), w) for t, w in zip(out, (x, gate, up)))
+    return (*out, g)
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+def test_e4m3_activation_relative_to_its_value(act, out):
+    say("activation e4m3", act, out)
+    x, gate, up, g = gate_case(act, F8, 16)
+    want = act64(act, g)[0] * 7
+    for rows in (slice(0, 13), slice(0, len(g))):
+        one = lambda n: torch.ones(1, n, device="cuda")
+        h = qse.gated_ffn(x[rows], gate, up, act=act, x_scales=one(len(g[rows])),
+                          gate_scales=one(1), up_scales=one(1), out_dtype=DT[out])
+        err = (h[:, 0].double() - want[rows]).abs()
+        rel = act_relative(act, g[rows], out == "f32") + half(DT[out])
+        # What underflows.  fp32: below 2^-126 a unit is 2^-149 whatever the
+        # value, so e^-|g| (3 units), its quotient (1) or erfc (16, its
+        # correction 1, half of it) are off by at most 17 * 2^-149, and act by
+        # |g| times that.  The hardware's exponential gives 0 below 2^-126.
+        low = (17 * g[rows].abs() + 1) * 7 * 2.0 ** -149 if out == "f32" else (
+            0 * g[rows] + 7 * 2.0 ** -119)
+        low = low + (2.0 ** -25 if out == "f16" else 0.0)
+        bad = ~(err <= rel * want[rows].abs() + low)
+        assert not bool(bad.any()), (g[rows][bad][:5], err[bad][:5] / want[rows][bad].abs()[:5])
+
+
+@pytest.mark.parametrize("k", [3, 20, 64])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_activation_and_slope_relative_to_their_values(k, act, dtype):
+    say("activation", k, act, dtype)
+    dt = DT[dtype]
+    x, gate, up, g = gate_case(act, dt, k)
+    f, d = act64(act, g)
+    low = 2.0 ** -25 if dtype == "f16" else 2.0 ** -115
+    for rows in (slice(0, 13), slice(0, len(g))):
+        h = qse.gated_ffn(x[rows], gate, up, act=act)[:, 0].double()
+        rel = act_relative(act, g[rows], False) + half(dt)
+        assert bool(((h - f[rows] * 7).abs() <= rel * f[rows].abs() * 7 + low).all())
+    # one column, so that dx holds dg (times 1) and du (times 7), each rounded
+    # once before the product and once after it
+    dh = torch.ones(len(g), 1, device="cuda").to(dt)
+    dx = qse.gated_ffn_backward(x, gate, up, dh, act=act)[0].double()
+    rel = act_relative(act, g, False)
+    twice = 2.5 * half(dt)
+    assert bool(((dx[:, 2] - f * 7).abs() <= (rel + twice) * f.abs() * 7 + 8 * low).all())
+    # the slope is a sum of two terms, each with that error: s or P, and g
+    # times s (1 - s) or the normal density
+    terms = torch.sigmoid(g) + f.abs() if act == "silu" else (
+        0.5 * torch.special.erfc(-g / math.sqrt(2)) +
+        g.abs() * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi))
+    tol = (rel + 2 * U) * terms * 7 + twice * (d.abs() * 7) + 8 * low
+    assert bool(((dx[:, 0] - d * 7).abs() <= tol).all())
