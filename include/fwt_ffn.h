@@ -77,10 +77,12 @@ int fwt_rotate_quantize(const void* x, fwt_ffn_dtype dtype, int64_t m, int64_t k
 
 /* c[i][j] = sum_k a[i][k] b[j][k]: a is m x k codes with row scales, b is
  * n x k codes with scales of either kind, c bf16, f16 or fp32.  Sums are in
- * 32 bits; the scales of a block multiply its 128-element sum.  For a 16-bit
- * c the products go through the 8-bit matrix instruction, which keeps each
- * to 2^-13 of the largest of 8 neighbours; for fp32 through the 16-bit one,
- * which keeps all of it, at half the rate.  A row of a
+ * 32 bits; the scales of a block multiply its 128-element sum.  For f16 and
+ * fp32 the products go through the 16-bit matrix instruction, which keeps all
+ * of them.  For bf16 they go through the 8-bit one at twice the rate, which
+ * cuts each towards zero to a step of 2^-13 of the largest of 8 neighbours
+ * along k: together at most 7 * 2^-13 of that largest one, a fifth of bf16's
+ * rounding where all products have one sign.  A row of a
  * or b is read up to k only, whatever its padding holds.  The strides lda
  * and ldb are multiples of 16 below 2^23, a and b 16-byte aligned
  * (FWT_EALIGN; a longer stride, or more than 2^22 tiles of 128 x 64 results,

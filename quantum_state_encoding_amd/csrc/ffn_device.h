@@ -70,11 +70,14 @@ __device__ __forceinline__ v8h widen(int lo, int hi)
 // 128 e4m3 elements, or two of 32 16-bit ones (a and b: [0] and [1]).
 //
 // The 8-bit instruction cuts each product, towards zero, to a step of 2^-13
-// of the largest of its eight neighbours along k (1.4e-5 of a sum of Gaussian
-// values in norm, measured; between the eights it keeps 32 bits): far below
-// the rounding of a 16-bit result, not of an fp32 one.  kTE4m3Exact widens the
-// codes for the f16 instruction, whose products and sums lose nothing but
-// fp32's rounding, at half its rate.
+// of the largest of its eight neighbours along k (between the eights it keeps
+// 32 bits): seven of them lose up to 7 * 2^-13 = 8.5e-4 of that largest one,
+// and with products of one sign the result loses as much (6.5e-4 measured with
+// one large product in each eight; zero-mean Gaussian codes lose 1.4e-5 in
+// norm).  That is 0.22 of half a step of bf16, whose results take it, but 1.75
+// of f16's.  kTE4m3Exact, for f16 and fp32 results, widens the codes for the
+// f16 instruction, whose products and sums lose nothing but fp32's rounding,
+// at half its rate.  (The 8-bit 16x16x32 instruction cuts as the 128 one does.)
 template <int TYPE>
 __device__ __forceinline__ v4f matrix_step(const v4i* a, const v4i* b, v4f acc)
 {

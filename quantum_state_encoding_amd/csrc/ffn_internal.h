@@ -13,7 +13,8 @@ constexpr int kFfnMaxBits = 14;       // log2 of the largest rotation
 constexpr int kFfnMaxBitsT = 7;       // the same, for a transposed input
 
 // Element types, as fwt_ffn_dtype numbers them.
-// kTE4m3Exact: e4m3 operands whose products and sums keep 32 bits.
+// kTE4m3Exact: e4m3 operands whose products and sums keep 32 bits, for f16 and
+// fp32 results.
 enum FfnType : int { kTBf16 = 0, kTF16 = 1, kTF32 = 2, kTE4m3 = 3, kTE4m3Exact = 4 };
 
 // Largest row stride of a product's operand, in bytes: 256 rows of a tile

@@ -112,10 +112,10 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const v4f (
     const int64_t m0 = (int64_t)tm * BM, n0 = (int64_t)tn * BNO;
     const int mrows = WHOLE || p.m - m0 > BM ? BM : (int)(p.m - m0);
     const int nrows = WHOLE || p.n - n0 > BNO ? BNO : (int)(p.n - n0);
-    const int ctype = TYPE == kTE4m3Exact ? (int)kTF32
-                      : TYPE != kTE4m3    ? TYPE
-                      : p.ctype == kTBf16 ? (int)kTBf16
-                                          : (int)kTF16;
+    const int ctype = TYPE == kTE4m3        ? (int)kTBf16
+                      : TYPE != kTE4m3Exact ? TYPE
+                      : p.ctype == kTF32    ? (int)kTF32
+                                            : (int)kTF16;
     const int act = ACT < 0 ? p.act : ACT;
     const auto row_at = [=](int i) __attribute__((always_inline)) {
         return wm * (TM * 16) + (AT ? (i0 + i) * 16 + l16 : l16 * TM + i0 + i);
@@ -761,12 +761,13 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
 // two fit) takes about a fixed time for each 128-byte step of k, so a product
 // takes ceil(tiles / slots) of those.  Microseconds a step, measured with full
 // rounds at k of 16384 bytes and more:
-//                                  slots   e4m3   fp32 out   16 bits
+//                                  slots   e4m3   exact(+)   16 bits
 //   256 x 256                        256   1.75      -         1.6
 //   128 x 128, two on a CU           512   1.05     2.0        1.06
 //   128 x 128, deeper (*)            256   0.65     1.1        0.62
 //   64 x 64, two on a CU             512   0.40     0.70        -
 //   64 x 64 (gated: 64 x 128)        256   0.26     0.36       0.42
+// (+) e4m3 with an f16 or fp32 result, through the 16-bit instruction.
 // (*) two groups of waves for e4m3, four rounds in LDS for 16 bits.  So m 512
 // n 4096 k 16384 (e4m3) takes 49 us with 64 x 64 tiles and 82 with 128 x 128
 // ones, m 4096 takes 451 and 260, and 227 with 256 x 256 ones.
@@ -874,8 +875,8 @@ hipError_t pick16(const ProductArgs& p, size_t* query, hipStream_t stream)
     return hipErrorInvalidValue;
 }
 
-// e4m3 operands.  The widened operands of an fp32 result, or a scale for each
-// row of B, leave no registers for the largest tile.
+// e4m3 operands.  The widened operands of an f16 or fp32 result, or a scale for
+// each row of B, leave no registers for the largest tile.
 template <int TYPE, int EP, int SM>
 hipError_t pick8(const ProductArgs& p, size_t* query, hipStream_t stream)
 {
@@ -905,8 +906,8 @@ hipError_t pick8(const ProductArgs& p, size_t* query, hipStream_t stream)
         else
             return run<TYPE, 64, 64, 2, 2, 2, 2, EP, SM>(p, 1, stream);
     case 4:
-        // (fp32 results: four groups of waves 10-15 % faster than two with
-        // four rounds in LDS; 16-bit results 5-10 % slower)
+        // (f16 and fp32 results: four groups of waves 10-15 % faster than two
+        // with four rounds in LDS; bf16 results 5-10 % slower)
         if constexpr (!dual)
             return run<TYPE, 64, 64, 2, 2, exact ? 4 : 2, exact ? 2 : 4, EP, SM>(p, c.splits, stream);
     }
@@ -939,8 +940,8 @@ hipError_t tiles_for(const ProductArgs& p, int type, int ep, bool row_scales, si
                      hipStream_t stream)
 {
     if (type == kTE4m3)
-        return p.ctype == kTF32 ? launch8<kTE4m3Exact>(p, ep, row_scales, query, stream)
-                                : launch8<kTE4m3>(p, ep, row_scales, query, stream);
+        return p.ctype != kTBf16 ? launch8<kTE4m3Exact>(p, ep, row_scales, query, stream)
+                                 : launch8<kTE4m3>(p, ep, row_scales, query, stream);
     return type == kTBf16 ? launch16<kTBf16>(p, ep, query, stream)
                           : launch16<kTF16>(p, ep, query, stream);
 }
@@ -949,12 +950,18 @@ hipError_t tiles_for(const ProductArgs& p, int type, int ep, bool row_scales, si
 // shared rows of A pay: e4m3 n 16384 k 4096 takes 13.3 us with tiles and 18.0
 // with strips at m = 16 (12.5 and 13.1 at m = 1), n 4096 k 16384 33 and 19;
 // gated bf16 n 16384 k 4096 takes 53 and 66 us at m = 32, 52 and 51 at 16.
-bool strips(const ProductArgs& p, int type, int ep)
+// A tile widens all its codes for an f16 or fp32 result, used or not, a strip
+// those it reads: n 16384 k 4096 takes 17.3 us with tiles and 12.9 with strips
+// at m = 1, 17.9 and 15.1 at 8, 17.9 and 18.0 at 16 (tile scales; with row
+// scales 18.1, 18.4 and 18.5, and 17.6, 19.8 and 22.4).
+bool strips(const ProductArgs& p, int type, int ep, bool row_scales)
 {
     if (p.m > kStripRows || ep == kEpGateGrad || (ep != kEpGate && type != kTE4m3))
         return false;
-    const bool fills = (p.n + 63) / 64 >= 256;
-    return !fills || (ep == kEpGate && p.m <= 16 && (p.n + 15) / 16 < kFfnMaxTiles);
+    if ((p.n + 63) / 64 < 256)
+        return true;
+    const bool few = ep == kEpGate ? p.m <= 16 : p.ctype != kTBf16 && !row_scales && p.m <= 8;
+    return few && (p.n + 15) / 16 < kFfnMaxTiles;
 }
 
 }  // namespace
@@ -962,7 +969,7 @@ bool strips(const ProductArgs& p, int type, int ep)
 hipError_t launch_product(const ProductArgs& p, int type, int ep, bool row_scales,
                           hipStream_t stream)
 {
-    if (strips(p, type, ep))
+    if (strips(p, type, ep, row_scales))
         return launch_strip(p, type, ep, row_scales, stream);
     return tiles_for(p, type, ep, row_scales, nullptr, stream);
 }
@@ -971,7 +978,7 @@ size_t product_workspace(ProductArgs p, int type, int ep, bool row_scales)
 {
     size_t bytes = 0;
     p.may_split = 1;
-    if (!strips(p, type, ep))
+    if (!strips(p, type, ep, row_scales))
         (void)tiles_for(p, type, ep, row_scales, &bytes, nullptr);
     return bytes;
 }

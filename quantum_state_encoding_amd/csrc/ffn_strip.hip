@@ -230,8 +230,9 @@ hipError_t run(const ProductArgs& p, hipStream_t stream)
 
 // Waves and steps in flight: sixteen waves pay for a long k alone (e4m3, m 1:
 // n 4096 k 16384 13.9 us, with eight waves 17.3; n 16384 k 4096, where eight
-// waves of four steps are all of k, 20.0 and 13.1), and only where their four
-// steps fit 128 registers.
+// waves of four steps are all of k, 20.0 and 13.1; f16 and fp32 results 13.9
+// and 17.8 at the first), and only where their four steps fit 128 registers:
+// not with a scale for each row of B (22 of them spill).
 template <int TYPE, int EP, int SM>
 hipError_t pick(const ProductArgs& p, hipStream_t stream)
 {
@@ -244,7 +245,7 @@ hipError_t pick(const ProductArgs& p, hipStream_t stream)
     }
     if (p.m > 16)
         return run<TYPE, 2, 8, 2, EP, SM>(p, stream);
-    if constexpr (EP == kEpStore && SM == 1 && TYPE == kTE4m3) {
+    if constexpr (EP == kEpStore && SM == 1) {
         if (p.kbytes >= 64 * kStep)
             return run<TYPE, 1, 16, 4, EP, SM>(p, stream);
     }
@@ -256,7 +257,7 @@ hipError_t pick(const ProductArgs& p, hipStream_t stream)
 hipError_t launch_strip(const ProductArgs& p, int type, int ep, bool row_scales,
                         hipStream_t stream)
 {
-    if (type == kTE4m3 && p.ctype == kTF32) {
+    if (type == kTE4m3 && p.ctype != kTBf16) {
         if (ep == kEpGate)
             return pick<kTE4m3Exact, kEpGate, 1>(p, stream);
         return row_scales ? pick<kTE4m3Exact, kEpStore, 2>(p, stream)

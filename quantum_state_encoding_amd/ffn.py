@@ -200,8 +200,9 @@ def rotate_quantize(x, bits=0, scales="row", transpose=False, stream=None):
 
 def scaled_matmul(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=None):
     """``a b^T`` of e4m3 codes: a (m, k) with row scales, b (n, k) with row
-    or tile scales (told by their shape).  ``out_dtype``: bfloat16 (default),
-    float16 or float32.  See fwt_scaled_matmul."""
+    or tile scales (told by their shape).  ``out_dtype``: bfloat16 (default,
+    twice the rate: its products lose what bfloat16 cannot show), float16 or
+    float32.  See fwt_scaled_matmul."""
     lib = _lib or _load()
     dev = _current()
     m, k, lda = _matrix(a, "a", (_f8,), dev)

@@ -309,3 +309,68 @@ def test_activation_and_slope_relative_to_their_values(k, act, dtype):
         g.abs() * torch.exp(-g * g / 2) / math.sqrt(2 * math.pi))
     tol = (rel + 2 * U) * terms * 7 + twice * (d.abs() * 7) + 8 * low
     assert bool(((dx[:, 0] - d * 7).abs() <= tol).all())
+
+
+# ---- products of codes of one sign -------------------------------------------
+
+def one_sign(g, rows, k, kind):
+    """Codes that are not negative: one large one in each eight beside 1.875
+    ("dominant"), or any from 2^-6 to 448."""
+    if kind == "dominant":
+        c = torch.full((rows, k), 0x3f, dtype=torch.uint8, device="cuda")
+        c[:, ::8] = 0x70
+    else:
+        c = torch.randint(8, 0x7f, (rows, k), generator=g, device="cuda").to(torch.uint8)
+    full = torch.full((rows, cdiv(k, 16) * 16), 0x7f, dtype=torch.uint8, device="cuda")
+    full[:, :k] = c
+    return full.view(F8)[:, :k]
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 40, 4096), (2, 100, 9000), (20, 33, 1000), (70, 130, 2000),
+                                   (300, 1025, 400), (300, 200, 16001), (1900, 4000, 260),
+                                   (3600, 3400, 272), (200, 16400, 520)])
+@pytest.mark.parametrize("kind", ["dominant", "any"])
+@pytest.mark.parametrize("scales", ["row", "tile"])
+def test_products_of_one_sign(m, n, k, kind, scales):
+    # Nothing averages out here: what the 8-bit instruction cuts off a product
+    # (up to 2^-13 of the largest of eight, one of which is that largest) adds
+    # up to 7 * 2^-13 of the result, 0.22 of half a step of bf16 but 1.75 of
+    # f16's.  f16 and fp32 results have none of it.
+    say("one sign", m, n, k, kind, scales)
+    g = gen(m + n + k)
+    a, b = one_sign(g, m, k, kind), one_sign(g, n, k, kind)
+    kb = cdiv(k, BLOCK)
+    sa = torch.full((kb, m), 2.0 ** -9 / k, device="cuda")
+    sb = torch.full((kb, n if scales == "row" else cdiv(n, BLOCK)), 0.75, device="cuda")
+    want = (a.double() @ b.double().t()) * (sa.double()[0, 0] * 0.75)
+    sums = (128 + kb + 3) * 2 * U * want
+    for out, dt in DT.items():
+        c = qse.scaled_matmul(a, sa, b, sb, out_dtype=dt).double()
+        cut = 7 * 2.0 ** -13 * want if out == "bf16" else 0
+        tol = sums + cut + half(dt) * (want + sums + cut) + 2.0 ** -25
+        off = float(((c - want) / want).mean()) / half(dt)
+        print("%s: mean error %.3f of half a step" % (out, off), flush=True)
+        assert bool(((c - want).abs() <= tol).all()), out
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 40, 4096), (70, 130, 2000), (300, 200, 8001),
+                                   (2100, 3100, 136)])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_gated_products_of_one_sign(m, n, k, act):
+    say("gated one sign", m, n, k, act)
+    g = gen(m + n + k)
+    x, wg, wu = (one_sign(g, r, k, "dominant") for r in (m, n, n))
+    kb = cdiv(k, BLOCK)
+    sx = torch.full((kb, m), 2.0 ** -9 / k, device="cuda")
+    sg, su = (torch.full((kb, cdiv(n, BLOCK)), s, device="cuda") for s in (0.75, 1.25))
+    base = (x.double() @ wg.double().t()) * sx.double()[0, 0]
+    gate, up = base * 0.75, base * 1.25
+    f, _ = act64(act, gate)
+    want = f * up
+    e = (128 + kb + 3) * 2 * U                     # of each product
+    rel = 2.13 * e + e * e + act_relative(act, gate, True)    # g act' / act <= 1.13 for g > 0
+    for out in ("f16", "f32"):
+        h = qse.gated_ffn(x, wg, wu, act=act, x_scales=sx, gate_scales=sg, up_scales=su,
+                          out_dtype=DT[out]).double()
+        tol = want * (rel + half(DT[out]) * (1 + rel)) + 2.0 ** -25
+        assert bool(((h - want).abs() <= tol).all()), out
