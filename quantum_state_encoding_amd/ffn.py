@@ -3,7 +3,9 @@
 Bindings of ``include/fwt_ffn.h``: rotation with quantisation to e4m3, the
 product of two quantised operands, the gated block and its gradients.  Like
 the rest of the package they only marshal arguments; outputs and scratch are
-torch allocations on the call's stream.
+torch allocations on the call's stream.  They record nothing for autograd: in
+grad mode operands that require gradients are refused (gated_ffn_backward takes
+them; its results are not differentiable themselves).
 
 Example (one feed-forward block of a served model; weights prepared once)::
 
@@ -33,12 +35,12 @@ _SCALES = {"row": 0, "tile": 1}
 _ACTS = {"silu": 0, "gelu": 1}
 _lib = None
 # of torch, set by _load
-_types = _f32 = _f8 = _floats = _halves = _gated = _raw_stream = _device = None
+_types = _f32 = _f8 = _floats = _halves = _gated = _raw_stream = _device = _grad_mode = None
 _here = contextlib.nullcontext()
 
 
 def _load():
-    global _lib, _types, _f32, _f8, _floats, _halves, _gated, _raw_stream, _device
+    global _lib, _types, _f32, _f8, _floats, _halves, _gated, _raw_stream, _device, _grad_mode
     if _lib is None:
         import torch
         lib = _qse.load_library()
@@ -63,6 +65,7 @@ def _load():
         _halves = (torch.bfloat16, torch.float16)
         _floats, _gated = _halves + (_f32,), _halves + (_f8,)
         _raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: no Stream object
+        _grad_mode = torch.is_grad_enabled
         _lib = lib
     return _lib
 
@@ -126,6 +129,25 @@ def _out_dtype(out_dtype, out):
     return dtype
 
 
+def _no_graph(what, *tensors):
+    """Refuses operands whose gradients would be lost: the calls record
+    nothing for autograd."""
+    if _grad_mode():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise ValueError("%s records no graph: call it under torch.no_grad() or with "
+                                 "detached tensors (gated_ffn_backward has gated_ffn's "
+                                 "gradients)" % what)
+
+
+def _written(out):
+    """Tells autograd that `out`, which may be saved for a backward pass, has
+    other values now."""
+    if out is not None:
+        import torch
+        torch.autograd.graph.increment_version(out)
+
+
 def _raise(status, what):
     if status != _qse.FWT_OK:
         raise _qse.FwtError(status, what)
@@ -177,6 +199,7 @@ def rotate_quantize(x, bits=0, scales="row", transpose=False, stream=None):
         _raise(_qse.FWT_EINVAL, "rotate_quantize: bits %d" % bits)
     dev = _current()
     m, k, ld = _matrix(x, "x", _floats, dev)
+    _no_graph("rotate_quantize", x)
     if transpose:
         m, k = k, m
     kind, t = _SCALES[scales], 1 if transpose else 0
@@ -213,6 +236,7 @@ def scaled_matmul(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=Non
     _scales_of(a_scales, "a_scales", dev, nblocks, m, ("row",))
     kind = _scales_of(b_scales, "b_scales", dev, nblocks, n, ("tile", "row"))
     dtype = _out_dtype(out_dtype, out)
+    _no_graph("scaled_matmul", a, a_scales, b, b_scales, out)
     need = 0
     if _may_share(m, n, k):
         size = ctypes.c_size_t(0)
@@ -226,6 +250,7 @@ def scaled_matmul(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=Non
     _raise(lib.fwt_scaled_matmul(a.data_ptr(), lda, a_scales.data_ptr(), b.data_ptr(), ldb,
                                  b_scales.data_ptr(), _SCALES[kind], m, n, k, c.data_ptr(),
                                  _types[dtype], ldc, wp, need, handle), "fwt_scaled_matmul")
+    _written(out)
     return c
 
 
@@ -262,6 +287,7 @@ def gated_ffn(x, gate, up, act="silu", x_scales=None, gate_scales=None, up_scale
         if dtype is not x.dtype:
             raise ValueError("the output has the operands' dtype")
     code = _act(act)
+    _no_graph("gated_ffn", x, gate, up, x_scales, gate_scales, up_scales, out)
     need = 0
     if _may_share(m, n, k):
         size = ctypes.c_size_t(0)
@@ -276,6 +302,7 @@ def gated_ffn(x, gate, up, act="silu", x_scales=None, gate_scales=None, up_scale
                              up.data_ptr(), ldu, sp[2], _types[x.dtype], m, n, k, code,
                              h.data_ptr(), _types[dtype], ldh, wp, need, handle),
            "fwt_gated_ffn")
+    _written(out)
     return h
 
 

@@ -374,3 +374,62 @@ def test_gated_products_of_one_sign(m, n, k, act):
                           out_dtype=DT[out]).double()
         tol = want * (rel + half(DT[out]) * (1 + rel)) + 2.0 ** -25
         assert bool(((h - want).abs() <= tol).all()), out
+
+
+# ---- autograd ----------------------------------------------------------------
+
+def test_operands_that_require_gradients_are_refused():
+    say("requires grad")
+    g = gen(1)
+    x, wg, wu = (torch.randn(r, 64, generator=g, device="cuda").bfloat16() for r in (5, 8, 8))
+    q, s = qse.rotate_quantize(x)
+    w, t = qse.rotate_quantize(wg, scales="tile")
+    leaf = lambda v: v.detach().clone().requires_grad_()
+    f8 = dict(x_scales=s, gate_scales=t, up_scales=t)
+    out = lambda dt: torch.zeros(5, 8, dtype=dt, device="cuda").requires_grad_()
+    calls = [lambda: qse.rotate_quantize(leaf(x)), lambda: qse.gated_ffn(leaf(x), wg, wu),
+             lambda: qse.gated_ffn(x, leaf(wg), wu), lambda: qse.gated_ffn(x, wg, leaf(wu)),
+             lambda: qse.gated_ffn(x, wg, wu, out=out(torch.bfloat16)),
+             lambda: qse.gated_ffn(q, w, w, **dict(f8, up_scales=leaf(t))),
+             lambda: qse.gated_ffn(leaf(x) * 2, wg, wu),
+             lambda: qse.scaled_matmul(q, leaf(s), w, t),
+             lambda: qse.scaled_matmul(q, s, w, leaf(t)),
+             lambda: qse.scaled_matmul(q, s, w, t, out=out(torch.float32))]
+    for call in calls:
+        with pytest.raises(ValueError, match="records no graph"):
+            call()
+        with torch.no_grad():
+            call()
+    # gradients are not refused, and a custom function can be made of the two
+    class Gated(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, x, gate, up):
+            ctx.save_for_backward(x, gate, up)
+            return qse.gated_ffn(x, gate, up)
+
+        @staticmethod
+        def backward(ctx, grad):
+            return qse.gated_ffn_backward(*ctx.saved_tensors, grad.contiguous())
+    leaves = [leaf(v) for v in (x, wg, wu)]
+    Gated.apply(*leaves).sum().backward()
+    want = qse.gated_ffn_backward(x, wg, wu, torch.ones(5, 8, device="cuda").bfloat16())
+    assert all(torch.equal(v.grad, p) for v, p in zip(leaves, want))
+    assert all(torch.equal(a, b) for a, b in zip(
+        qse.gated_ffn_backward(*leaves, torch.ones(5, 8, device="cuda").bfloat16()), want))
+
+
+def test_an_output_that_autograd_saved_is_noticed():
+    say("saved out")
+    x = torch.randn(5, 64, generator=gen(2), device="cuda").bfloat16()
+    q, s = qse.rotate_quantize(x)
+    for dt, call in ((torch.bfloat16, lambda o: qse.gated_ffn(x, x, x, out=o)),
+                     (torch.float32, lambda o: qse.scaled_matmul(q, s, q, s, out=o))):
+        o = torch.zeros(5, 5, dtype=dt, device="cuda")
+        y = (torch.ones(5, 5, dtype=dt, device="cuda", requires_grad=True) * o).sum()
+        version = o._version
+        call(o[:, :])                       # a view shares its base's version
+        assert o._version > version
+        with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+            y.backward()
+        with torch.inference_mode():        # (such a tensor has no version)
+            call(torch.zeros(5, 5, dtype=dt, device="cuda"))
