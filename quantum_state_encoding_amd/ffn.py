@@ -3,7 +3,10 @@
 Bindings of ``include/fwt_ffn.h``: rotation with quantisation to e4m3, the
 product of two quantised operands, the gated block and its gradients.  Like
 the rest of the package they only marshal arguments; outputs and scratch are
-torch allocations on the call's stream.  They record nothing for autograd: in
+torch allocations on the call's stream.  ``stream`` (the current one by
+default) is one of the current device; it is not made to wait for the operands,
+nor another stream for the results, but the operands' memory is kept until it
+has passed the call.  The calls record nothing for autograd: in
 grad mode operands that require gradients are refused (gated_ffn_backward takes
 them; its results are not differentiable themselves).
 
@@ -104,11 +107,18 @@ def _scales_of(s, name, dev, blocks, rows, kinds):
         str((blocks, rows if k == "row" else -(-rows // BLOCK))) for k in kinds), shape))
 
 
-def _on(stream, dev):
-    """(stream handle, a context in which torch allocates for that stream)."""
+def _on(stream, dev, *tensors):
+    """(stream handle, a context in which torch allocates for that stream).
+    The memory of the call's tensors is kept until a given stream has passed
+    the call."""
     if stream is None:
         return _raw_stream(dev), _here
     import torch
+    if stream.device_index != dev:
+        raise ValueError("stream must be one of the current device")
+    for t in tensors:
+        if t is not None:
+            t.record_stream(stream)
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
@@ -209,7 +219,7 @@ def rotate_quantize(x, bits=0, scales="row", transpose=False, stream=None):
         _raise(lib.fwt_rotate_quantize_workspace(m, k, bits, kind, t, ctypes.byref(size)),
                "fwt_rotate_quantize_workspace")
         need = size.value
-    handle, where = _on(stream, dev)
+    handle, where = _on(stream, dev, x)
     with where:
         ldq = -(-k // 16) * 16
         codes = x.new_empty((m, ldq), dtype=_f8)
@@ -243,7 +253,7 @@ def scaled_matmul(a, a_scales, b, b_scales, out_dtype=None, out=None, stream=Non
         _raise(lib.fwt_scaled_matmul_workspace(m, n, k, _SCALES[kind], _types[dtype],
                                                ctypes.byref(size)), "fwt_scaled_matmul_workspace")
         need = size.value
-    handle, where = _on(stream, dev)
+    handle, where = _on(stream, dev, a, a_scales, b, b_scales, out)
     with where:
         c, ldc = _result(out, "out", dev, m, n, dtype, a)
         ws, wp = _scratch(need, a)
@@ -294,7 +304,7 @@ def gated_ffn(x, gate, up, act="silu", x_scales=None, gate_scales=None, up_scale
         _raise(lib.fwt_gated_ffn_workspace(_types[x.dtype], m, n, k, _types[dtype],
                                            ctypes.byref(size)), "fwt_gated_ffn_workspace")
         need = size.value
-    handle, where = _on(stream, dev)
+    handle, where = _on(stream, dev, x, gate, up, x_scales, gate_scales, up_scales, out)
     with where:
         h, ldh = _result(out, "out", dev, m, n, dtype, x)
         ws, wp = _scratch(need, x)
@@ -323,7 +333,7 @@ def gated_ffn_backward(x, gate, up, grad, act="silu", stream=None):
     size = ctypes.c_size_t(0)
     _raise(lib.fwt_gated_ffn_backward_workspace(m, n, k, ctypes.byref(size)),
            "fwt_gated_ffn_backward_workspace")
-    handle, where = _on(stream, dev)
+    handle, where = _on(stream, dev, x, gate, up, grad)
     with where:
         dx = x.new_empty((m, k))
         dgate = x.new_empty((n, k))

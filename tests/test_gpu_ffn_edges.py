@@ -433,3 +433,93 @@ def test_an_output_that_autograd_saved_is_noticed():
             y.backward()
         with torch.inference_mode():        # (such a tensor has no version)
             call(torch.zeros(5, 5, dtype=dt, device="cuda"))
+
+
+# ---- streams -----------------------------------------------------------------
+
+def test_operands_live_until_another_stream_is_done():
+    # A stream that is still busy when the call returns and its operands go:
+    # their memory must not be handed out again before it has read them.
+    say("operands on another stream")
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    make = lambda r, k=1 << 16: torch.ones(r, k, device="cuda").bfloat16()
+    w8 = qse.rotate_quantize(make(4096, 1024), scales="tile")
+
+    def rotate():
+        x = make(37)
+        return [x], qse.rotate_quantize(x, stream=side)
+
+    def matmul():
+        a = qse.rotate_quantize(make(2000, 1024))
+        out = torch.empty(2000, 4096, dtype=torch.bfloat16, device="cuda")
+        return [*a, out], qse.scaled_matmul(*a, *w8, out=out, stream=side)
+
+    def gated():
+        x, wg, wu = make(999, 1024), make(500, 1024), make(500, 1024)
+        return [x, wg, wu], qse.gated_ffn(x, wg, wu, stream=side)
+
+    def gated8():
+        a = qse.rotate_quantize(make(2100, 1024))
+        return [*a], qse.gated_ffn(a[0], w8[0], w8[0], x_scales=a[1], gate_scales=w8[1],
+                                   up_scales=w8[1], stream=side)
+
+    def backward():
+        t = make(900, 1024), make(510, 1024), make(510, 1024), make(900, 510)
+        return [*t], qse.gated_ffn_backward(*t, stream=side)
+
+    for call in (rotate, matmul, gated, gated8, backward):
+        call()
+        torch.cuda.synchronize()
+        done = torch.cuda.Event()
+        side.wait_stream(torch.cuda.current_stream())
+        with torch.cuda.stream(side):
+            torch.cuda._sleep(50_000_000)
+        operands, result = call()
+        done.record(side)
+        places = {t.untyped_storage().data_ptr(): t.untyped_storage().nbytes() for t in operands}
+        result = None
+        del operands
+        new = [torch.empty(n, dtype=torch.uint8, device="cuda") for n in places.values()]
+        assert not done.query(), "the stream is to be busy still"
+        assert not any(t.data_ptr() == p for t in new for p in places), call.__name__
+        torch.cuda.synchronize()
+        del new
+
+
+def test_results_of_a_given_stream():
+    say("stream results")
+    x = torch.randn(70, 256, generator=gen(3), device="cuda").bfloat16()
+    want = qse.gated_ffn(x, x, x), qse.gated_ffn_backward(x, x, x, x[:, :70])
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = qse.gated_ffn(x, x, x, stream=side), qse.gated_ffn_backward(x, x, x, x[:, :70], stream=side)
+    side.synchronize()
+    assert torch.equal(got[0], want[0]) and all(torch.equal(a, b) for a, b in zip(got[1], want[1]))
+
+
+def test_a_given_stream_in_a_captured_graph():
+    say("stream in a graph")
+    g = gen(4)
+    x = torch.randn(70, 256, generator=g, device="cuda").bfloat16()
+    w = torch.randn(96, 256, generator=g, device="cuda").bfloat16()
+    side = torch.cuda.Stream()
+
+    def step():
+        side.wait_stream(torch.cuda.current_stream())
+        y = qse.rotate_quantize(x, bits=8, stream=side)
+        h = qse.gated_ffn(x, w, w, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        return (y[0].float(), y[1], h)
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = step()
+    for _ in range(4):
+        x.copy_(torch.randn(70, 256, generator=g, device="cuda"))
+        graph.replay()
+        torch.cuda.synchronize()
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(out, want))
