@@ -523,3 +523,271 @@ def test_a_given_stream_in_a_captured_graph():
         want = step()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(out, want))
+
+
+# ---- gradients of views, by value ---------------------------------------------
+
+def check_gradients(got, x, wg, wu, dh, act):
+    """The bounds of test_gpu_ffn's test_gated_backward, with the activation's
+    error relative to its terms."""
+    dt = x.dtype
+    xd, gd, ud, hd = (t.double() for t in (x, wg, wu, dh))
+    k = xd.shape[1]
+    g, u = xd @ gd.t(), xd @ ud.t()
+    eg, eu = ((k + 2) * 2 * U * (xd.abs() @ w.abs().t()) for w in (gd, ud))
+    f, d = act64(act, g)
+    dg, du = hd * u * d, hd * f
+    tiny = 2.0 ** -25 if dt is torch.float16 else 0.0
+    rel = act_relative(act, g, False)
+    ed = 0.8 * eg + (rel + 2 * U) * (1 + g.abs())        # |act''| <= 0.8
+    ef = 1.13 * eg + rel * f.abs() + 2.0 ** -119          # |act'| <= 1.13
+    e_dg = hd.abs() * (eu * (d.abs() + ed) + u.abs() * ed)
+    e_du = hd.abs() * ef
+    e_dg = e_dg + (half(dt) + 4 * U) * (dg.abs() + e_dg) + tiny
+    e_du = e_du + (half(dt) + 4 * U) * (du.abs() + e_du) + tiny
+    m, n = hd.shape
+    for name, out, terms, count in (
+            ("dx", got[0], [(dg, gd, e_dg), (du, ud, e_du)], 2 * n + 2),
+            ("dgate", got[1], [(dg.t(), xd, e_dg.t())], m + 2),
+            ("dup", got[2], [(du.t(), xd, e_du.t())], m + 2)):
+        want = sum(a @ b for a, b, _ in terms)
+        tol = sum(e @ b.abs() + count * 2 * U * ((a.abs() + e) @ b.abs()) for a, b, e in terms)
+        tol = tol + half(dt) * (want.abs() + tol) + tiny
+        bad = ~((out.double() - want).abs() <= tol)      # (NaN is bad)
+        assert not bool(bad.any()), (name, int(bad.sum()))
+
+
+def framed(t, off):
+    """t as a view of an array that is NaN all around it."""
+    big = torch.full((t.shape[0] + 2, t.shape[1] + 24), float("nan"), device="cuda").to(t.dtype)
+    view = big[1:-1, off:off + t.shape[1]]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("m,n,k", [(1, 33, 37), (5, 9, 7), (17, 50, 129), (40, 20, 1001),
+                                   (300, 130, 64), (300, 9, 7), (17, 7, 300), (300, 33, 37),
+                                   (129, 300, 130), (2050, 130, 515)])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gradients_of_views(m, n, k, dtype):
+    say("gradients of views", m, n, k, dtype)
+    g = gen(m + n + k)
+    dt = DT[dtype]
+    x, wg, wu, dh = (torch.randn(r, c, generator=g, device="cuda").mul_(s).to(dt)
+                     for r, c, s in ((m, k, 1), (n, k, 2 / math.sqrt(k)), (n, k, 1 / math.sqrt(k)),
+                                     (m, n, 1)))
+    for off in (0, 1, 2, 3, 4, 7, 8, 11, 16):
+        views = [framed(t, off) for t in (x, wg, wu, dh)]
+        check_gradients(qse.gated_ffn_backward(*views), x, wg, wu, dh, "silu")
+    # each operand alone at an odd address, the others aligned
+    for i in range(4):
+        views = [framed(t, 1) if i == j else framed(t, 8) for j, t in enumerate((x, wg, wu, dh))]
+        check_gradients(qse.gated_ffn_backward(*views, act="gelu"), x, wg, wu, dh, "gelu")
+
+
+# ---- values that are not finite inside operands ---------------------------------
+
+def same_bits(a, b, rows=None, cols=None):
+    """Whether the rows (columns) other than the given one have the same bits."""
+    v = torch.int32 if a.dtype is torch.float32 else torch.int16
+    keep = torch.ones(a.shape, dtype=torch.bool, device="cuda")
+    if rows is not None:
+        keep[rows] = False
+    if cols is not None:
+        keep[:, cols] = False
+    return bool((a.view(v) == b.view(v))[keep].all())
+
+
+def nowhere_finite(t):
+    return not bool(torch.isfinite(t).any())
+
+
+BAD = [(3, 33, 70), (5, 16, 8), (20, 300, 136), (70, 130, 136), (300, 257, 100), (64, 64, 8016),
+       (300, 513, 260), (70, 2051, 133), (2100, 1600, 136)]
+
+
+@pytest.mark.parametrize("m,n,k", BAD)
+@pytest.mark.parametrize("bad", ["nan", "inf"])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_gated_keeps_what_is_not_finite_to_its_row(m, n, k, bad, dtype):
+    say("not finite", m, n, k, bad, dtype)
+    g = gen(m + n + k)
+    dt, bad = DT[dtype], float(bad)
+    # (no zeros: infinity times any of them is not finite)
+    x, wg, wu, dh = (torch.randn(r, c, generator=g, device="cuda").sign()
+                     .mul_(torch.rand(r, c, generator=g, device="cuda") + 0.1).mul_(s).to(dt)
+                     for r, c, s in ((m, k, 1), (n, k, 2 / math.sqrt(k)), (n, k, 1 / math.sqrt(k)),
+                                     (m, n, 1)))
+    h = qse.gated_ffn(x, wg, wu)
+    clean = qse.gated_ffn_backward(x, wg, wu, dh)
+    i, j, c = m - 1, n // 2, k - 1
+    y = x.clone()
+    y[i, c] = bad
+    got = qse.gated_ffn(y, wg, wu)
+    # (a gate of minus infinity gives -inf * 0)
+    assert same_bits(got, h, rows=i) and nowhere_finite(got[i])
+    dx, dg, du = qse.gated_ffn_backward(y, wg, wu, dh)
+    assert same_bits(dx, clean[0], rows=i) and nowhere_finite(dx[i])
+    assert nowhere_finite(dg[:, c]) and nowhere_finite(du[:, c])
+    for which in range(2):
+        w = [wg.clone(), wu.clone()]
+        w[which][j, c] = bad
+        got = qse.gated_ffn(x, *w)
+        assert same_bits(got, h, cols=j) and nowhere_finite(got[:, j])
+        dx, dg, du = qse.gated_ffn_backward(x, *w, dh)
+        assert same_bits(dg, clean[1], rows=j) and same_bits(du, clean[2], rows=j)
+        assert nowhere_finite(dg[j]) and nowhere_finite(dx[:, c])
+        assert nowhere_finite(du[j]) if which == 0 else torch.equal(du, clean[2])
+
+
+@pytest.mark.parametrize("m,n,k", [(3, 33, 70), (20, 300, 1360), (70, 130, 136), (300, 257, 100),
+                                   (300, 200, 16001), (1900, 4000, 260), (5, 16390, 200)])
+@pytest.mark.parametrize("scales", ["row", "tile"])
+@pytest.mark.parametrize("out", ["bf16", "f16", "f32"])
+def test_matmul_keeps_nan_codes_to_their_row(m, n, k, scales, out):
+    say("nan codes", m, n, k, scales, out)
+    g = gen(m + n + k)
+    ld = cdiv(k, 16) * 16
+    a, b = (torch.randn(r, ld, generator=g, device="cuda").to(F8)[:, :k] for r in (m, n))
+    kb = cdiv(k, BLOCK)
+    sa = torch.rand(kb, m, generator=g, device="cuda") + 0.1
+    sb = torch.rand(kb, n if scales == "row" else cdiv(n, BLOCK), generator=g, device="cuda") + 0.1
+    clean = qse.scaled_matmul(a, sa, b, sb, out_dtype=DT[out])
+    i, j, c = m - 1, n // 2, k - 1
+    y = a.clone()
+    y.view(torch.uint8)[i, c] = 0xff
+    y = torch.nn.functional.pad(y.view(torch.uint8), (0, ld - k)).view(F8)[:, :k]
+    got = qse.scaled_matmul(y, sa, b, sb, out_dtype=DT[out])
+    assert same_bits(got, clean, rows=i) and bool(torch.isnan(got[i]).all())
+    y = torch.nn.functional.pad(b.view(torch.uint8), (0, ld - k)).view(F8)[:, :k]
+    y.view(torch.uint8)[j, c] = 0x7f
+    got = qse.scaled_matmul(a, sa, y, sb, out_dtype=DT[out])
+    assert same_bits(got, clean, cols=j) and bool(torch.isnan(got[:, j]).all())
+
+
+# ---- few rows where tiles would fill the CUs -------------------------------------
+
+@pytest.mark.parametrize("m,n,k", [(1, 16384, 512), (3, 16500, 300), (8, 16401, 1111),
+                                   (9, 16401, 1111), (5, 17000, 8200), (7, 300, 8200)])
+@pytest.mark.parametrize("scales", ["row", "tile"])
+def test_few_rows_of_wide_products(m, n, k, scales):
+    # as test_gpu_ffn's test_matmul, for the results that keep 32 bits
+    say("wide", m, n, k, scales)
+    g = gen(m + n + k)
+    ld = cdiv(k, 16) * 16
+    a, b = ((torch.randn(r, ld, generator=g, device="cuda") * 30).to(F8)[:, :k] for r in (m, n))
+    kb = cdiv(k, BLOCK)
+    sa = torch.rand(kb, m, generator=g, device="cuda") * 1e-2
+    sb = torch.rand(kb, n if scales == "row" else cdiv(n, BLOCK), generator=g, device="cuda") * 1e-2
+    spread = lambda s, r: (s if s.shape[1] == r else s.repeat_interleave(BLOCK, 1)[:, :r]
+                           ).repeat_interleave(BLOCK, 0)[:k].t().double()
+    av, bv = a.double() * spread(sa, m), b.double() * spread(sb, n)
+    want, mag = av @ bv.t(), av.abs() @ bv.abs().t()
+    for dt in (torch.float16, torch.float32):
+        c = qse.scaled_matmul(a, sa, b, sb, out_dtype=dt)
+        tol = (128 + kb + 2) * 2 * U * mag
+        tol = tol + half(dt) * (want.abs() + tol) + 2.0 ** -25
+        assert bool(((c.double() - want).abs() <= tol).all()), dt
+
+
+# ---- rotations whose results are subnormal ----------------------------------------
+
+@pytest.mark.parametrize("bits", [0, 1, 4, 7, 8, 9, 10, 11, 14])
+@pytest.mark.parametrize("integers", [True, False])
+def test_subnormal_rotations_by_row_and_by_tile(bits, integers):
+    # 128 equal rows have one scale by row and by tile, 2^-126, the smallest.
+    # Sums of subnormals are exact; the factor is taken out before the division
+    # or with it, which rounds y to a multiple of 2^-149, 2^-24 of the scale, or
+    # not: codes are the exact quotient's rounding but for ties that near.
+    say("subnormal", bits, integers)
+    k = max(256, 1 << bits)
+    if integers:
+        x = torch.randint(-8, 9, (1, k), generator=gen(bits), device="cuda") * 2.0 ** (-134 + (bits + 1) // 2)
+    else:
+        x = torch.randn(1, k, generator=gen(bits), device="cuda").double() * 2.0 ** -129
+    x = x.double().float()
+    y = x.double()
+    for b in range(bits):
+        y = y.reshape(-1, 2, 1 << b)
+        y = torch.stack([y[:, 0] + y[:, 1], y[:, 0] - y[:, 1]], 1)
+    mag = x.double().abs().reshape(k >> bits, 1 << bits).sum(1).repeat_interleave(1 << bits)
+    r = y.reshape(k) * 2.0 ** (-bits / 2) * 2.0 ** 126
+    assert float(r.abs().max()) < 448 and bool((r.abs() > 2.0 ** -10).any())
+    err = (bits + 3) * U * mag * 2.0 ** (-bits / 2) * 2.0 ** 126 + 2.0 ** -23
+    tol = torch.maximum(r.abs() * 2.0 ** -4, torch.full_like(r, 2.0 ** -10)) + 2 * U * r.abs() + err
+    full = x.expand(128, k).contiguous()
+    for scales in ("row", "tile"):
+        q, s = qse.rotate_quantize(full, bits=bits, scales=scales)
+        assert bool((s == 2.0 ** -126).all())
+        assert bool((q.float() == q[:1].float()).all())
+        assert bool(((q[0].double() - r).abs() <= tol).all())
+        assert bool((q.float() != 0).any())
+        if integers and bits % 2 == 0:        # every value is exact: so are its codes
+            assert torch.equal(q[0].float(), r.float().to(F8).float())
+
+
+# ---- arrays past 4 GiB with ragged numbers of rows ----------------------------------
+
+def small_integers(rows, cols, dtype, seed):
+    t = torch.empty(rows, cols, dtype=torch.int8, device="cuda")
+    t.random_(-4, 5, generator=gen(seed))
+    out = torch.empty(rows, cols, dtype=dtype, device="cuda")
+    for lo in range(0, rows, 1 << 14):
+        out[lo:lo + (1 << 14)] = t[lo:lo + (1 << 14)].to(dtype)
+    return out
+
+
+@pytest.mark.parametrize("bits,scales", [(3, "row"), (7, "tile"), (10, "tile"), (12, "row")])
+def test_ragged_rotations_past_32_bits(bits, scales):
+    say("large ragged rotate", bits, scales)
+    m = 70013
+    x = small_integers(m, 65536, torch.bfloat16, bits)
+    q, s = qse.rotate_quantize(x, bits=bits, scales=scales)
+    lo = m // BLOCK * BLOCK - 128
+    q2, s2 = qse.rotate_quantize(x[lo:], bits=bits, scales=scales)
+    assert torch.equal(q[lo:].view(torch.uint8), q2.view(torch.uint8))
+    assert torch.equal(s[:, lo // BLOCK if scales == "tile" else lo:], s2)
+
+
+@pytest.mark.parametrize("m", [3, 70, 601])
+@pytest.mark.parametrize("scales", ["row", "tile"])
+def test_ragged_matmul_past_32_bits(m, scales):
+    say("large ragged matmul", m, scales)
+    n, k = 70017, 65504
+    a = small_integers(m, 65536, F8, 2)[:, :k]
+    b = small_integers(n, 65536, F8, 3)[:, :k]
+    kb = cdiv(k, BLOCK)
+    sa = torch.ones(kb, m, device="cuda")
+    sb = torch.ones(kb, n if scales == "row" else cdiv(n, BLOCK), device="cuda")
+    for out in (torch.float32, torch.bfloat16):
+        c = qse.scaled_matmul(a, sa, b, sb, out_dtype=out)
+        for rows in (slice(0, 100), slice(n - 201, n)):
+            want = qse.scaled_matmul(a, sa, b[rows], torch.ones(kb, len(b[rows]), device="cuda"),
+                                     out_dtype=out)
+            assert torch.equal(c[:, rows], want)
+
+
+@pytest.mark.parametrize("m,k", [(5, 16384), (201, 16383)])
+def test_ragged_gated_past_32_bits(m, k):
+    say("large ragged gated", m, k)
+    n = 140037
+    x = small_integers(m, 16384, torch.bfloat16, 6)[:, :k] * 0.0625
+    wg, wu = (small_integers(n, 16384, torch.bfloat16, seed)[:, :k] for seed in (7, 8))
+    h = qse.gated_ffn(x, wg, wu)
+    for rows in (slice(0, 200), slice(n - 201, n)):
+        assert torch.equal(h[:, rows], qse.gated_ffn(x, wg[rows], wu[rows]))
+
+
+@pytest.mark.parametrize("k", [16384, 16383])
+def test_ragged_backward_past_32_bits(k):
+    # one token's gradient is not zero: each weight gradient is one product
+    say("large ragged backward", k)
+    m, n = 140031, 33
+    x = small_integers(m, 16384, torch.bfloat16, 9)[:, :k]
+    wg, wu = (small_integers(n, 16384, torch.bfloat16, s)[:, :k] * 0.0625 for s in (10, 11))
+    dh = torch.zeros(m, n, dtype=torch.bfloat16, device="cuda")
+    dh[-3] = 1.0
+    dx, dg, du = qse.gated_ffn_backward(x, wg, wu, dh)
+    sx, sg, su = qse.gated_ffn_backward(x[-127:], wg, wu, dh[-127:])
+    assert torch.equal(dx[-127:], sx) and torch.equal(dg, sg) and torch.equal(du, su)
+    assert float(dx[:-3].abs().max()) == 0.0 and float(dx[-3].abs().max()) > 0.0
