@@ -228,11 +228,12 @@ hipError_t run(const ProductArgs& p, hipStream_t stream)
     return hipGetLastError();
 }
 
-// Waves and steps in flight: sixteen waves pay for a long k alone (e4m3, m 1:
-// n 4096 k 16384 13.9 us, with eight waves 17.3; n 16384 k 4096, where eight
-// waves of four steps are all of k, 20.0 and 13.1; f16 and fp32 results 13.9
-// and 17.8 at the first), and only where their four steps fit 128 registers:
-// not with a scale for each row of B (22 of them spill).
+// Waves and steps in flight: sixteen waves pay for a long k alone, from 8192 on,
+// where every wave has its four steps (microseconds in a graph with eight and
+// sixteen, e4m3, m 1, cold weights: n 4096 k 4096 6.1 and 6.3, 8192 10.0 and 8.9,
+// 12288 13.8 and 13.3, 16384 18.8 and 16.6; n 8192 9.2 and 10.9, 15.9 and 15.4,
+// 23.3 and 24.3, 32.7 and 30.1; f16 results alike), and only where their four
+// steps fit 128 registers: not with a scale for each row of B (22 spill).
 template <int TYPE, int EP, int SM>
 hipError_t pick(const ProductArgs& p, hipStream_t stream)
 {
