@@ -791,3 +791,38 @@ def test_ragged_backward_past_32_bits(k):
     sx, sg, su = qse.gated_ffn_backward(x[-127:], wg, wu, dh[-127:])
     assert torch.equal(dx[-127:], sx) and torch.equal(dg, sg) and torch.equal(du, su)
     assert float(dx[:-3].abs().max()) == 0.0 and float(dx[-3].abs().max()) > 0.0
+
+
+def test_calls_from_two_threads():
+    say("threads")
+    import threading
+    g = gen(8)
+    x = torch.randn(200, 520, generator=g, device="cuda").half()
+    w = torch.randn(96, 520, generator=g, device="cuda").half()
+    dh = torch.randn(200, 96, generator=g, device="cuda").half()
+    wq = qse.rotate_quantize(w, bits=3, scales="tile")
+
+    def work():
+        q, s = qse.rotate_quantize(x, bits=3)
+        return [q.float(), s, qse.scaled_matmul(q, s, *wq, out_dtype=torch.float32),
+                qse.gated_ffn(x, w, w), *qse.gated_ffn_backward(x, w, w, dh)]
+    want = work()
+    torch.cuda.synchronize()
+    results, errors = [], []
+
+    def run():
+        try:
+            stream = torch.cuda.Stream()
+            with torch.cuda.stream(stream):
+                got = [work() for _ in range(20)]
+            stream.synchronize()
+            results.extend(got)
+        except Exception as e:      # (a thread's exception would be lost)
+            errors.append(e)
+    threads = [threading.Thread(target=run) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors and len(results) == 40
+    assert all(torch.equal(a, b) for got in results for a, b in zip(got, want))
