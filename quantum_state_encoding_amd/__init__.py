@@ -23,7 +23,8 @@ __all__ = ["Plan", "FwtError", "execute", "stream_copy", "library_path", "load_l
            "FWT_OK", "FWT_EINVAL", "FWT_EALIGN", "FWT_EUNSUPPORTED", "FWT_EHIP",
            "FWT_ENOMEM", "FWT_ESCRATCH", "STATIC_SCRATCH_BYTES", "ablation_execute_static",
            "EXPORTED_SYMBOLS", "workspace_status", "rotate_quantize", "scaled_matmul",
-           "gated_ffn", "gated_ffn_backward"]
+           "gated_ffn", "gated_ffn_backward", "rotate_quantize_int8", "int8_matmul",
+           "grouped_matmul", "grouped_matmul_backward"]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 _LIB_PATH = os.path.join(_HERE, "libfwt.so")
@@ -551,3 +552,5 @@ def stream_copy(dst, src, stream=None):
 
 
 from .ffn import gated_ffn, gated_ffn_backward, rotate_quantize, scaled_matmul  # noqa: E402
+from .experts import (grouped_matmul, grouped_matmul_backward, int8_matmul,  # noqa: E402
+                      rotate_quantize_int8)

@@ -17,9 +17,12 @@ SOURCES = [os.path.join(CSRC, f) for f in ("fwt_kernels.hip", "fwt_onepass.hip",
                                            "fwt_ablation.hip", "fwt_ozaki.hip",
                                            "fwt_static.hip", "fwt_api.cpp",
                                            "ffn_rotate.hip", "ffn_matmul.hip", "ffn_strip.hip",
-                                           "ffn_api.cpp")]
+                                           "ffn_api.cpp", "ffn_quantize8.hip", "ffn_int8.hip",
+                                           "ffn_grouped.hip", "experts_api.cpp")]
 HEADERS = [os.path.join(CSRC, "fwt_internal.h"), os.path.join(CSRC, "fwt_device.h"),
-           os.path.join(CSRC, "ffn_internal.h"), os.path.join(CSRC, "ffn_device.h"),
+           os.path.join(CSRC, "ffn_internal.h"), os.path.join(CSRC, "ffn_device.h"), os.path.join(CSRC, "ffn_product.h"),
+           os.path.join(CSRC, "ffn_strip.h"), os.path.join(CSRC, "ffn_rotate.h"),
+           os.path.join(CSRC, "ffn_checks.h"), os.path.join(ROOT, "include", "fwt_experts.h"),
            os.path.join(ROOT, "include", "fwt.h"), os.path.join(ROOT, "include", "fwt_ffn.h")]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -1,0 +1,350 @@
+// C ABI of the 8-bit integer products and of the products grouped by expert
+// (include/fwt_experts.h): argument checks and the choice of kernels.
+#include "../../include/fwt_experts.h"
+
+#include <hip/hip_runtime_api.h>
+
+#include "ffn_checks.h"
+#include "ffn_internal.h"
+#include "fwt_internal.h"
+
+using qse::GroupArgs;
+using qse::ProductArgs;
+
+static_assert(FWT_INT8 == (int)qse::kTI8, "types");
+
+namespace {
+
+constexpr int64_t kMaxInt8K = (int64_t)1 << 17;      // sums of 128^2 stay in 32 bits
+constexpr int64_t kMaxExperts = (int64_t)1 << 16;
+
+// Row tiles of 128 that m rows of so many groups may have, and whether those
+// of 64 columns are too many for a launch.
+bool too_many_grouped(int64_t m, int64_t n, int64_t groups)
+{
+    const int64_t r = groups < m ? groups : m;
+    const int64_t tn = (n + 63) / 64;
+    return (m + r * 127) / 128 > qse::kFfnMaxTiles / tn ||
+           (m + r * 127) / 128 * tn >= qse::kFfnMaxTiles;
+}
+
+// An array for each expert, rows x cols: a sane row stride, ...
+bool rows_ok(int64_t rows, int64_t ld, int64_t cols)
+{
+    return ld >= cols && ld <= ((int64_t)1 << 40) && ld <= INT64_MAX / 8 / rows;
+}
+
+// ... and all of them as one array with a row for each (check_call sees to the
+// stride between experts).
+Array experts_array(const void* p, int64_t experts, int64_t rows, int64_t ld, int64_t cols,
+                    int64_t stride, int64_t size, bool written)
+{
+    return Array{p, experts, (rows - 1) * ld + cols,
+                 experts > 1 ? stride : (rows - 1) * ld + cols, size, written};
+}
+
+GroupArgs groups(const int32_t* ends, int64_t experts, int64_t m)
+{
+    GroupArgs g{};
+    g.ends = ends;
+    g.experts = (int)experts;
+    g.rows = m;
+    return g;
+}
+
+ProductArgs sizes(int64_t m, int64_t n, int64_t kbytes)
+{
+    ProductArgs p{};
+    p.m = m;
+    p.n = n;
+    p.kbytes = kbytes;
+    p.parts = 1;
+    return p;
+}
+
+// Tiles of 128 x 64 of the gradients of all experts' weights.
+bool too_many_weights(int64_t experts, int64_t n, int64_t k)
+{
+    const int64_t tiles = ((n + 127) / 128) * ((k + 63) / 64);
+    return too_many(n, k) || tiles * experts >= qse::kFfnMaxTiles;
+}
+
+// dx = dy w_e (contraction over n) and dw_e = dy^T x (over the rows).
+size_t backward_need(int64_t experts, int64_t m, int64_t n, int64_t k)
+{
+    GroupArgs g = groups(nullptr, experts, m);
+    const size_t dw = qse::grouped_t_workspace(sizes(n, k, 2 * m), g, FWT_BF16);
+    g.zero_rest = 1;
+    const size_t dx = qse::grouped_workspace(sizes(m, k, 2 * n), g, FWT_BF16, true);
+    return dx > dw ? dx : dw;
+}
+
+}  // namespace
+
+extern "C" {
+
+int fwt_rotate_quantize_int8(const void* x, fwt_ffn_dtype dtype, int64_t m, int64_t k,
+                             int64_t ldx, int bits, void* codes, int64_t ldcodes, float* s,
+                             hipStream_t stream)
+{
+    if (!dims_ok(m, 0, k) || bits < 0 || bits > qse::kFfnMaxBits || !is_out(dtype) ||
+        (k & (((int64_t)1 << bits) - 1)))
+        return FWT_EINVAL;
+    if (m == 0)
+        return FWT_OK;
+    if (!x || !codes || !s)
+        return FWT_EINVAL;
+    if (!aligned16(codes, ldcodes))
+        return FWT_EALIGN;
+    if (qse::quantize8_groups(m, k) >= qse::kFfnMaxTiles)
+        return FWT_EUNSUPPORTED;
+    const Array arrays[] = {
+        {x, m, k, ldx, size_of(dtype), false},
+        {codes, m, (k + 15) & ~(int64_t)15, ldcodes, 1, true},
+        {s, 1, m, m, 4, true},
+    };
+    const int rc = check_call(arrays, stream);
+    if (rc != FWT_OK)
+        return rc;
+    qse::Quantize8Args a{};
+    a.x = x;
+    a.ldx = ldx;
+    a.m = m;
+    a.k = k;
+    a.bits = bits;
+    a.q = (int8_t*)codes;
+    a.ldq = ldcodes;
+    a.s = s;
+    return status(qse::launch_quantize8(a, (int)dtype, stream));
+}
+
+int fwt_int8_matmul_workspace(int64_t m, int64_t n, int64_t k, fwt_ffn_dtype ctype,
+                              size_t* bytes)
+{
+    if (!bytes || !dims_ok(m, n, k) || !is_out(ctype))
+        return FWT_EINVAL;
+    *bytes = m == 0 || n == 0 ? 0 : qse::int8_workspace(sizes(m, n, k));
+    return FWT_OK;
+}
+
+int fwt_int8_matmul(const void* a, int64_t lda, const float* a_scales, const void* b,
+                    int64_t ldb, const float* b_scales, int64_t m, int64_t n, int64_t k, void* c,
+                    fwt_ffn_dtype ctype, int64_t ldc, void* ws, size_t ws_bytes,
+                    hipStream_t stream)
+{
+    size_t need = 0;
+    const int rc0 = fwt_int8_matmul_workspace(m, n, k, ctype, &need);
+    if (rc0 != FWT_OK)
+        return rc0;
+    if (m == 0 || n == 0)
+        return FWT_OK;
+    if (!ws)
+        need = 0;
+    if (ws_bytes < need)
+        return FWT_EINVAL;
+    if (need && !aligned16(ws, 0))
+        return FWT_EALIGN;
+    if (!a || !b || !c || !a_scales || !b_scales)
+        return FWT_EINVAL;
+    if (!aligned16(a, lda) || !aligned16(b, ldb))
+        return FWT_EALIGN;
+    if (k >= kMaxInt8K || lda >= qse::kFfnMaxStride || ldb >= qse::kFfnMaxStride ||
+        too_many(m, n))
+        return FWT_EUNSUPPORTED;
+    const Array arrays[] = {
+        {a, m, k, lda, 1, false},
+        {b, n, k, ldb, 1, false},
+        {a_scales, 1, m, m, 4, false},
+        {b_scales, 1, n, n, 4, false},
+        {c, m, n, ldc, size_of(ctype), true},
+        need ? Array{ws, 1, (int64_t)need, (int64_t)need, 1, true} : kNone,
+    };
+    const int rc = check_call(arrays, stream);
+    if (rc != FWT_OK)
+        return rc;
+    ProductArgs p = sizes(m, n, k);
+    p.a = a;
+    p.b0 = b;
+    p.lda = lda;
+    p.ldb0 = ldb;
+    p.sa = a_scales;
+    p.sb0 = b_scales;
+    p.c = c;
+    p.ldc = ldc;
+    p.ctype = (int)ctype;
+    p.may_split = need != 0;
+    p.partial = ws;
+    return status(qse::launch_int8(p, stream));
+}
+
+int fwt_grouped_matmul_workspace(int dtype, int64_t experts, int64_t m, int64_t n, int64_t k,
+                                 size_t* bytes)
+{
+    if (!bytes || !dims_ok(m, n, k) || experts < 1 ||
+        (!is16(dtype) && dtype != FWT_INT8))
+        return FWT_EINVAL;
+    *bytes = 0;
+    if (m == 0 || n == 0 || experts > kMaxExperts || too_many_grouped(m, n, experts + 1))
+        return FWT_OK;                   // (no work, or refused)
+    GroupArgs g = groups(nullptr, experts, m);
+    g.zero_rest = 1;
+    *bytes = qse::grouped_workspace(sizes(m, n, k * size_of(dtype)), g, dtype, false);
+    return FWT_OK;
+}
+
+int fwt_grouped_matmul(const void* x, int64_t ldx, const float* x_scales, const void* w,
+                       int64_t ldw, int64_t stride_w, const float* w_scales,
+                       const int32_t* ends, int64_t experts, int dtype, int64_t m, int64_t n,
+                       int64_t k, void* y, fwt_ffn_dtype ytype, int64_t ldy, int zero_rest,
+                       void* ws, size_t ws_bytes, hipStream_t stream)
+{
+    size_t need = 0;
+    const int rc0 = fwt_grouped_matmul_workspace(dtype, experts, m, n, k, &need);
+    if (rc0 != FWT_OK)
+        return rc0;
+    const bool i8 = dtype == FWT_INT8;
+    if (i8 ? !is_out(ytype) : (int)ytype != dtype)
+        return FWT_EINVAL;
+    if (m == 0 || n == 0)
+        return FWT_OK;
+    if (!ws)
+        need = 0;
+    if (ws_bytes < need)
+        return FWT_EINVAL;
+    if (need && !aligned16(ws, 0))
+        return FWT_EALIGN;
+    if (!x || !w || !y || !ends || i8 != (x_scales != nullptr) || i8 != (w_scales != nullptr))
+        return FWT_EINVAL;
+    const int64_t sz = size_of(dtype);
+    if (i8 && (!aligned16(x, ldx) || !aligned16(w, ldw) || (experts > 1 && (stride_w & 15))))
+        return FWT_EALIGN;
+    if (experts > kMaxExperts || too_many_grouped(m, n, experts + 1) ||
+        ldx * sz >= qse::kFfnMaxStride || ldw * sz >= qse::kFfnMaxStride ||
+        (i8 && k >= kMaxInt8K))
+        return FWT_EUNSUPPORTED;
+    if (!rows_ok(n, ldw, k))
+        return FWT_EINVAL;
+    const Array arrays[] = {
+        {x, m, k, ldx, sz, false},
+        experts_array(w, experts, n, ldw, k, stride_w, sz, false),
+        {ends, 1, experts, experts, 4, false},
+        {y, m, n, ldy, size_of(ytype), true},
+        i8 ? Array{x_scales, 1, m, m, 4, false} : kNone,
+        i8 ? Array{w_scales, experts, n, n, 4, false} : kNone,
+        need ? Array{ws, 1, (int64_t)need, (int64_t)need, 1, true} : kNone,
+    };
+    const int rc = check_call(arrays, stream);
+    if (rc != FWT_OK)
+        return rc;
+    ProductArgs p = sizes(m, n, k * sz);
+    p.a = x;
+    p.lda = ldx * sz;
+    p.b0 = w;
+    p.ldb0 = ldw * sz;
+    p.sa = x_scales;
+    p.sb0 = w_scales;
+    p.c = y;
+    p.ldc = ldy;
+    p.ctype = (int)ytype;
+    p.may_split = need != 0;
+    p.partial = ws;
+    GroupArgs g = groups(ends, experts, m);
+    g.stride_b = experts > 1 ? stride_w * sz : 0;
+    g.zero_rest = zero_rest != 0;
+    return status(qse::launch_grouped(p, g, dtype, false, stream));
+}
+
+int fwt_grouped_matmul_backward_workspace(int64_t experts, int64_t m, int64_t n, int64_t k,
+                                          size_t* bytes)
+{
+    if (!bytes || !dims_ok(m, n, k) || experts < 1)
+        return FWT_EINVAL;
+    *bytes = 0;
+    if (m == 0 || n == 0 || experts > kMaxExperts || too_many_grouped(m, k, experts + 1) ||
+        too_many_weights(experts, n, k))
+        return FWT_OK;                   // (no sums, or refused)
+    *bytes = backward_need(experts, m, n, k);
+    return FWT_OK;
+}
+
+int fwt_grouped_matmul_backward(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                int64_t stride_w, const int32_t* ends, int64_t experts,
+                                const void* dy, int64_t lddy, fwt_ffn_dtype dtype, int64_t m,
+                                int64_t n, int64_t k, void* dx, int64_t lddx, void* dw,
+                                int64_t lddw, int64_t stride_dw, void* ws, size_t ws_bytes,
+                                hipStream_t stream)
+{
+    size_t need = 0;
+    const int rc0 = fwt_grouped_matmul_backward_workspace(experts, m, n, k, &need);
+    if (rc0 != FWT_OK)
+        return rc0;
+    if (!is16(dtype))
+        return FWT_EINVAL;
+    const bool rows = m != 0 && dx, weights = n != 0 && dw;
+    if (!rows && !weights)
+        return FWT_OK;
+    if (!ws)
+        need = 0;
+    if (ws_bytes < need)
+        return FWT_EINVAL;
+    if (need && !aligned16(ws, 0))
+        return FWT_EALIGN;
+    const bool sums = m != 0 && n != 0;      // otherwise what is written is zeros
+    if (!ends || (sums && (!dy || (rows && !w) || (weights && !x))))
+        return FWT_EINVAL;
+    if (experts > kMaxExperts || (m && too_many_grouped(m, k, experts + 1)) ||
+        (n && too_many_weights(experts, n, k)) || ldx * 2 >= qse::kFfnMaxStride ||
+        ldw * 2 >= qse::kFfnMaxStride || lddy * 2 >= qse::kFfnMaxStride)
+        return FWT_EUNSUPPORTED;
+    if (n && ((sums && rows && !rows_ok(n, ldw, k)) || (weights && !rows_ok(n, lddw, k))))
+        return FWT_EINVAL;
+    const Array arrays[] = {
+        sums && weights ? Array{x, m, k, ldx, 2, false} : kNone,
+        sums && rows ? experts_array(w, experts, n, ldw, k, stride_w, 2, false) : kNone,
+        sums ? Array{dy, m, n, lddy, 2, false} : kNone,
+        {ends, 1, experts, experts, 4, false},
+        rows ? Array{dx, m, k, lddx, 2, true} : kNone,
+        weights ? experts_array(dw, experts, n, lddw, k, stride_dw, 2, true) : kNone,
+        need ? Array{ws, 1, (int64_t)need, (int64_t)need, 1, true} : kNone,
+    };
+    const int rc = check_call(arrays, stream);
+    if (rc != FWT_OK)
+        return rc;
+    GroupArgs g = groups(ends, experts, m);
+    hipError_t e = hipSuccess;
+    if (rows && !sums) {
+        e = qse::launch_zero16(dx, lddx, m, k, stream);
+    } else if (rows) {
+        // the contraction runs over n, which w has as its rows
+        ProductArgs p = sizes(m, k, 2 * n);
+        p.a = dy;
+        p.lda = 2 * lddy;
+        p.b0 = w;
+        p.ldb0 = 2 * ldw;
+        p.c = dx;
+        p.ldc = lddx;
+        p.ctype = (int)dtype;
+        p.may_split = need != 0;
+        p.partial = ws;
+        GroupArgs d = g;
+        d.stride_b = experts > 1 ? 2 * stride_w : 0;
+        d.zero_rest = 1;
+        e = qse::launch_grouped(p, d, (int)dtype, true, stream);
+    }
+    if (e != hipSuccess || !weights)
+        return status(e);
+    ProductArgs p = sizes(n, k, 2 * m);
+    p.a = dy;
+    p.lda = 2 * lddy;
+    p.b0 = x;
+    p.ldb0 = 2 * ldx;
+    p.c = dw;
+    p.ldc = lddw;
+    p.ctype = (int)dtype;
+    p.may_split = need != 0;
+    p.partial = ws;
+    g.stride_c = experts > 1 ? stride_dw : 0;
+    return status(qse::launch_grouped_t(p, g, (int)dtype, stream));
+}
+
+}  // extern "C"

@@ -4,6 +4,8 @@
 
 #include <hip/hip_runtime.h>
 
+#include <type_traits>
+
 #include "ffn_internal.h"
 
 namespace qse {
@@ -14,6 +16,12 @@ typedef int v8i __attribute__((ext_vector_type(8)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef _Float16 v8h __attribute__((ext_vector_type(8)));
+
+// Four sums of a matrix instruction.
+template <int TYPE>
+using Sums = std::conditional_t<TYPE == kTI8, v4i, v4f>;
+
+constexpr int kStep = 128;   // bytes of k that a product takes at a time
 
 constexpr unsigned kRsrcFlags = 0x00020000;   // raw 32-bit buffer
 
@@ -64,6 +72,14 @@ __device__ __forceinline__ v8h widen(int lo, int hi)
     const v2h p2 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false);
     const v2h p3 = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true);
     return v8h{p0[0], p0[1], p1[0], p1[1], p2[0], p2[1], p3[0], p3[1]};
+}
+
+// 8-bit integers (kTI8) are two instructions of 64 elements with 32-bit integer
+// sums: nothing is lost.
+__device__ __forceinline__ v4i matrix_step_i8(const v4i* a, const v4i* b, v4i acc)
+{
+    acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(a[0], b[0], acc, 0, 0, 0);
+    return __builtin_amdgcn_mfma_i32_16x16x64_i8(a[1], b[1], acc, 0, 0, 0);
 }
 
 // acc += a b over 32 bytes of each operand's row: one matrix instruction of

@@ -1,0 +1,71 @@
+// Products of 8-bit integers with a scale for each row of A and of B:
+// C[m][n] = sa[m] sb[n] sum_k A[m][k] B[n][k], in ffn_matmul.hip's tiles and
+// ffn_strip.hip's strips.  The sums are 32-bit integers, exact, so neither the
+// tile nor the number of shares changes a result; the scales are the epilogue.
+#include <hip/hip_runtime.h>
+
+#include "ffn_product.h"
+#include "ffn_strip.h"
+
+namespace qse {
+namespace {
+
+// Microseconds a step of 128, as ffn_matmul.hip's table has them.
+hipError_t tiles_int8(const ProductArgs& p, size_t* query, hipStream_t stream)
+{
+    constexpr Tile tiles[] = {{256, 256, 256, 1.5f, 0},
+                              {128, 128, 512, 1.0f, 0},
+                              {128, 128, 256, .60f, 0},
+                              {64, 64, 512, .40f, 0},
+                              {64, 64, 256, .26f, 64 * 64}};
+    const Choice c = cheapest(tiles, p);
+    if (query) {
+        *query = c.bytes;
+        return hipSuccess;
+    }
+    switch (c.tile) {
+    case 0:
+        return run<kTI8, 256, 256, 2, 4, 1, 2, kEpStore, kNoScale>(p, 1, stream);
+    case 1:
+        return run<kTI8, 128, 128, 2, 2, 1, 2, kEpStore, kNoScale>(p, 1, stream);
+    case 2:
+        return run<kTI8, 128, 128, 2, 2, 2, 2, kEpStore, kNoScale>(p, 1, stream);
+    case 3:
+        return run<kTI8, 64, 64, 2, 2, 2, 2, kEpStore, kNoScale>(p, 1, stream);
+    }
+    return run<kTI8, 64, 64, 2, 2, 2, 4, kEpStore, kNoScale>(p, c.splits, stream);
+}
+
+// Few rows of A.
+bool strips(const ProductArgs& p) { return p.m <= kStripRows && (p.n + 63) / 64 < 256; }
+
+template <int MT, int W, int U>
+hipError_t strip(const ProductArgs& p, hipStream_t stream)
+{
+    hipLaunchKernelGGL((strip_kernel<kTI8, MT, W, U, kEpStore, 0, false>),
+                       dim3((unsigned)((p.n + 15) / 16)), dim3(64 * W), W * MT * 4 * 64 * 4, stream,
+                       p);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_int8(const ProductArgs& p, hipStream_t stream)
+{
+    if (!strips(p))
+        return tiles_int8(p, nullptr, stream);
+    if (p.m > 16)
+        return strip<2, 8, 2>(p, stream);
+    return p.kbytes >= 64 * kStep ? strip<1, 16, 4>(p, stream) : strip<1, 8, 4>(p, stream);
+}
+
+size_t int8_workspace(ProductArgs p)
+{
+    size_t bytes = 0;
+    p.may_split = 1;
+    if (!strips(p))
+        (void)tiles_int8(p, &bytes, nullptr);
+    return bytes;
+}
+
+}  // namespace qse

@@ -15,7 +15,8 @@ constexpr int kFfnMaxBitsT = 7;       // the same, for a transposed input
 // Element types, as fwt_ffn_dtype numbers them.
 // kTE4m3Exact: e4m3 operands whose products and sums keep 32 bits, for f16 and
 // fp32 results.
-enum FfnType : int { kTBf16 = 0, kTF16 = 1, kTF32 = 2, kTE4m3 = 3, kTE4m3Exact = 4 };
+// kTI8: 8-bit integers, with 32-bit integer sums.
+enum FfnType : int { kTBf16 = 0, kTF16 = 1, kTF32 = 2, kTE4m3 = 3, kTE4m3Exact = 4, kTI8 = 5 };
 
 // Largest row stride of a product's operand, in bytes: 256 rows of a tile
 // stay within a 32-bit offset of its first one.
@@ -84,6 +85,46 @@ size_t product_workspace(ProductArgs p, int type, int epilogue, bool row_scales)
 constexpr int kStripRows = 32;
 hipError_t launch_strip(const ProductArgs& p, int type, int epilogue, bool row_scales,
                         hipStream_t stream);
+
+// Products of rows grouped by expert.  ends (device): group e has the rows from
+// ends[e - 1] up to ends[e] of `rows`.
+struct GroupArgs {
+    const int32_t* ends;
+    int experts;
+    int64_t rows;
+    int64_t stride_b;       // bytes from an expert's weights to the next one's
+    int64_t stride_c;       // elements between the experts' results (gradients of weights)
+    int zero_rest;          // rows of no expert become 0
+};
+// C[i] = A[i] B_e^T for the rows i of group e; p.m, the sizes of all of A.
+// bt: 16-bit types, B_e is stored [k][n].
+hipError_t launch_grouped(const ProductArgs& p, const GroupArgs& g, int type, bool bt,
+                          hipStream_t stream);
+// C_e = A^T B over the rows of group e: A is rows x p.m, B rows x p.n, 16 bits.
+hipError_t launch_grouped_t(const ProductArgs& p, const GroupArgs& g, int type,
+                            hipStream_t stream);
+// Bytes of ProductArgs::partial that these would use (p.kbytes of
+// launch_grouped_t: of all rows).
+size_t grouped_workspace(ProductArgs p, const GroupArgs& g, int type, bool bt);
+size_t grouped_t_workspace(ProductArgs p, const GroupArgs& g, int type);
+
+// A product of 8-bit integers with a scale for each row of A and of B.
+hipError_t launch_int8(const ProductArgs& p, hipStream_t stream);
+size_t int8_workspace(ProductArgs p);
+
+// Rotation and quantisation to 8-bit integers with a scale for each row.
+struct Quantize8Args {
+    const void* x;
+    int64_t ldx;            // elements
+    int64_t m, k;
+    int bits;
+    int8_t* q;
+    int64_t ldq;            // bytes
+    float* s;
+};
+hipError_t launch_quantize8(const Quantize8Args& p, int type, hipStream_t stream);
+// Workgroups of that launch.
+int64_t quantize8_groups(int64_t m, int64_t k);
 
 // Zeros to rows x cols 16-bit elements.
 hipError_t launch_zero16(void* dst, int64_t ld, int64_t rows, int64_t cols, hipStream_t stream);
