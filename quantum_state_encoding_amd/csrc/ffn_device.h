@@ -123,6 +123,20 @@ __device__ __forceinline__ v4f matrix_step(const v4i* a, const v4i* b, v4f acc)
     }
 }
 
+// Half of such a step, of 16-bit types and 8-bit integers: 16 bytes a lane.
+template <int TYPE>
+__device__ __forceinline__ Sums<TYPE> half_step(v4i a, v4i b, Sums<TYPE> acc)
+{
+    if constexpr (TYPE == kTI8)
+        return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, acc, 0, 0, 0);
+    else if constexpr (TYPE == kTBf16)
+        return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(v8bf, a),
+                                                       __builtin_bit_cast(v8bf, b), acc, 0, 0, 0);
+    else
+        return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(v8h, a),
+                                                      __builtin_bit_cast(v8h, b), acc, 0, 0, 0);
+}
+
 // Sixteen bytes at any address.
 __device__ __forceinline__ v4i load16(const char* p)
 {
@@ -247,6 +261,28 @@ __device__ __forceinline__ void store4(void* c, int64_t at, v4f v, int type, int
             if (k < cnt)
                 p[k] = h[k];
     }
+}
+
+// Eight neighbours.
+__device__ __forceinline__ void store8(void* c, int64_t at, v4f u, v4f v, int type, int cnt)
+{
+    if (type != kTF32 && cnt == 8) {
+        typedef unsigned short v8s __attribute__((ext_vector_type(8)));
+        struct __attribute__((packed)) Any {
+            v8s v;
+        };
+        v8s h;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            h[k] = to16(u[k], type == kTBf16);
+            h[k + 4] = to16(v[k], type == kTBf16);
+        }
+        ((Any*)((unsigned short*)c + at))->v = h;
+        return;
+    }
+    store4(c, at, u, type, cnt < 4 ? cnt : 4);
+    if (cnt > 4)
+        store4(c, at + 4, v, type, cnt - 4);
 }
 
 // f16 gradients between two products.  dg and du are rounded to f16 for the

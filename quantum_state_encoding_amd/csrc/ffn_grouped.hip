@@ -129,7 +129,8 @@ grouped_kernel(ProductArgs p, const GroupArgs g)
     enter<TYPE>(p, g, at);
     int tm, tn;
     tile_at(at.tile, (at.rows + BM - 1) / BM, p.tiles_n, tm, tn);
-    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, false, BT>(
+    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, false, BT,
+                 BM == 256 && !REG>(
         p, tm, tn, (int)blockIdx.y, EveryWorkgroup{});
 }
 
@@ -216,7 +217,8 @@ grouped_grad_kernel(ProductArgs p, const GroupArgs g)
         if ((int)blockIdx.y * ((steps + p.splits - 1) / p.splits) >= steps)
             return;
     }
-    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, true, true>(
+    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, true, true,
+                 BM == 256 && !REG>(
         p, where.tm, where.tn, (int)blockIdx.y, where);
 }
 

@@ -25,7 +25,8 @@ hipError_t tiles_int8(const ProductArgs& p, size_t* query, hipStream_t stream)
     }
     switch (c.tile) {
     case 0:
-        return run<kTI8, 256, 256, 2, 4, 1, 2, kEpStore, kNoScale>(p, 1, stream);
+        return run<kTI8, 256, 256, 2, 4, 1, 2, kEpStore, kNoScale, kAligned, false, false, true>(
+            p, 1, stream);
     case 1:
         return run<kTI8, 128, 128, 2, 2, 1, 2, kEpStore, kNoScale>(p, 1, stream);
     case 2:

@@ -58,22 +58,29 @@ __device__ __forceinline__ void tile_of(int w, int tiles_m, int tiles_n, int& tm
 // 32 bytes each, so those 32-byte units are spread over the banks by k.
 __device__ __forceinline__ int unit_mask(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
 
-template <int BR>
-__device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile, int block, int lane)
+// WIDE: the block's rows are every second four of 32 (wide_row).
+template <int BR, bool WIDE = false>
+__device__ __forceinline__ v4i read_t_half(const unsigned char* tile, int block, int lane, int h)
 {
     typedef short v4s __attribute__((ext_vector_type(4)));
     const int q = lane >> 4, l16 = lane & 15;
+    const int unit = WIDE ? (block & ~1) + ((l16 >> 1) & 1) : block;
     const unsigned char* at = tile + (q * 8 + (l16 >> 2)) * (BR * 2) +
-                              ((block ^ unit_mask(q * 8 + (l16 >> 2))) * 32) + (l16 & 3) * 8;
+                              ((unit ^ unit_mask(q * 8 + (l16 >> 2))) * 32) +
+                              (WIDE ? (l16 & 1) * 16 + (block & 1) * 8 : (l16 & 3) * 8);
+    v4s r[2];
 #pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        v4s r[2];
+    for (int e = 0; e < 2; ++e)
+        r[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+            (__attribute__((address_space(3))) v4s*)(at + (h * 32 + e * 4) * (BR * 2)));
+    return __builtin_bit_cast(v4i, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7));
+}
+template <int BR>
+__device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile, int block, int lane)
+{
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            r[e] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-                (__attribute__((address_space(3))) v4s*)(at + (h * 32 + e * 4) * (BR * 2)));
-        out[h] = __builtin_bit_cast(v4i, __builtin_shufflevector(r[0], r[1], 0, 1, 2, 3, 4, 5, 6, 7));
-    }
+    for (int h = 0; h < 2; ++h)
+        out[h] = read_t_half<BR>(tile, block, lane, h);
 }
 
 // From a tile's sums to results: lane l holds rows l % 16 * TM .. of A (AT:
@@ -85,8 +92,16 @@ __device__ __forceinline__ void read_t(v4i (&out)[2], const unsigned char* tile,
 // fetching the code: so a whole tile has a path of its own without bounds, and
 // each activation too (gated e4m3 m 8192 n 16384 k 4096: 992 us without,
 // 970 with them).
+//
+// WIDE (plain stores): B's rows stand in LDS as wide_row says, so that a lane has
+// eight neighbours of each pair of blocks and a row of C gets 64 bytes at once.
+__device__ __forceinline__ constexpr int wide_row(int r)
+{
+    return (r & ~31) | ((r >> 2) & 3) * 8 | ((r >> 4) & 1) * 4 | (r & 3);
+}
+
 template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN, int ACT,
-          bool WHOLE>
+          bool WHOLE, bool WIDE>
 __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<TYPE> (&acc)[NI][TN],
                                                int i0, int j0, int tm, int tn, int wave, int lane)
 {
@@ -108,11 +123,14 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
         return wm * (TM * 16) + (AT ? (i0 + i) * 16 + l16 : l16 * TM + i0 + i);
     };
     const auto column_at = [=](int j) __attribute__((always_inline)) {
-        return wn * kRowsB + (j0 + j) * 16 + q * 4;
+        return WIDE ? wn * kRowsB + (j >> 1) * 32 + q * 8 + (j & 1) * 4
+                    : wn * kRowsB + (j0 + j) * 16 + q * 4;
     };
+    constexpr int kSide = WIDE ? 8 : 4;      // neighbours of a store
     const auto count_at = [=](int nc) __attribute__((always_inline)) {
-        return WHOLE || nrows - nc > 4 ? 4 : nrows - nc;
+        return WHOLE || nrows - nc > kSide ? kSide : nrows - nc;
     };
+    v4f before = v4f{0.f, 0.f, 0.f, 0.f};
     // f16 gradients: the factor that dg and du are stored with, or that the
     // sums of what was stored so are multiplied by
     constexpr bool kGrad16 = EP == kEpGateGrad && TYPE == kTF16;
@@ -170,7 +188,7 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
         }
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
-            const int nc = column_at(j);
+            const int nc = column_at(WIDE ? j & ~1 : j);
             if (!WHOLE && nc >= nrows)
                 continue;
             const int64_t at = m * ldc + n0 + nc;
@@ -213,7 +231,12 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
             }
             if constexpr (EP == kEpGateGrad)
                 store4(c, at + p.part_c, u, ctype, count_at(nc));
-            store4(c, at, v, ctype, count_at(nc));
+            if constexpr (!WIDE)
+                store4(c, at, v, ctype, count_at(nc));
+            else if (j & 1)
+                store8(c, at, before, v, ctype, count_at(nc));
+            else
+                before = v;
         }
         // (rows side by side would need more registers than there are)
         if constexpr (kGrad16)
@@ -225,17 +248,20 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
     }
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, int NI, int TN>
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, bool WIDE = false, int NI, int TN>
 __device__ __forceinline__ void finish_rows(const ProductArgs& p, const Sums<TYPE> (&acc)[NI][TN], int i0,
                                             int j0, int tm, int tn, int wave, int lane)
 {
     constexpr int BNO = EP != kEpStore ? BN / 2 : BN;
     if ((int64_t)(tm + 1) * BM > p.m || (int64_t)(tn + 1) * BNO > p.n)
-        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, -1, false>(p, acc, i0, j0, tm, tn, wave, lane);
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, -1, false, WIDE>(
+            p, acc, i0, j0, tm, tn, wave, lane);
     else if (EP == kEpStore || p.act == 0)
-        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 0, true>(p, acc, i0, j0, tm, tn, wave, lane);
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 0, true, WIDE>(
+            p, acc, i0, j0, tm, tn, wave, lane);
     else
-        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 1, true>(p, acc, i0, j0, tm, tn, wave, lane);
+        finish_rows_as<TYPE, BM, BN, WM, WN, EP, AT, NI, TN, 1, true, WIDE>(
+            p, acc, i0, j0, tm, tn, wave, lane);
 }
 
 // REG: the operands' rows need not be 16-byte aligned; they go through
@@ -263,7 +289,7 @@ struct EveryWorkgroup {
 // (asked for late, not to hold registers); part: its share of the contraction's
 // p.splits.
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG,
-          bool AT, bool BT, class Where>
+          bool AT, bool BT, bool PIPE = false, class Where>
 __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int tn, int part,
                                              const Where& where)
 {
@@ -314,7 +340,8 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
     const int64_t kround = (p.kbytes + 15) & ~(int64_t)15;
     const int lr = lane >> 3, lc = slot(wave * 8 + (lane >> 3), lane & 7);
     const int ra0 = row_of(wave * 8 + lr, TM * 16);
-    const int rb0 = wave * 8 + lr;
+    constexpr bool kWide = PIPE && !kDual;
+    const int rb0 = kWide ? wide_row(wave * 8 + lr) : wave * 8 + lr;
     constexpr int kCa = BM / 8, kCb = BN / 8;        // chunks in a row of k
     const int ka0 = wave * (64 / kCa) + lane / kCa, kb0 = wave * (64 / kCb) + lane / kCb;
     const int ca = (((lane % kCa) >> 1) ^ unit_mask(ka0)) * 2 + (lane & 1);
@@ -517,6 +544,115 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
     const int sbo = (BM + BN) * kStep + (BM + wn * kRowsB + q * 4) * 4;
     const int ktail = (int)(p.kbytes % kStep);
 
+    auto cut = [&](int kt, unsigned char* buf) __attribute__((always_inline)) {
+        // Past the end of k both operands are 0, whatever was read there.
+        const bool mine = kt == all - 1 || kt == nks - 1;
+        if constexpr (AT)
+            for (int c = (ktail / 2) * kCa + tid; mine && c < BM * 8; c += 64 * W)
+                *(v4i*)(buf + c * 16) = v4i{0, 0, 0, 0};
+        if constexpr (BT)
+            for (int c = (ktail / 2) * kCb + tid; mine && c < BN * 8; c += 64 * W)
+                *(v4i*)(buf + BM * kStep + c * 16) = v4i{0, 0, 0, 0};
+        for (int r = tid + (AT ? BM : 0); mine && r < BM + (BT ? 0 : BN); r += 64 * W) {
+            for (int c = ktail >> 4; c < 8; ++c) {
+                v4i* at = (v4i*)(buf + r * kStep + slot(r, c) * 16);
+                const int keep = ktail - c * 16;   // bytes of this chunk
+                v4i v = v4i{0, 0, 0, 0};
+                if (keep > 0) {
+                    v = *at;
+#pragma unroll
+                    for (int w = 0; w < 4; ++w) {
+                        const int b = keep - 4 * w;
+                        v[w] = b >= 4 ? v[w] : b <= 0 ? 0 : v[w] & ((1 << (8 * b)) - 1);
+                    }
+                }
+                *at = v;
+            }
+        }
+    };
+
+    if constexpr (PIPE) {
+        // Half a step's operands in registers ahead of its matrix instructions:
+        // a row block of A is replaced by the next half's as soon as its four
+        // have been issued, so the waves of a SIMD have matrix instructions on both
+        // sides of the barrier.  At the barrier, in a step's second half, all of
+        // the step has been read, so its buffer takes the step after the next, whose
+        // loads have a step's time; the next step's have arrived.
+        static_assert(!PIPE || (!REG && SM == kNoScale && WK == 1 && NS == 2 && TM >= TN + 1), "PIPE");
+        constexpr int kAt = 1;       // row blocks of the second half before the barrier
+        v4i a[TM], b[2][TN];
+        const auto read_a = [&](const unsigned char* buf, int h, int i) __attribute__((always_inline)) {
+            if constexpr (AT)
+                return read_t_half<BM>(buf, wm * TM + i, lane, h);
+            else
+                return *(const v4i*)(buf + (ao ^ (h * 64)) + i * 16 * kStep);
+        };
+        const auto read_b = [&](const unsigned char* buf, int h, int j) __attribute__((always_inline)) {
+            const int row = kDual && j >= TN / 2 ? BNO + (j - TN / 2) * 16 : j * 16;
+            if constexpr (BT)
+                return read_t_half<BN, kWide>(buf + BM * kStep, wn * TN + j, lane, h);
+            else
+                return *(const v4i*)(buf + (bo ^ (h * 64)) + row * kStep);
+        };
+        const auto ragged = [&](int kt) __attribute__((always_inline)) {
+            return ktail && (kt == all - 1 || (p.parts > 1 && kt == nks - 1));
+        };
+        if (first + 1 < nk) {
+            stage(first + 1);
+            wait_vm<kLoads>();
+        } else {
+            wait_vm<0>();
+        }
+        __syncthreads();
+        if (first < nk && ragged(first)) {
+            cut(first, lds + buffer_of(first));
+            __syncthreads();
+        }
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+            b[0][j] = read_b(lds + buffer_of(first), 0, j);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+            a[i] = read_a(lds + buffer_of(first), 0, i);
+        for (int kt = first; kt < nk; ++kt) {
+            unsigned char* const cur = lds + buffer_of(kt);
+            unsigned char* const next = lds + buffer_of(kt + 1);
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = half_step<TYPE>(b[0][j], a[i], acc[i][j]);
+                a[i] = read_a(cur, 1, i);
+                if (i < TN)
+                    b[1][i] = read_b(cur, 1, i);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+#pragma unroll
+            for (int i = 0; i < TM; ++i) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    acc[i][j] = half_step<TYPE>(b[1][j], a[i], acc[i][j]);
+                if (i == kAt) {
+                    wait_vm<0>();
+                    __syncthreads();
+                    if (kt + 1 < nk && ragged(kt + 1)) {
+                        cut(kt + 1, next);
+                        __syncthreads();
+                    }
+                    if (kt + 2 < nk)
+                        stage(kt + 2);
+#pragma unroll
+                    for (int e = 0; e < kAt; ++e)
+                        a[e] = read_a(next, 0, e);
+                }
+                if (i >= kAt)
+                    a[i] = read_a(next, 0, i);
+                if (i >= kAt && i - kAt < TN)
+                    b[0][i - kAt] = read_b(next, 0, i - kAt);
+                __builtin_amdgcn_sched_barrier(0);
+            }
+        }
+    } else
     for (int kt = first + kg; kt - kg < nk; kt += WK) {
         // The step's own loads have arrived, those of later steps go on.
         if constexpr (!REG) {
@@ -529,30 +665,7 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
         unsigned char* buf = lds + buffer_of(kt);
         const int k0 = kt - kg;      // the round's first step
         if (!REG && ktail && (k0 + WK >= all || (p.parts > 1 && k0 < nks && k0 + WK >= nks))) {
-            // Past the end of k both operands are 0, whatever was read there.
-            const bool mine = kt == all - 1 || kt == nks - 1;
-            if constexpr (AT)
-                for (int c = (ktail / 2) * kCa + tid; mine && c < BM * 8; c += 64 * W)
-                    *(v4i*)(buf + c * 16) = v4i{0, 0, 0, 0};
-            if constexpr (BT)
-                for (int c = (ktail / 2) * kCb + tid; mine && c < BN * 8; c += 64 * W)
-                    *(v4i*)(buf + BM * kStep + c * 16) = v4i{0, 0, 0, 0};
-            for (int r = tid + (AT ? BM : 0); mine && r < BM + (BT ? 0 : BN); r += 64 * W) {
-                for (int c = ktail >> 4; c < 8; ++c) {
-                    v4i* at = (v4i*)(buf + r * kStep + slot(r, c) * 16);
-                    const int keep = ktail - c * 16;   // bytes of this chunk
-                    v4i v = v4i{0, 0, 0, 0};
-                    if (keep > 0) {
-                        v = *at;
-#pragma unroll
-                        for (int w = 0; w < 4; ++w) {
-                            const int b = keep - 4 * w;
-                            v[w] = b >= 4 ? v[w] : b <= 0 ? 0 : v[w] & ((1 << (8 * b)) - 1);
-                        }
-                    }
-                    *at = v;
-                }
-            }
+            cut(kt, buf);
             __syncthreads();
         }
         v4i held[REG ? GA + GB : 1];
@@ -688,11 +801,11 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
                 out[(i * TN + j) * 64 * W] = acc[i][j];
         return;
     }
-    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, 0, 0, tm, tn, wave, lane);
+    finish_rows<TYPE, BM, BN, WM, WN, EP, AT, kWide>(p, acc, 0, 0, tm, tn, wave, lane);
 }
 
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG,
-          bool AT, bool BT>
+          bool AT, bool BT, bool PIPE = false>
 __global__ __launch_bounds__(64 * WM * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void
 product_kernel(const ProductArgs p)
 {
@@ -702,7 +815,7 @@ product_kernel(const ProductArgs p)
     }
     int tm, tn;
     tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-    product_body<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT>(
+    product_body<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT, PIPE>(
         p, tm, tn, (int)blockIdx.y, EveryWorkgroup{});
 }
 
@@ -758,7 +871,7 @@ __global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
 }
 
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG = kAligned,
-          bool AT = false, bool BT = false>
+          bool AT = false, bool BT = false, bool PIPE = false>
 hipError_t run(ProductArgs p, int splits, hipStream_t stream)
 {
     p.splits = splits;
@@ -767,7 +880,7 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
     static_assert(kLds <= 160 * 1024 && (size_t)(WK - 1) * BM * BN * 4 <= kLds, "LDS of a CU");
     p.tiles_m = (int)((p.m + BM - 1) / BM);
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
-    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT>;
+    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT, PIPE>;
     if (kLds > 65536) {
         // once for each device
         static std::atomic<uint64_t> done{0};
