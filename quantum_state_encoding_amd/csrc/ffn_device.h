@@ -123,6 +123,17 @@ __device__ __forceinline__ v4f matrix_step(const v4i* a, const v4i* b, v4f acc)
     }
 }
 
+// An integer sum times its row's scale and its column's, one after the other (the
+// scales' product alone may leave the range that the result is in), rounded after
+// each in every kernel: the last product and the rounding to f16 are not to
+// become one instruction.
+__device__ __forceinline__ float scaled(int sum, float sa, float sb)
+{
+    float v = (float)sum * sa * sb;
+    asm("" : "+v"(v));       // (v_fma_mixlo_f16 otherwise, with contraction off too)
+    return v;
+}
+
 // Half of such a step, of 16-bit types and 8-bit integers: 16 bytes a lane.
 template <int TYPE>
 __device__ __forceinline__ Sums<TYPE> half_step(v4i a, v4i b, Sums<TYPE> acc)
@@ -263,21 +274,31 @@ __device__ __forceinline__ void store4(void* c, int64_t at, v4f v, int type, int
     }
 }
 
+// Sixteen bytes to any address.
+__device__ __forceinline__ void put16(void* p, v4i v)
+{
+    struct __attribute__((packed)) Any {
+        v4i v;
+    };
+    ((Any*)p)->v = v;
+}
+
 // Eight neighbours.
+__device__ __forceinline__ v4i pack8(v4f u, v4f v, int type)
+{
+    typedef unsigned short v8s __attribute__((ext_vector_type(8)));
+    v8s h;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        h[k] = to16(u[k], type == kTBf16);
+        h[k + 4] = to16(v[k], type == kTBf16);
+    }
+    return __builtin_bit_cast(v4i, h);
+}
 __device__ __forceinline__ void store8(void* c, int64_t at, v4f u, v4f v, int type, int cnt)
 {
     if (type != kTF32 && cnt == 8) {
-        typedef unsigned short v8s __attribute__((ext_vector_type(8)));
-        struct __attribute__((packed)) Any {
-            v8s v;
-        };
-        v8s h;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-            h[k] = to16(u[k], type == kTBf16);
-            h[k + 4] = to16(v[k], type == kTBf16);
-        }
-        ((Any*)((unsigned short*)c + at))->v = h;
+        put16((unsigned short*)c + at, pack8(u, v, type));
         return;
     }
     store4(c, at, u, type, cnt < 4 ? cnt : 4);

@@ -186,6 +186,45 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
             if (m >= p.split_rows)
                 continue;
         }
+        if constexpr (WIDE && WHOLE && TJ == 4) {
+            if (ctype != kTF32) {
+                // Two lanes side by side have a row each: they give each other
+                // half of them, so that a store has all 128 bytes of a row.
+                v4i half[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    v4f v[2];
+#pragma unroll
+                    for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            if constexpr (TYPE == kTI8)
+                                v[j][k] = scaled(acc[i][2 * h + j][k], sa, sb[2 * h + j][k]);
+                            else if constexpr (TYPE == kTF16)
+                                v[j][k] = acc[i][2 * h + j][k] * factor;
+                            else
+                                v[j][k] = acc[i][2 * h + j][k];
+                        }
+                    }
+                    half[h] = pack8(v[0], v[1], ctype);
+                }
+                const bool odd = l16 & 1;
+                v4i mine, theirs;
+#pragma unroll
+                for (int w = 0; w < 4; ++w) {
+                    const int give = odd ? half[0][w] : half[1][w];
+                    const int got = __builtin_amdgcn_mov_dpp(give, 0xb1, 0xf, 0xf, true);
+                    mine[w] = odd ? got : half[0][w];
+                    theirs[w] = odd ? half[1][w] : got;
+                }
+                const int64_t step = (AT ? 1 : TM) * ldc;
+                unsigned short* at = (unsigned short*)c + (odd ? m * ldc - step : m * ldc) + n0 +
+                                     wn * kRowsB + (odd ? 32 : 0) + q * 8;
+                put16(at, mine);
+                put16(at + step, theirs);
+                continue;
+            }
+        }
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
             const int nc = column_at(WIDE ? j & ~1 : j);
@@ -194,11 +233,9 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
             const int64_t at = m * ldc + n0 + nc;
             v4f v, u;
             if constexpr (TYPE == kTI8) {
-                // (the scales one after the other: their product alone may
-                // leave the range that the result is in)
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    v[k] = (float)acc[i][j][k] * sa * sb[j][k];
+                    v[k] = scaled(acc[i][j][k], sa, sb[j][k]);
             } else {
                 v = acc[i][j];
             }

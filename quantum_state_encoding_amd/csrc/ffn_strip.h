@@ -199,7 +199,7 @@ __device__ __forceinline__ void strip_body(const ProductArgs& p, int64_t strip)
             continue;
         float v = (float)s[0];
         if constexpr (TYPE == kTI8)
-            v = v * p.sa[mm] * p.sb0[n];
+            v = scaled(s[0], p.sa[mm], p.sb0[n]);
         if constexpr (EP == kEpGate) {
             float d;
             if constexpr (TYPE == kTE4m3Exact)
