@@ -18,6 +18,7 @@ struct Group {
     int e;
     int first, rows;
     int tile;
+    int half;        // 0 all of it, 1 its first rows, 2 the others
 };
 
 // Rows of group e (e == experts: of the rows behind the last one).
@@ -33,7 +34,10 @@ __device__ __forceinline__ int rows_of(const GroupArgs& g, int e, int& first)
 // The tile of workgroup w among all groups' tiles of bm rows and tiles_n
 // columns: 64 groups at a time, one on each lane, whose tiles are summed across
 // the wave (every wave finds the same).  Each XCD gets a contiguous run of them.
-template <int BM>
+// HALVES: where the last round of tiles would leave half of the CUs without one,
+// two workgroups (of one XCD) take half of each tile's rows.
+constexpr int kCus = 256;
+template <int BM, bool HALVES = false>
 __device__ __forceinline__ bool find_group(const GroupArgs& g, int w, int tiles_n, Group& at)
 {
     const int lane = threadIdx.x & 63;
@@ -56,6 +60,15 @@ __device__ __forceinline__ bool find_group(const GroupArgs& g, int w, int tiles_
     for (int base = 64; base < groups; base += 64) {
         int f, r, t;
         total += __builtin_amdgcn_readlane(sum(base, f, r, t), 63);
+    }
+    at.half = 0;
+    if constexpr (HALVES) {
+        const int last = total % kCus, whole = total - last;
+        if (last <= kCus / 2 && w >= whole) {
+            const int j = w - whole;
+            at.half = 1 + ((j >> 3) & 1);
+            w = whole + ((j >> 4) << 3) + (j & 7);
+        }
     }
     if (w >= total)
         return false;
@@ -92,6 +105,23 @@ __device__ __forceinline__ void enter(ProductArgs& p, const GroupArgs& g, const 
     }
 }
 
+// Tile t of a group's tiles_m x tiles_n, in columns of about 8 row tiles, evenly:
+// a few row tiles over a multiple of 8 by themselves would read all of the expert's
+// weights once more.
+__device__ __forceinline__ void group_tile_at(int t, int tiles_m, int tiles_n, int& tm, int& tn)
+{
+    const int columns = tiles_m > 10 ? (tiles_m + 5) >> 3 : 1;
+    const int rows = tiles_m / columns, more = tiles_m - rows * columns;
+    const int wide = more * (rows + 1);          // row tiles of the columns with one more
+    const bool late = t >= wide * tiles_n;
+    const int r = rows + (late ? 0 : 1);
+    t -= late ? wide * tiles_n : 0;
+    const int c = t / (r * tiles_n);
+    t -= c * r * tiles_n;
+    tm = (late ? wide : 0) + c * r + t % r;
+    tn = t / r;
+}
+
 // Zeros to rows x cols results at (m0, n0).
 __device__ __forceinline__ void zero_tile(void* c, int64_t ldc, int type, int64_t m0, int64_t n0,
                                           int rows, int cols)
@@ -118,19 +148,28 @@ template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int REG, boo
 __global__ __launch_bounds__(64 * WM * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void
 grouped_kernel(ProductArgs p, const GroupArgs g)
 {
+    constexpr bool kPipe = BM == 256 && !REG;
     Group at;
-    if (!find_group<BM>(g, (int)blockIdx.x, p.tiles_n, at))
+    if (!find_group<BM, kPipe>(g, (int)blockIdx.x, p.tiles_n, at))
         return;
     if (at.e == g.experts) {
-        if (blockIdx.y == 0)
+        if (blockIdx.y == 0 && at.half < 2)
             zero_rows<BM, BN>(p, at, p.tiles_n);
         return;
     }
-    enter<TYPE>(p, g, at);
     int tm, tn;
-    tile_at(at.tile, (at.rows + BM - 1) / BM, p.tiles_n, tm, tn);
+    group_tile_at(at.tile, (at.rows + BM - 1) / BM, p.tiles_n, tm, tn);
+    if (kPipe && at.half) {
+        const int skip = tm * BM + (at.half - 1) * (BM / 2);
+        if (skip >= at.rows)
+            return;
+        at.first += skip;
+        at.rows = at.rows - skip < BM / 2 ? at.rows - skip : BM / 2;
+        tm = 0;
+    }
+    enter<TYPE>(p, g, at);
     product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, false, BT,
-                 BM == 256 && !REG>(
+                 kPipe, true>(
         p, tm, tn, (int)blockIdx.y, EveryWorkgroup{});
 }
 
@@ -140,7 +179,7 @@ struct GroupPlace : EveryWorkgroup {
     Group at;
     __device__ __forceinline__ void place(const ProductArgs& p, int& tm, int& tn) const
     {
-        tile_at(at.tile, (at.rows + BM - 1) / BM, p.tiles_n, tm, tn);
+        group_tile_at(at.tile, (at.rows + BM - 1) / BM, p.tiles_n, tm, tn);
     }
 };
 template <int TYPE, int BM, int BN, int WM, int WN>
@@ -150,7 +189,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_join_kernel(ProductArgs 
     if (!find_group<BM>(g, (int)blockIdx.x, p.tiles_n, where.at) || where.at.e == g.experts)
         return;
     enter<TYPE>(p, g, where.at);
-    join_body<TYPE, BM, BN, WM, WN, kEpStore, false>(p, where);
+    join_body<TYPE, BM, BN, WM, WN, kEpStore, false, true>(p, where);
 }
 
 // Few rows to a group: strips of 16 rows of B, for MT * 16 rows of A.
@@ -166,7 +205,7 @@ __global__ __launch_bounds__(64 * W) void grouped_strip_kernel(ProductArgs p, co
         return;
     }
     int tm, tn;
-    tile_at(at.tile, (at.rows + BM - 1) / BM, p.tiles_n, tm, tn);
+    group_tile_at(at.tile, (at.rows + BM - 1) / BM, p.tiles_n, tm, tn);
     at.first += tm * BM;
     at.rows = at.rows - tm * BM < BM ? at.rows - tm * BM : BM;
     enter<TYPE>(p, g, at);
@@ -183,15 +222,27 @@ struct GradPlace : EveryWorkgroup {
         n = tn;
     }
 };
+// One expert's tiles after the other's, each expert's spread over the XCDs (their
+// times differ by the experts'), and of up to 64 experts those with the most rows
+// first, so that the last tiles are short.
 __device__ __forceinline__ int enter_grad(ProductArgs& p, const GroupArgs& g, GradPlace& where)
 {
     const int per = p.tiles_m * p.tiles_n;
-    const int t = place_of((int)blockIdx.x, per * g.experts);
-    const int e = t / per;
-    int first;
+    int e = (int)blockIdx.x / per, first;
+    const int t = place_of((int)blockIdx.x - e * per, per);
+    if (g.experts > 1 && g.experts <= 64) {
+        const int lane = threadIdx.x & 63;
+        const int n = lane < g.experts ? rows_of(g, lane, first) : -1;
+        int rank = 0;
+        for (int o = 0; o < g.experts; ++o) {
+            const int other = __builtin_amdgcn_readlane(n, o);
+            rank += other > n || (other == n && o < lane) ? 1 : 0;
+        }
+        e = __builtin_ctzll(__ballot(lane < g.experts && rank == e));
+    }
     const int rows = __builtin_amdgcn_readfirstlane(rows_of(g, e, first));
     first = __builtin_amdgcn_readfirstlane(first);
-    tile_at(t - e * per, p.tiles_m, p.tiles_n, where.tm, where.tn);
+    tile_at(t, p.tiles_m, p.tiles_n, where.tm, where.tn);
     p.a = (const char*)p.a + first * p.lda;
     p.b0 = (const char*)p.b0 + first * p.ldb0;
     p.c = (char*)p.c + e * g.stride_c * 2;
@@ -218,7 +269,7 @@ grouped_grad_kernel(ProductArgs p, const GroupArgs g)
             return;
     }
     product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, true, true,
-                 BM == 256 && !REG>(
+                 BM == 256 && !REG, true>(
         p, where.tm, where.tn, (int)blockIdx.y, where);
 }
 
@@ -233,7 +284,7 @@ __global__ __launch_bounds__(64 * WM * WN) void grouped_grad_join_kernel(Product
     const int steps = (int)((p.kbytes + kStep - 1) / kStep);
     const int share = (steps + p.splits - 1) / p.splits;
     p.splits = (steps + share - 1) / share;      // those that have steps
-    join_body<TYPE, BM, BN, WM, WN, kEpStore, true>(p, where);
+    join_body<TYPE, BM, BN, WM, WN, kEpStore, true, true>(p, where);
 }
 
 // Row tiles that m rows in up to `groups` groups may have.
@@ -280,7 +331,9 @@ hipError_t run_grouped(ProductArgs p, const GroupArgs& g, int splits, hipStream_
         return e;
     p.splits = splits;
     p.tiles_n = (int)((p.n + BN - 1) / BN);
-    const unsigned tiles = (unsigned)(most_tiles(p.m, groups_of(g), BM) * p.tiles_n);
+    unsigned tiles = (unsigned)(most_tiles(p.m, groups_of(g), BM) * p.tiles_n);
+    if (BM == 256 && !REG)
+        tiles += kCus / 2;               // (halves)
     hipLaunchKernelGGL(k, dim3(tiles, (unsigned)splits), dim3(64 * WM * WN * WK), kLds, stream, p, g);
     e = hipGetLastError();
     if (splits == 1 || e != hipSuccess)

@@ -10,6 +10,13 @@
 namespace qse {
 namespace {
 
+template <int BM, int BN, int WM, int WN, int WK, int NS>
+hipError_t run_int8(const ProductArgs& p, int splits, hipStream_t stream)
+{
+    return run<kTI8, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, kAligned, false, false, BM == 256,
+               true>(p, splits, stream);
+}
+
 // Microseconds a step of 128, as ffn_matmul.hip's table has them.
 hipError_t tiles_int8(const ProductArgs& p, size_t* query, hipStream_t stream)
 {
@@ -25,16 +32,15 @@ hipError_t tiles_int8(const ProductArgs& p, size_t* query, hipStream_t stream)
     }
     switch (c.tile) {
     case 0:
-        return run<kTI8, 256, 256, 2, 4, 1, 2, kEpStore, kNoScale, kAligned, false, false, true>(
-            p, 1, stream);
+        return run_int8<256, 256, 2, 4, 1, 2>(p, 1, stream);
     case 1:
-        return run<kTI8, 128, 128, 2, 2, 1, 2, kEpStore, kNoScale>(p, 1, stream);
+        return run_int8<128, 128, 2, 2, 1, 2>(p, 1, stream);
     case 2:
-        return run<kTI8, 128, 128, 2, 2, 2, 2, kEpStore, kNoScale>(p, 1, stream);
+        return run_int8<128, 128, 2, 2, 2, 2>(p, 1, stream);
     case 3:
-        return run<kTI8, 64, 64, 2, 2, 2, 2, kEpStore, kNoScale>(p, 1, stream);
+        return run_int8<64, 64, 2, 2, 2, 2>(p, 1, stream);
     }
-    return run<kTI8, 64, 64, 2, 2, 2, 4, kEpStore, kNoScale>(p, c.splits, stream);
+    return run_int8<64, 64, 2, 2, 2, 4>(p, c.splits, stream);
 }
 
 // Few rows of A.

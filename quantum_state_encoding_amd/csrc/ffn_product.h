@@ -123,10 +123,11 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
         return wm * (TM * 16) + (AT ? (i0 + i) * 16 + l16 : l16 * TM + i0 + i);
     };
     const auto column_at = [=](int j) __attribute__((always_inline)) {
-        return WIDE ? wn * kRowsB + (j >> 1) * 32 + q * 8 + (j & 1) * 4
+        return WIDE ? wn * kRowsB + ((j0 + j) >> 1) * 32 + q * 8 + ((j0 + j) & 1) * 4
                     : wn * kRowsB + (j0 + j) * 16 + q * 4;
     };
-    constexpr int kSide = WIDE ? 8 : 4;      // neighbours of a store
+    constexpr bool kPairs = WIDE && TJ > 1;
+    constexpr int kSide = kPairs ? 8 : 4;    // neighbours of a store
     const auto count_at = [=](int nc) __attribute__((always_inline)) {
         return WHOLE || nrows - nc > kSide ? kSide : nrows - nc;
     };
@@ -227,7 +228,7 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
         }
 #pragma unroll
         for (int j = 0; j < TJ; ++j) {
-            const int nc = column_at(WIDE ? j & ~1 : j);
+            const int nc = column_at(kPairs ? j & ~1 : j);
             if (!WHOLE && nc >= nrows)
                 continue;
             const int64_t at = m * ldc + n0 + nc;
@@ -268,7 +269,7 @@ __device__ __forceinline__ void finish_rows_as(const ProductArgs& p, const Sums<
             }
             if constexpr (EP == kEpGateGrad)
                 store4(c, at + p.part_c, u, ctype, count_at(nc));
-            if constexpr (!WIDE)
+            if constexpr (!kPairs)
                 store4(c, at, v, ctype, count_at(nc));
             else if (j & 1)
                 store8(c, at, before, v, ctype, count_at(nc));
@@ -326,7 +327,7 @@ struct EveryWorkgroup {
 // (asked for late, not to hold registers); part: its share of the contraction's
 // p.splits.
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG,
-          bool AT, bool BT, bool PIPE = false, class Where>
+          bool AT, bool BT, bool PIPE = false, bool WIDE = PIPE, class Where>
 __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int tn, int part,
                                              const Where& where)
 {
@@ -377,7 +378,8 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
     const int64_t kround = (p.kbytes + 15) & ~(int64_t)15;
     const int lr = lane >> 3, lc = slot(wave * 8 + (lane >> 3), lane & 7);
     const int ra0 = row_of(wave * 8 + lr, TM * 16);
-    constexpr bool kWide = PIPE && !kDual;
+    constexpr bool kWide = WIDE && !kDual;
+    static_assert(!kWide || kRowsB % 32 == 0, "pairs of blocks");
     const int rb0 = kWide ? wide_row(wave * 8 + lr) : wave * 8 + lr;
     constexpr int kCa = BM / 8, kCb = BN / 8;        // chunks in a row of k
     const int ka0 = wave * (64 / kCa) + lane / kCa, kb0 = wave * (64 / kCb) + lane / kCb;
@@ -651,6 +653,23 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
 #pragma unroll
         for (int i = 0; i < TM; ++i)
             a[i] = read_a(lds + buffer_of(first), 0, i);
+        // The next step's data have arrived, and all of this one's have been read.
+        const auto turn = [&](int kt) __attribute__((always_inline)) {
+            wait_vm<0>();
+            __syncthreads();
+            if (kt + 1 < nk && ragged(kt + 1)) {
+                cut(kt + 1, lds + buffer_of(kt + 1));
+                __syncthreads();
+            }
+            if (kt + 2 < nk)
+                stage(kt + 2);
+        };
+        if (wm * TM * 16 >= mrows) {
+            // a wave without rows: the others have the matrix units for themselves
+            for (int kt = first; kt < nk; ++kt)
+                turn(kt);
+            return;
+        }
         for (int kt = first; kt < nk; ++kt) {
             unsigned char* const cur = lds + buffer_of(kt);
             unsigned char* const next = lds + buffer_of(kt + 1);
@@ -670,14 +689,7 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
                 for (int j = 0; j < TN; ++j)
                     acc[i][j] = half_step<TYPE>(b[1][j], a[i], acc[i][j]);
                 if (i == kAt) {
-                    wait_vm<0>();
-                    __syncthreads();
-                    if (kt + 1 < nk && ragged(kt + 1)) {
-                        cut(kt + 1, next);
-                        __syncthreads();
-                    }
-                    if (kt + 2 < nk)
-                        stage(kt + 2);
+                    turn(kt);
 #pragma unroll
                     for (int e = 0; e < kAt; ++e)
                         a[e] = read_a(next, 0, e);
@@ -733,7 +745,8 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
         for (int j = 0; j < TN; ++j) {
             const int row = kDual && j >= TN / 2 ? BNO + (j - TN / 2) * 16 : j * 16;
             if constexpr (BT) {
-                read_t<BN>(b[j], buf + BM * kStep, wn * TN + j, lane);
+                b[j][0] = read_t_half<BN, kWide>(buf + BM * kStep, wn * TN + j, lane, 0);
+                b[j][1] = read_t_half<BN, kWide>(buf + BM * kStep, wn * TN + j, lane, 1);
             } else {
                 b[j][0] = *(const v4i*)(buf + bo + row * kStep);
                 b[j][1] = *(const v4i*)(buf + (bo ^ 64) + row * kStep);
@@ -842,7 +855,7 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
 }
 
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG,
-          bool AT, bool BT, bool PIPE = false>
+          bool AT, bool BT, bool PIPE = false, bool WIDE = PIPE>
 __global__ __launch_bounds__(64 * WM * WN * WK) __attribute__((amdgpu_waves_per_eu(2))) void
 product_kernel(const ProductArgs p)
 {
@@ -852,7 +865,7 @@ product_kernel(const ProductArgs p)
     }
     int tm, tn;
     tile_of((int)blockIdx.x, p.tiles_m, p.tiles_n, tm, tn);
-    product_body<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT, PIPE>(
+    product_body<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT, PIPE, WIDE>(
         p, tm, tn, (int)blockIdx.y, EveryWorkgroup{});
 }
 
@@ -861,7 +874,7 @@ product_kernel(const ProductArgs p)
 // still spread over the CUs, and eight shares' loads in flight (f16 m 862 n
 // 15195 k 67, gradients: the join of 7 tiles in 16 shares takes 4.9 us, 7.3
 // with 16 rows of A and all of B to a workgroup).
-template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, class Where>
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, bool WIDE, class Where>
 __device__ __forceinline__ void join_body(const ProductArgs& p, const Where& where)
 {
     constexpr int W = WM * WN, TM = BM / WM / 16, TN = BN / WN / 16;
@@ -892,23 +905,23 @@ __device__ __forceinline__ void join_body(const ProductArgs& p, const Where& whe
     }
     int tm, tn;
     where.place(p, tm, tn);
-    finish_rows<TYPE, BM, BN, WM, WN, EP, AT>(p, acc, i, j, tm, tn,
-                                              __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6),
-                                              threadIdx.x & 63);
+    finish_rows<TYPE, BM, BN, WM, WN, EP, AT, WIDE>(
+        p, acc, i, j, tm, tn, __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6),
+        threadIdx.x & 63);
 }
 
-template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT>
+template <int TYPE, int BM, int BN, int WM, int WN, int EP, bool AT, bool WIDE = false>
 __global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
 {
     if constexpr (TYPE == kTF16 && EP == kEpGateGrad) {
         if (p.again && range_exponent(p.range) == 0)
             return;
     }
-    join_body<TYPE, BM, BN, WM, WN, EP, AT>(p, EveryWorkgroup{});
+    join_body<TYPE, BM, BN, WM, WN, EP, AT, WIDE>(p, EveryWorkgroup{});
 }
 
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG = kAligned,
-          bool AT = false, bool BT = false, bool PIPE = false>
+          bool AT = false, bool BT = false, bool PIPE = false, bool WIDE = PIPE>
 hipError_t run(ProductArgs p, int splits, hipStream_t stream)
 {
     p.splits = splits;
@@ -917,7 +930,7 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
     static_assert(kLds <= 160 * 1024 && (size_t)(WK - 1) * BM * BN * 4 <= kLds, "LDS of a CU");
     p.tiles_m = (int)((p.m + BM - 1) / BM);
     p.tiles_n = (int)((p.n + BNO - 1) / BNO);
-    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT, PIPE>;
+    auto* k = &product_kernel<TYPE, BM, BN, WM, WN, WK, NS, EP, SM, REG, AT, BT, PIPE, WIDE>;
     if (kLds > 65536) {
         // once for each device
         static std::atomic<uint64_t> done{0};
@@ -942,7 +955,7 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
         return e;
     if constexpr (BM <= 128 && BN <= 128) {      // (larger tiles are never split)
         const dim3 grid(tiles, BM / WM / 16, BNO / WN / 16);
-        hipLaunchKernelGGL((join_kernel<TYPE, BM, BN, WM, WN, EP, AT>), grid, dim3(64 * WM * WN), 0,
+        hipLaunchKernelGGL((join_kernel<TYPE, BM, BN, WM, WN, EP, AT, WIDE>), grid, dim3(64 * WM * WN), 0,
                            stream, p);
     }
     return hipGetLastError();
