@@ -122,18 +122,21 @@ __device__ __forceinline__ void group_tile_at(int t, int tiles_m, int tiles_n, i
     tn = t / r;
 }
 
-// Zeros to rows x cols results at (m0, n0).
+// Zeros to rows x cols results at (m0, n0), 16 bytes a lane.
 __device__ __forceinline__ void zero_tile(void* c, int64_t ldc, int type, int64_t m0, int64_t n0,
                                           int rows, int cols)
 {
-    for (int r = 0; r < rows; ++r)
-        for (int n = (int)threadIdx.x; n < cols; n += (int)blockDim.x) {
-            const int64_t at = (m0 + r) * ldc + n0 + n;
-            if (type == kTF32)
-                ((float*)c)[at] = 0.0f;
-            else
-                ((unsigned short*)c)[at] = 0;
-        }
+    const int size = type == kTF32 ? 4 : 2, each = 16 / size;
+    const int chunks = (cols + each - 1) / each;
+    for (int i = (int)threadIdx.x; i < rows * chunks; i += (int)blockDim.x) {
+        const int r = i / chunks, n = (i - r * chunks) * each;
+        char* at = (char*)c + ((m0 + r) * ldc + n0 + n) * size;
+        if (cols - n >= each)
+            put16(at, v4i{0, 0, 0, 0});
+        else
+            for (int b = 0; b < (cols - n) * size; b += 2)
+                *(unsigned short*)(at + b) = 0;
+    }
 }
 template <int BM, int BN>
 __device__ __forceinline__ void zero_rows(const ProductArgs& p, const Group& at, int tiles_n)
@@ -294,7 +297,9 @@ int64_t most_tiles(int64_t m, int64_t groups, int64_t bm)
     return (m + r * (bm - 1)) / bm;
 }
 
-int64_t groups_of(const GroupArgs& g) { return g.experts + (g.zero_rest ? 1 : 0); }
+// (the rows of no expert count whether they are written or not, so that the choice
+// and its scratch do not go by it)
+int64_t groups_of(const GroupArgs& g) { return g.experts + 1; }
 
 template <class K>
 hipError_t allow_lds(K* k, size_t bytes, std::atomic<uint64_t>& done)
@@ -369,41 +374,126 @@ hipError_t run_grad(ProductArgs p, const GroupArgs& g, int splits, hipStream_t s
     return hipGetLastError();
 }
 
-// Which tile, as ffn_matmul.hip chooses: rounds of workgroups times the time of
-// a step.  How the rows are spread is not known: a group is taken to have the
-// average number, and half a tile of rows more than it fills.
-template <int N>
-Choice cheapest_grouped(const Tile (&tiles)[N], const ProductArgs& p, const GroupArgs& g)
+// Which tile.  A round of workgroups takes its steps' time and that of its first
+// loads and its stores, and all rounds at least the time of the operands' and
+// results' bytes; 0.3 of the shorter of the two does not overlap the longer.
+// Microseconds a step of 128 bytes, and a round beside them, measured:
+//                              slots   16 bits   any address   8 bits
+//   256 x 256                    256   1.45  9     1.9  11    1.45  9
+//   128 x 128, two on a CU       512   1.06  6     1.2   7    1.0   6
+//   128 x 128, deeper            256    .62  5       -         .60  5
+//   64 x 128 (8 bits: 64 x 64)   256    .42  4      .85  6     .40  4, two on a CU
+//   64 x 128, three on a CU      768                1.4   6
+//   8 bits, 64 x 64, deeper      256                           .26  3
+// and the bytes at 6.5 TB/s, at any address 2.5, 2.7 and 3.8.
+// How the rows are spread is not known: a group is taken to have the average
+// number, and half a tile of rows more than it fills.  Over 53 sizes (1 to 128
+// experts, 0.5 to 2048 rows for each) the choice takes 1.4 % longer than the best
+// tile in the mean.  Where most of a round's slots are empty the workgroups of a
+// tile may share its steps, for a second launch and their sums' bytes.
+struct GroupTile {
+    int bm, bn, slots;
+    float step, round;
+    int area;                // of the sums, 0: not split
+    float rate = 6.5e6f;     // bytes a microsecond
+};
+constexpr double kSumBytes = 4.5e6;
+constexpr double kNever = 1e30;
+
+struct GroupCosts {
+    int64_t steps;
+    double bytes;
+    bool may_split;
+};
+// count(tile, most): the tiles to expect, and those of the grid.
+template <int N, class Count>
+Choice cheapest_grouped(const GroupTile (&tiles)[N], const GroupCosts& w, const Count& count,
+                        double& least)
 {
-    const int64_t steps = (p.kbytes + kStep - 1) / kStep;
-    const double groups = (double)(g.experts < p.m ? g.experts : p.m), avg = p.m / groups;
     Choice best{0, 1, 0};
-    double least = 0;
+    least = 2 * kNever;
     for (int i = 0; i < N; ++i) {
-        const Tile& t = tiles[i];
-        const int64_t tn = (p.n + t.bn - 1) / t.bn;
-        const int64_t most = most_tiles(p.m, groups_of(g), t.bm) * tn;
-        const double each = g.experts == 1 || avg <= t.bm / 2 ? (double)((int64_t)(avg / t.bm) + 1)
-                                                              : avg / t.bm + 0.5;
-        const double rounds = groups * each * tn / t.slots;
-        double cost = most >= kFfnMaxTiles ? 1e300 : (rounds < 1 ? 1 : rounds) * t.step * steps;
+        const GroupTile& t = tiles[i];
+        int64_t most = 0;
+        const double expect = count(t, most);
+        const auto both = [&](double compute) {
+            const double memory = w.bytes / t.rate;
+            return compute > memory ? compute + 0.3 * memory : memory + 0.3 * compute;
+        };
+        const double rounds = (double)((int64_t)((expect - 1e-6) / t.slots) + 1);
+        double cost = most >= kFfnMaxTiles ? kNever : both(rounds * (w.steps * t.step + t.round));
         int splits = 1;
-        if (t.area && p.may_split && most * 2 <= t.slots) {
+        if (t.area && w.may_split && most * 2 <= t.slots) {
             int64_t s = t.slots / most < 32 ? t.slots / most : 32;
-            s = s < steps / 4 ? s : steps / 4;
-            s = s > 1 ? (steps + (steps + s - 1) / s - 1) / ((steps + s - 1) / s) : 1;
-            const double shared = (double)((steps + s - 1) / s) * t.step + 5.0;
+            s = s < w.steps / 4 ? s : w.steps / 4;
+            // every share has steps, the last one fewer
+            s = s > 1 ? (w.steps + (w.steps + s - 1) / s - 1) / ((w.steps + s - 1) / s) : 1;
+            const double sums = 2.0 * s * most * t.area * 4;
+            const double shared =
+                both((double)((w.steps + s - 1) / s) * t.step + t.round) + 4.0 + sums / kSumBytes;
             if (s > 1 && shared < cost) {
                 cost = shared;
                 splits = (int)s;
             }
         }
-        if (i == 0 || cost < least) {
+        if (cost < least) {
             least = cost;
             best = Choice{i, splits, splits > 1 ? (size_t)splits * most * t.area * 4 : 0};
         }
     }
     return best;
+}
+
+double groups_with_rows(const ProductArgs& p, const GroupArgs& g)
+{
+    return (double)(g.experts < p.m ? g.experts : p.m);
+}
+
+// Row tiles of bm that a group is expected to have.
+double tiles_of_group(const ProductArgs& p, const GroupArgs& g, int bm)
+{
+    const double avg = p.m / groups_with_rows(p, g);
+    return g.experts == 1 || avg <= bm / 2 ? (double)((int64_t)(avg / bm) + 1) : avg / bm + 0.5;
+}
+
+template <int N>
+Choice choose(const GroupTile (&tiles)[N], const ProductArgs& p, const GroupArgs& g, double& least)
+{
+    const double groups = groups_with_rows(p, g);
+    const double bytes = (groups * p.n + p.m) * p.kbytes + 2.0 * p.m * p.n;
+    const GroupCosts w{(p.kbytes + kStep - 1) / kStep, bytes, p.may_split != 0};
+    return cheapest_grouped(
+        tiles, w,
+        [&](const GroupTile& t, int64_t& most) {
+            const int64_t tn = (p.n + t.bn - 1) / t.bn;
+            most = most_tiles(p.m, groups_of(g), t.bm) * tn;
+            return groups * tiles_of_group(p, g, t.bm) * tn;
+        },
+        least);
+}
+
+// Strips: the weights' bytes for every 16 rows of a group, and some time to start.
+// Groups of a row or two take them (about 26 experts of 2048 x 4096, bf16: 70 us and
+// 75 with 64 x 128 tiles, in two rounds; 18 experts of 496 x 3712: 16.8 and 23.9),
+// others are faster in tiles (64 experts of 2048 x 4096, 4 rows each in the mean,
+// unevenly: 212 us and 169).
+constexpr double kStrip16 = 5.7e6, kStripOdd = 3.0e6, kStrip8 = 4.6e6;   // bytes a microsecond
+double strips_cost(const ProductArgs& p, const GroupArgs& g, double rate)
+{
+    if (most_tiles(p.m, groups_of(g), 16) * ((p.n + 15) / 16) >= kFfnMaxTiles)
+        return kNever;
+    const double groups = groups_with_rows(p, g), avg = p.m / groups;
+    return 4.0 + groups * (avg > 1 ? 1 + avg / 16 : 1) * p.n * p.kbytes / rate;
+}
+
+template <int TYPE, int MT, int W, int U, bool ODD>
+hipError_t run_strips(ProductArgs p, const GroupArgs& g, hipStream_t stream)
+{
+    p.tiles_n = (int)((p.n + 15) / 16);
+    const unsigned count = (unsigned)(most_tiles(p.m, groups_of(g), MT * 16) * p.tiles_n);
+    hipLaunchKernelGGL((grouped_strip_kernel<TYPE, MT, W, U, ODD>), dim3(count), dim3(64 * W),
+                       W * MT * 4 * 64 * 4, stream, p, g);
+    return hipGetLastError();
 }
 
 bool any_address(const ProductArgs& p, const GroupArgs& g, uintptr_t mask)
@@ -415,22 +505,35 @@ bool any_address(const ProductArgs& p, const GroupArgs& g, uintptr_t mask)
 template <int TYPE, bool BT>
 hipError_t grouped16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipStream_t stream)
 {
-    constexpr Tile any[] = {{256, 256, 256, 1.9f, 0}, {128, 128, 512, 1.2f, 128 * 128}};
-    constexpr Tile tiles[] = {{256, 256, 256, 1.6f, 0},
-                              {128, 128, 512, 1.06f, 0},
-                              {128, 128, 256, .62f, 128 * 128},
-                              {64, 128, 256, .42f, 64 * 128}};
-    const Choice ca = cheapest_grouped(any, p, g), c = cheapest_grouped(tiles, p, g);
+    constexpr GroupTile any[] = {{256, 256, 256, 1.9f, 11.f, 0, 2.5e6f},
+                                 {128, 128, 512, 1.2f, 7.f, 0, 2.7e6f},
+                                 {64, 128, 768, 1.4f, 6.f, 64 * 128, 3.8e6f},
+                                 {64, 128, 256, .85f, 6.f, 0, 3.8e6f}};
+    constexpr GroupTile tiles[] = {{256, 256, 256, 1.45f, 9.f, 0},
+                                   {128, 128, 512, 1.06f, 6.f, 0},
+                                   {128, 128, 256, .62f, 5.f, 128 * 128},
+                                   {64, 128, 256, .42f, 4.f, 64 * 128}};
+    double cost_any, cost;
+    const Choice ca = choose(any, p, g, cost_any), c = choose(tiles, p, g, cost);
     if (query) {
         *query = ca.bytes > c.bytes ? ca.bytes : c.bytes;
         return hipSuccess;
     }
-    if (any_address(p, g, 15)) {
+    const bool anywhere = any_address(p, g, 15);
+    if constexpr (!BT) {
+        const bool odd = any_address(p, g, 3);
+        if (strips_cost(p, g, odd ? kStripOdd : kStrip16) < (anywhere ? cost_any : cost))
+            return odd ? run_strips<TYPE, 1, 8, 4, true>(p, g, stream)
+                       : run_strips<TYPE, 1, 8, 4, false>(p, g, stream);
+    }
+    if (anywhere) {
         if (p.kbytes < 16 || (BT && p.n < 8))
             return run_grouped<TYPE, 128, 128, 2, 2, 1, 2, BT, kShortRows>(p, g, 1, stream);
         if (ca.tile == 0)
             return run_grouped<TYPE, 256, 256, 2, 4, 1, 2, BT, kAnyAddress>(p, g, 1, stream);
-        return run_grouped<TYPE, 128, 128, 2, 2, 1, 2, BT, kAnyAddress>(p, g, ca.splits, stream);
+        if (ca.tile == 1)
+            return run_grouped<TYPE, 128, 128, 2, 2, 1, 2, BT, kAnyAddress>(p, g, 1, stream);
+        return run_grouped<TYPE, 64, 128, 1, 4, 1, 2, BT, kAnyAddress>(p, g, ca.splits, stream);
     }
     switch (c.tile) {
     case 0:
@@ -445,16 +548,20 @@ hipError_t grouped16(const ProductArgs& p, const GroupArgs& g, size_t* query, hi
 
 hipError_t grouped8(const ProductArgs& p, const GroupArgs& g, size_t* query, hipStream_t stream)
 {
-    constexpr Tile tiles[] = {{256, 256, 256, 1.5f, 0},
-                              {128, 128, 512, 1.0f, 0},
-                              {128, 128, 256, .60f, 0},
-                              {64, 64, 512, .40f, 0},
-                              {64, 64, 256, .26f, 64 * 64}};
-    const Choice c = cheapest_grouped(tiles, p, g);
+    constexpr GroupTile tiles[] = {{256, 256, 256, 1.45f, 9.f, 0},
+                                   {128, 128, 512, 1.0f, 6.f, 0},
+                                   {128, 128, 256, .60f, 5.f, 0},
+                                   {64, 64, 512, .40f, 4.f, 0},
+                                   {64, 64, 256, .26f, 3.f, 64 * 64}};
+    double cost;
+    const Choice c = choose(tiles, p, g, cost);
+    const bool strips = strips_cost(p, g, kStrip8) < cost;
     if (query) {
-        *query = c.bytes;
+        *query = strips ? 0 : c.bytes;
         return hipSuccess;
     }
+    if (strips)
+        return run_strips<kTI8, 1, 8, 4, false>(p, g, stream);
     switch (c.tile) {
     case 0:
         return run_grouped<kTI8, 256, 256, 2, 4, 1, 2, false>(p, g, 1, stream);
@@ -468,46 +575,28 @@ hipError_t grouped8(const ProductArgs& p, const GroupArgs& g, size_t* query, hip
     return run_grouped<kTI8, 64, 64, 2, 2, 2, 4, false>(p, g, c.splits, stream);
 }
 
+// Gradients of weights: an expert's tiles have its own rows as their steps; the
+// average's count, twice as many where they may be shared (the expert with the most
+// rows ends last).
 template <int TYPE>
 hipError_t grad16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipStream_t stream)
 {
-    // (an expert's tiles take its own rows: the average's steps)
-    ProductArgs q = p;
-    q.kbytes = (p.kbytes + g.experts - 1) / g.experts;
-    constexpr Tile any[] = {{256, 256, 256, 1.9f, 0}, {128, 128, 512, 1.2f, 128 * 128}};
-    constexpr Tile tiles[] = {{256, 256, 256, 1.6f, 0},
-                              {128, 128, 512, 1.06f, 0},
-                              {128, 128, 256, .62f, 128 * 128}};
-    const auto pick = [&](const auto& list) {
-        const int64_t steps = (q.kbytes + kStep - 1) / kStep;
-        Choice best{0, 1, 0};
-        double least = 0;
-        int i = 0;
-        for (const Tile& t : list) {
-            const int64_t count =
-                ((p.m + t.bm - 1) / t.bm) * ((p.n + t.bn - 1) / t.bn) * g.experts;
-            double cost = count >= kFfnMaxTiles
-                              ? 1e300
-                              : (double)((count + t.slots - 1) / t.slots) * t.step * steps;
-            int splits = 1;
-            if (t.area && p.may_split && count * 2 <= t.slots) {
-                int64_t s = t.slots / count < 32 ? t.slots / count : 32;
-                s = s < steps / 4 ? s : steps / 4;
-                const double shared = s > 1 ? (double)((steps + s - 1) / s) * t.step + 5.0 : 1e300;
-                if (shared < cost) {
-                    cost = shared;
-                    splits = (int)s;
-                }
-            }
-            if (i == 0 || cost < least) {
-                least = cost;
-                best = Choice{i, splits, splits > 1 ? (size_t)splits * count * t.area * 4 : 0};
-            }
-            ++i;
-        }
-        return best;
+    constexpr GroupTile any[] = {{256, 256, 256, 1.9f, 11.f, 0},
+                                 {128, 128, 512, 1.2f, 7.f, 128 * 128}};
+    constexpr GroupTile tiles[] = {{256, 256, 256, 1.6f, 9.f, 0},
+                                   {128, 128, 512, 1.06f, 6.f, 0},
+                                   {128, 128, 256, .62f, 5.f, 128 * 128}};
+    const auto count = [&](const GroupTile& t, int64_t& most) {
+        most = ((p.m + t.bm - 1) / t.bm) * ((p.n + t.bn - 1) / t.bn) * g.experts;
+        return (double)most;
     };
-    const Choice ca = pick(any), c = pick(tiles);
+    const int64_t rows = (p.kbytes + 2 * g.experts - 1) / (2 * g.experts);
+    const double bytes = 2.0 * p.m * p.n * g.experts + (double)p.kbytes * (p.m + p.n);
+    const int64_t few = (rows * 2 + kStep - 1) / kStep;
+    const GroupCosts w{g.experts > 1 && p.may_split ? 2 * few : few, bytes,
+                       p.may_split != 0};
+    double cost;
+    const Choice ca = cheapest_grouped(any, w, count, cost), c = cheapest_grouped(tiles, w, count, cost);
     if (query) {
         *query = ca.bytes > c.bytes ? ca.bytes : c.bytes;
         return hipSuccess;
@@ -528,57 +617,27 @@ hipError_t grad16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipSt
     return run_grad<TYPE, 128, 128, 2, 2, 1, 4>(p, g, c.splits, stream);
 }
 
-// Few rows to a group: strips.
-bool strips(const ProductArgs& p, const GroupArgs& g, bool bt)
-{
-    return !bt && p.m <= 16 * (int64_t)g.experts &&
-           most_tiles(p.m, groups_of(g), 16) * ((p.n + 15) / 16) < kFfnMaxTiles;
-}
-
-template <int TYPE, int MT, int W, int U, bool ODD>
-hipError_t run_strips(ProductArgs p, const GroupArgs& g, hipStream_t stream)
-{
-    p.tiles_n = (int)((p.n + 15) / 16);
-    const unsigned count = (unsigned)(most_tiles(p.m, groups_of(g), MT * 16) * p.tiles_n);
-    hipLaunchKernelGGL((grouped_strip_kernel<TYPE, MT, W, U, ODD>), dim3(count), dim3(64 * W),
-                       W * MT * 4 * 64 * 4, stream, p, g);
-    return hipGetLastError();
-}
-
-template <int TYPE>
-hipError_t pick_strips(const ProductArgs& p, const GroupArgs& g, hipStream_t stream)
-{
-    if constexpr (TYPE != kTI8) {
-        if (any_address(p, g, 3))
-            return run_strips<TYPE, 1, 8, 4, true>(p, g, stream);
-    }
-    return run_strips<TYPE, 1, 8, 4, false>(p, g, stream);
-}
-
 }  // namespace
 
 hipError_t launch_grouped(const ProductArgs& p, const GroupArgs& g, int type, bool bt,
                           hipStream_t stream)
 {
-    const bool few = strips(p, g, bt);
     if (type == kTI8)
-        return few ? pick_strips<kTI8>(p, g, stream) : grouped8(p, g, nullptr, stream);
+        return grouped8(p, g, nullptr, stream);
     if (type == kTBf16)
-        return few  ? pick_strips<kTBf16>(p, g, stream)
-               : bt ? grouped16<kTBf16, true>(p, g, nullptr, stream)
-                    : grouped16<kTBf16, false>(p, g, nullptr, stream);
-    return few  ? pick_strips<kTF16>(p, g, stream)
-           : bt ? grouped16<kTF16, true>(p, g, nullptr, stream)
-                : grouped16<kTF16, false>(p, g, nullptr, stream);
+        return bt ? grouped16<kTBf16, true>(p, g, nullptr, stream)
+                  : grouped16<kTBf16, false>(p, g, nullptr, stream);
+    return bt ? grouped16<kTF16, true>(p, g, nullptr, stream)
+              : grouped16<kTF16, false>(p, g, nullptr, stream);
 }
 
 size_t grouped_workspace(ProductArgs p, const GroupArgs& g, int type, bool bt)
 {
     size_t bytes = 0;
     p.may_split = 1;
-    if (!strips(p, g, bt))
-        (void)(type == kTI8 ? grouped8(p, g, &bytes, nullptr)
-                            : grouped16<kTBf16, false>(p, g, &bytes, nullptr));
+    (void)(type == kTI8 ? grouped8(p, g, &bytes, nullptr)
+           : bt         ? grouped16<kTBf16, true>(p, g, &bytes, nullptr)
+                        : grouped16<kTBf16, false>(p, g, &bytes, nullptr));
     return bytes;
 }
 
