@@ -10,7 +10,8 @@
 // joined their maxima: one pass over memory, which bounds it.  Rows above 32768
 // elements (1024 lanes) are rotated twice, for the maximum and for the codes.
 // The rotations run in ffn_rotate.hip's layouts:
-//   b <= 5        32 neighbours of a lane, register stages
+//   b <= 4        twice 16 neighbours of a lane (rows of up to 2048 elements, and
+//                 b = 5: 32 neighbours), register stages
 //   b = 6 .. 10   H_32 (16-bit inputs: matrix cores), LDS, register stages of
 //                 the others
 //   b = 11 .. 14  three layouts
@@ -83,11 +84,24 @@ __device__ __forceinline__ void rotated(const void* x, int bits, float* lds, int
                                         const Place& place, float (&v)[32])
 {
     if constexpr (BITS <= 5) {
-        int64_t at;
-        const int64_t left = place(t * 32, at);
-        load32<TYPE>(x, at, left, v);
+        if constexpr (BITS < 5) {
 #pragma unroll
-        for (int b = 0; b < 5; ++b)
+            for (int h = 0; h < 2; ++h) {
+                int64_t at;
+                const int64_t left = place((t >> 6) * kWaveRow + h * 1024 + (t & 63) * 16, at);
+                float u[16];
+                load_elements<TYPE>(x, at, left > 16 ? 16 : (int)left, u);
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[16 * h + i] = u[i];
+            }
+        } else {
+            int64_t at;
+            const int64_t left = place(t * 32, at);
+            load32<TYPE>(x, at, left, v);
+        }
+#pragma unroll
+        for (int b = 0; b < BITS; ++b)
             if (b < bits) {
 #pragma unroll
                 for (int i = 0; i < 32; ++i)
@@ -170,18 +184,20 @@ __device__ __forceinline__ unsigned largest(const float (&v)[32])
     return __float_as_uint(f) & 0x7fffffffu;
 }
 
-// Codes of a lane's 32 elements, the first `left` of which exist.
+// Codes of a lane's 32 elements, the row's last one `left` from the first; the second
+// 16 are NEXT from it.
+template <int NEXT>
 __device__ __forceinline__ void write32(int8_t* q, int64_t left, const float (&v)[32], float s,
                                         float inv, bool finite)
 {
 #pragma unroll
     for (int h = 0; h < 2; ++h) {
-        if (left <= 16 * h)
+        if (left <= NEXT * h)
             break;
         v4i c = encode8(v + 16 * h, s, inv);
         if (!finite)
             c = v4i{0, 0, 0, 0};
-        const int64_t l = left - 16 * h;
+        const int64_t l = left - NEXT * h;
         if (l < 16) {                    // the row's padding is zeros
 #pragma unroll
             for (int w = 0; w < 4; ++w) {
@@ -189,7 +205,7 @@ __device__ __forceinline__ void write32(int8_t* q, int64_t left, const float (&v
                 c[w] = b >= 4 ? c[w] : b <= 0 ? 0 : c[w] & ((1 << (8 * b)) - 1);
             }
         }
-        *(v4i*)(q + 16 * h) = c;
+        *(v4i*)(q + NEXT * h) = c;
     }
 }
 
@@ -261,7 +277,11 @@ __global__ __launch_bounds__(ONE ? 1024 : 256) void quantize8_kernel(const Quant
     const bool finite = s == s;
     const float sv = exact ? s / norm : s;
     const float inv = 1.0f / sv;
-    const int col = ONE ? t * 32 : (t & ((1 << shift) - 1)) * 32;
+    constexpr bool kTwo = ONE && BITS < 5;      // twice 16 neighbours
+    constexpr int kNext = kTwo ? 1024 : 16;
+    const int col = kTwo  ? wave * kWaveRow + lane * 16
+                    : ONE ? t * 32
+                          : (t & ((1 << shift) - 1)) * 32;
     if (row < p.m && col == 0)
         p.s[row] = s;
     if constexpr (TWICE) {
@@ -269,10 +289,10 @@ __global__ __launch_bounds__(ONE ? 1024 : 256) void quantize8_kernel(const Quant
             __syncthreads();
             rotated<TYPE, BITS>(p.x, p.bits, lds, t, place(begin), v);
             normalise();
-            write32(p.q + row * p.ldq + begin + col, p.k - begin - col, v, sv, inv, finite);
+            write32<kNext>(p.q + row * p.ldq + begin + col, p.k - begin - col, v, sv, inv, finite);
         }
     } else if (row < p.m) {
-        write32(p.q + row * p.ldq + col, p.k - col, v, sv, inv, finite);
+        write32<kNext>(p.q + row * p.ldq + col, p.k - col, v, sv, inv, finite);
     }
 }
 
@@ -343,7 +363,8 @@ hipError_t by_bits(const Quantize8Args& p, hipStream_t stream)
     case 14:
         return run<TYPE, 14>(p, norm, stream);
     default:
-        return run<TYPE, 5>(p, norm, stream);
+        return p.bits < 5 && p.k > kWaveRow ? run<TYPE, 4>(p, norm, stream)
+                                            : run<TYPE, 5>(p, norm, stream);
     }
 }
 
