@@ -382,14 +382,14 @@ hipError_t run_grad(ProductArgs p, const GroupArgs& g, int splits, hipStream_t s
 //   256 x 256                    256   1.45  9     1.9  11    1.45  9
 //   128 x 128, two on a CU       512   1.06  6     1.2   7    1.0   6
 //   128 x 128, deeper            256    .62  5       -         .60  5
-//   64 x 128 (8 bits: 64 x 64)   256    .42  4      .85  6     .40  4, two on a CU
+//   64 x 128                     256    .42  4      .85  6     .42  4
 //   64 x 128, three on a CU      768                1.4   6
 //   8 bits, 64 x 64, deeper      256                           .26  3
 // and the bytes at 6.5 TB/s, at any address 2.5, 2.7 and 3.8.
 // How the rows are spread is not known: a group is taken to have the average
-// number, and half a tile of rows more than it fills.  Over 53 sizes (1 to 128
-// experts, 0.5 to 2048 rows for each) the choice takes 1.4 % longer than the best
-// tile in the mean.  Where most of a round's slots are empty the workgroups of a
+// number, and half a tile of rows more than it fills.  Over 53 sizes (4 to 64
+// experts, 0.5 to 2048 rows for each, unevenly) the choice takes 1.5 % longer than
+// the best tile in the mean, at most 16 %.  Where most of a round's slots are empty the workgroups of a
 // tile may share its steps, for a second launch and their sums' bytes.
 struct GroupTile {
     int bm, bn, slots;
@@ -404,6 +404,7 @@ struct GroupCosts {
     int64_t steps;
     double bytes;
     bool may_split;
+    bool known;              // the number of tiles is
 };
 // count(tile, most): the tiles to expect, and those of the grid.
 template <int N, class Count>
@@ -420,7 +421,11 @@ Choice cheapest_grouped(const GroupTile (&tiles)[N], const GroupCosts& w, const 
             const double memory = w.bytes / t.rate;
             return compute > memory ? compute + 0.3 * memory : memory + 0.3 * compute;
         };
-        const double rounds = (double)((int64_t)((expect - 1e-6) / t.slots) + 1);
+        // (a number that is not known ends anywhere in its last round)
+        const double full = expect / t.slots;
+        const double rounds = w.known      ? (double)((int64_t)(full - 1e-9) + 1)
+                              : full > 0.6 ? full + 0.4
+                                           : 1.0;
         double cost = most >= kFfnMaxTiles ? kNever : both(rounds * (w.steps * t.step + t.round));
         int splits = 1;
         if (t.area && w.may_split && most * 2 <= t.slots) {
@@ -453,7 +458,9 @@ double groups_with_rows(const ProductArgs& p, const GroupArgs& g)
 double tiles_of_group(const ProductArgs& p, const GroupArgs& g, int bm)
 {
     const double avg = p.m / groups_with_rows(p, g);
-    return g.experts == 1 || avg <= bm / 2 ? (double)((int64_t)(avg / bm) + 1) : avg / bm + 0.5;
+    if (g.experts == 1)
+        return (double)((p.m + bm - 1) / bm);
+    return avg > bm / 2 ? avg / bm + 0.5 : 1.0;
 }
 
 template <int N>
@@ -461,7 +468,7 @@ Choice choose(const GroupTile (&tiles)[N], const ProductArgs& p, const GroupArgs
 {
     const double groups = groups_with_rows(p, g);
     const double bytes = (groups * p.n + p.m) * p.kbytes + 2.0 * p.m * p.n;
-    const GroupCosts w{(p.kbytes + kStep - 1) / kStep, bytes, p.may_split != 0};
+    const GroupCosts w{(p.kbytes + kStep - 1) / kStep, bytes, p.may_split != 0, false};
     return cheapest_grouped(
         tiles, w,
         [&](const GroupTile& t, int64_t& most) {
@@ -551,7 +558,7 @@ hipError_t grouped8(const ProductArgs& p, const GroupArgs& g, size_t* query, hip
     constexpr GroupTile tiles[] = {{256, 256, 256, 1.45f, 9.f, 0},
                                    {128, 128, 512, 1.0f, 6.f, 0},
                                    {128, 128, 256, .60f, 5.f, 0},
-                                   {64, 64, 512, .40f, 4.f, 0},
+                                   {64, 128, 256, .42f, 4.f, 0},
                                    {64, 64, 256, .26f, 3.f, 64 * 64}};
     double cost;
     const Choice c = choose(tiles, p, g, cost);
@@ -568,9 +575,9 @@ hipError_t grouped8(const ProductArgs& p, const GroupArgs& g, size_t* query, hip
     case 1:
         return run_grouped<kTI8, 128, 128, 2, 2, 1, 2, false>(p, g, 1, stream);
     case 2:
-        return run_grouped<kTI8, 128, 128, 2, 2, 2, 2, false>(p, g, 1, stream);
+        return run_grouped<kTI8, 128, 128, 2, 2, 1, 4, false>(p, g, 1, stream);
     case 3:
-        return run_grouped<kTI8, 64, 64, 2, 2, 2, 2, false>(p, g, 1, stream);
+        return run_grouped<kTI8, 64, 128, 1, 4, 1, 4, false>(p, g, 1, stream);
     }
     return run_grouped<kTI8, 64, 64, 2, 2, 2, 4, false>(p, g, c.splits, stream);
 }
@@ -594,7 +601,7 @@ hipError_t grad16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipSt
     const double bytes = 2.0 * p.m * p.n * g.experts + (double)p.kbytes * (p.m + p.n);
     const int64_t few = (rows * 2 + kStep - 1) / kStep;
     const GroupCosts w{g.experts > 1 && p.may_split ? 2 * few : few, bytes,
-                       p.may_split != 0};
+                       p.may_split != 0, true};
     double cost;
     const Choice ca = cheapest_grouped(any, w, count, cost), c = cheapest_grouped(tiles, w, count, cost);
     if (query) {

@@ -17,13 +17,16 @@ hipError_t run_int8(const ProductArgs& p, int splits, hipStream_t stream)
                true>(p, splits, stream);
 }
 
-// Microseconds a step of 128, as ffn_matmul.hip's table has them.
+// Microseconds a step of 128, as ffn_matmul.hip's table has them; tiles of 64 x 128
+// with four steps in LDS took the place of two 64 x 64 ones on a CU (m 128 n 16384
+// k 4096: 22.3 us and 19.5), and four steps for 128 x 128 that of two groups of waves
+// (m 5327 n 435 k 2730: 22.9 and 20.1).
 hipError_t tiles_int8(const ProductArgs& p, size_t* query, hipStream_t stream)
 {
     constexpr Tile tiles[] = {{256, 256, 256, 1.5f, 0},
                               {128, 128, 512, 1.0f, 0},
                               {128, 128, 256, .60f, 0},
-                              {64, 64, 512, .40f, 0},
+                              {64, 128, 256, .42f, 0},
                               {64, 64, 256, .26f, 64 * 64}};
     const Choice c = cheapest(tiles, p);
     if (query) {
@@ -36,9 +39,9 @@ hipError_t tiles_int8(const ProductArgs& p, size_t* query, hipStream_t stream)
     case 1:
         return run_int8<128, 128, 2, 2, 1, 2>(p, 1, stream);
     case 2:
-        return run_int8<128, 128, 2, 2, 2, 2>(p, 1, stream);
+        return run_int8<128, 128, 2, 2, 1, 4>(p, 1, stream);
     case 3:
-        return run_int8<64, 64, 2, 2, 2, 2>(p, 1, stream);
+        return run_int8<64, 128, 1, 4, 1, 4>(p, 1, stream);
     }
     return run_int8<64, 64, 2, 2, 2, 4>(p, c.splits, stream);
 }
