@@ -225,24 +225,16 @@ struct GradPlace : EveryWorkgroup {
         n = tn;
     }
 };
-// One expert's tiles after the other's, each expert's spread over the XCDs (their
-// times differ by the experts'), and of up to 64 experts those with the most rows
-// first, so that the last tiles are short.
+// One expert's tiles after the other's, each expert's spread over the XCDs, since
+// their times differ by the experts' (m 16384 e 16 n 4096 k 4096, unevenly: 848 us
+// with a run of experts to each XCD, 565 so; those with the most rows first: 580, as
+// finding them takes each workgroup longer than it gains).
 __device__ __forceinline__ int enter_grad(ProductArgs& p, const GroupArgs& g, GradPlace& where)
 {
     const int per = p.tiles_m * p.tiles_n;
-    int e = (int)blockIdx.x / per, first;
+    const int e = (int)blockIdx.x / per;
     const int t = place_of((int)blockIdx.x - e * per, per);
-    if (g.experts > 1 && g.experts <= 64) {
-        const int lane = threadIdx.x & 63;
-        const int n = lane < g.experts ? rows_of(g, lane, first) : -1;
-        int rank = 0;
-        for (int o = 0; o < g.experts; ++o) {
-            const int other = __builtin_amdgcn_readlane(n, o);
-            rank += other > n || (other == n && o < lane) ? 1 : 0;
-        }
-        e = __builtin_ctzll(__ballot(lane < g.experts && rank == e));
-    }
+    int first;
     const int rows = __builtin_amdgcn_readfirstlane(rows_of(g, e, first));
     first = __builtin_amdgcn_readfirstlane(first);
     tile_at(t, p.tiles_m, p.tiles_n, where.tm, where.tn);
@@ -382,7 +374,7 @@ hipError_t run_grad(ProductArgs p, const GroupArgs& g, int splits, hipStream_t s
 //   256 x 256                    256   1.45  9     1.9  11    1.45  9
 //   128 x 128, two on a CU       512   1.06  6     1.2   7    1.0   6
 //   128 x 128, deeper            256    .62  5       -         .60  5
-//   64 x 128                     256    .42  4      .85  6     .42  4
+//   64 x 128                     256    .42  4      .68  6     .42  4
 //   64 x 128, three on a CU      768                1.4   6
 //   8 bits, 64 x 64, deeper      256                           .26  3
 // and the bytes at 6.5 TB/s, at any address 2.5, 2.7 and 3.8.
@@ -515,7 +507,7 @@ hipError_t grouped16(const ProductArgs& p, const GroupArgs& g, size_t* query, hi
     constexpr GroupTile any[] = {{256, 256, 256, 1.9f, 11.f, 0, 2.5e6f},
                                  {128, 128, 512, 1.2f, 7.f, 0, 2.7e6f},
                                  {64, 128, 768, 1.4f, 6.f, 64 * 128, 3.8e6f},
-                                 {64, 128, 256, .85f, 6.f, 0, 3.8e6f}};
+                                 {64, 128, 256, .68f, 6.f, 0, 3.8e6f}};
     constexpr GroupTile tiles[] = {{256, 256, 256, 1.45f, 9.f, 0},
                                    {128, 128, 512, 1.06f, 6.f, 0},
                                    {128, 128, 256, .62f, 5.f, 128 * 128},

@@ -562,6 +562,11 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
     // Scales: rows of A stand on lanes, TM consecutive ones on a lane (that is
     // what row_of is for), rows of B on the four registers of a result.
     const int q = lane >> 4, l16 = lane & 15;
+    // Steps that operands at any address are fetched ahead of: two where a tile's
+    // registers hold them, since with one a step lasts as long as its loads (64 x 128
+    // tiles, bf16 m 921 e 7 n 1501 k 2047: 33 us with one, 27.6 with two; 128 x 128
+    // ones, two on a CU, 39.4 and 39.6).
+    constexpr int kAhead = REG == kAnyAddress && WIDE && BM == 64 ? 2 : 1;
     if constexpr (REG) {
         v4i held[GA + GB];
         if constexpr (REG == kAnyAddress)
@@ -608,6 +613,123 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
                 *at = v;
             }
         }
+    };
+
+    // A step; what is fetched comes into one, what has been goes to LDS from the other.
+    auto step = [&](int kt, auto& into, auto& from) __attribute__((always_inline)) {
+        // The step's own loads have arrived, those of later steps go on.
+        if constexpr (!REG) {
+            if (NS > 2 && kt + (NS - 2) * WK < nk)
+                wait_vm<(NS - 2) * kLoads>();
+            else
+                wait_vm<0>();
+        }
+        __syncthreads();
+        unsigned char* buf = lds + buffer_of(kt);
+        const int k0 = kt - kg;      // the round's first step
+        if (!REG && ktail && (k0 + WK >= all || (p.parts > 1 && k0 < nks && k0 + WK >= nks))) {
+            cut(kt, buf);
+            __syncthreads();
+        }
+        if constexpr (REG == kAnyAddress)
+            fetch(kt + kAhead < nk ? kt + kAhead : nk - 1, into);
+        else if constexpr (REG == kShortRows)
+            fetch_short(kt + 1 < nk ? kt + 1 : kt, into);
+        if (WK > 1 && kt >= nk)
+            return false;     // (the last round: no barrier follows in the loop)
+        float sa[TM], sb[2];
+        v4f sbr[TN];
+        if constexpr (SM != kNoScale) {
+#pragma unroll
+            for (int i = 0; i < TM; ++i)
+                sa[i] = ((const float*)(buf + so))[i];
+            if constexpr (SM == kRowScale) {
+#pragma unroll
+                for (int j = 0; j < TN; ++j)
+                    sbr[j] = *(const v4f*)(buf + sbo + j * 64);
+            } else {
+                sb[0] = *(const float*)(buf + sbo);
+                if constexpr (kDual)
+                    sb[1] = *(const float*)(buf + sbo + BNO * 4);
+            }
+        }
+        v4i b[TN][2];
+#pragma unroll
+        for (int j = 0; j < TN; ++j) {
+            const int row = kDual && j >= TN / 2 ? BNO + (j - TN / 2) * 16 : j * 16;
+            if constexpr (BT) {
+                b[j][0] = read_t_half<BN, kWide>(buf + BM * kStep, wn * TN + j, lane, 0);
+                b[j][1] = read_t_half<BN, kWide>(buf + BM * kStep, wn * TN + j, lane, 1);
+            } else {
+                b[j][0] = *(const v4i*)(buf + bo + row * kStep);
+                b[j][1] = *(const v4i*)(buf + (bo ^ 64) + row * kStep);
+            }
+        }
+        constexpr int kMfmas = TYPE == kTE4m3Exact ? 4 : 1;
+        constexpr int kValus = TYPE == kTE4m3Exact ? 4 : SM == kRowScale ? 8 : 5;
+        // Rows of A in turn: while the matrix instructions of one run, the
+        // next one's operand comes from LDS, and the sums of the last one
+        // are scaled and added.
+        v4i a[2][2];
+        v4f t[2][SM == kNoScale ? 1 : TN];
+        auto read_a = [&](int i) __attribute__((always_inline)) {
+            if constexpr (AT) {
+                read_t<BM>(a[i & 1], buf, wm * TM + i, lane);
+            } else {
+                a[i & 1][0] = *(const v4i*)(buf + ao + i * 16 * kStep);
+                a[i & 1][1] = *(const v4i*)(buf + (ao ^ 64) + i * 16 * kStep);
+            }
+        };
+        read_a(0);
+        auto add = [&](int i) __attribute__((always_inline)) {
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                const float s = sa[i] * (kDual && j >= TN / 2 ? sb[1] : sb[0]);
+#pragma unroll
+                for (int r = 0; r < 4; ++r)
+                    acc[i][j][r] =
+                        __builtin_fmaf(t[i & 1][j][r], SM == kTileScale ? s : sa[i] * sbr[j][r],
+                                       acc[i][j][r]);
+            }
+        };
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+            if (i + 1 < TM)
+                read_a(i + 1);
+#pragma unroll
+            for (int j = 0; j < TN; ++j) {
+                if constexpr (TYPE == kTI8)
+                    acc[i][j] = matrix_step_i8(b[j], a[i & 1], acc[i][j]);
+                else if constexpr (SM == kNoScale)
+                    acc[i][j] = matrix_step<TYPE>(b[j], a[i & 1], acc[i][j]);
+                else
+                    t[i & 1][j] = matrix_step<TYPE>(b[j], a[i & 1], v4f{0.f, 0.f, 0.f, 0.f});
+            }
+            if constexpr (SM != kNoScale)
+                if (i > 0)
+                    add(i - 1);
+            // (after the first rows' matrix instructions are on their way)
+            if constexpr (!REG)
+                if (i == 0 && kt + (NS - 1) * WK < nk)
+                    stage(kt + (NS - 1) * WK);
+            if (i + 1 < TM)
+                __builtin_amdgcn_sched_group_barrier(0x100, AT ? 4 : 2, 0);   // LDS reads
+            if constexpr (SM != kNoScale) {
+#pragma unroll
+                for (int j = 0; j < TN * kMfmas; ++j) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix
+                    __builtin_amdgcn_sched_group_barrier(0x002, kValus, 0);   // vector
+                }
+            }
+            __builtin_amdgcn_sched_barrier(0);
+        }
+        if constexpr (SM != kNoScale)
+            add(TM - 1);
+        if constexpr (REG) {
+            if (kt + 1 < nk)
+                put(kt + 1, from);
+        }
+        return true;
     };
 
     if constexpr (PIPE) {
@@ -701,121 +823,19 @@ __device__ __forceinline__ void product_body(const ProductArgs& p, int tm, int t
                 __builtin_amdgcn_sched_barrier(0);
             }
         }
-    } else
-    for (int kt = first + kg; kt - kg < nk; kt += WK) {
-        // The step's own loads have arrived, those of later steps go on.
-        if constexpr (!REG) {
-            if (NS > 2 && kt + (NS - 2) * WK < nk)
-                wait_vm<(NS - 2) * kLoads>();
-            else
-                wait_vm<0>();
-        }
-        __syncthreads();
-        unsigned char* buf = lds + buffer_of(kt);
-        const int k0 = kt - kg;      // the round's first step
-        if (!REG && ktail && (k0 + WK >= all || (p.parts > 1 && k0 < nks && k0 + WK >= nks))) {
-            cut(kt, buf);
-            __syncthreads();
-        }
-        v4i held[REG ? GA + GB : 1];
-        if constexpr (REG == kAnyAddress)
-            fetch(kt + 1 < nk ? kt + 1 : kt, held);
-        else if constexpr (REG == kShortRows)
-            fetch_short(kt + 1 < nk ? kt + 1 : kt, held);
-        if (WK > 1 && kt >= nk)
-            break;     // (the last round: no barrier follows in the loop)
-        float sa[TM], sb[2];
-        v4f sbr[TN];
-        if constexpr (SM != kNoScale) {
-#pragma unroll
-            for (int i = 0; i < TM; ++i)
-                sa[i] = ((const float*)(buf + so))[i];
-            if constexpr (SM == kRowScale) {
-#pragma unroll
-                for (int j = 0; j < TN; ++j)
-                    sbr[j] = *(const v4f*)(buf + sbo + j * 64);
-            } else {
-                sb[0] = *(const float*)(buf + sbo);
-                if constexpr (kDual)
-                    sb[1] = *(const float*)(buf + sbo + BNO * 4);
-            }
-        }
-        v4i b[TN][2];
-#pragma unroll
-        for (int j = 0; j < TN; ++j) {
-            const int row = kDual && j >= TN / 2 ? BNO + (j - TN / 2) * 16 : j * 16;
-            if constexpr (BT) {
-                b[j][0] = read_t_half<BN, kWide>(buf + BM * kStep, wn * TN + j, lane, 0);
-                b[j][1] = read_t_half<BN, kWide>(buf + BM * kStep, wn * TN + j, lane, 1);
-            } else {
-                b[j][0] = *(const v4i*)(buf + bo + row * kStep);
-                b[j][1] = *(const v4i*)(buf + (bo ^ 64) + row * kStep);
-            }
-        }
-        constexpr int kMfmas = TYPE == kTE4m3Exact ? 4 : 1;
-        constexpr int kValus = TYPE == kTE4m3Exact ? 4 : SM == kRowScale ? 8 : 5;
-        // Rows of A in turn: while the matrix instructions of one run, the
-        // next one's operand comes from LDS, and the sums of the last one
-        // are scaled and added.
-        v4i a[2][2];
-        v4f t[2][SM == kNoScale ? 1 : TN];
-        auto read_a = [&](int i) __attribute__((always_inline)) {
-            if constexpr (AT) {
-                read_t<BM>(a[i & 1], buf, wm * TM + i, lane);
-            } else {
-                a[i & 1][0] = *(const v4i*)(buf + ao + i * 16 * kStep);
-                a[i & 1][1] = *(const v4i*)(buf + (ao ^ 64) + i * 16 * kStep);
-            }
-        };
-        read_a(0);
-        auto add = [&](int i) __attribute__((always_inline)) {
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                const float s = sa[i] * (kDual && j >= TN / 2 ? sb[1] : sb[0]);
-#pragma unroll
-                for (int r = 0; r < 4; ++r)
-                    acc[i][j][r] =
-                        __builtin_fmaf(t[i & 1][j][r], SM == kTileScale ? s : sa[i] * sbr[j][r],
-                                       acc[i][j][r]);
-            }
-        };
-#pragma unroll
-        for (int i = 0; i < TM; ++i) {
-            if (i + 1 < TM)
-                read_a(i + 1);
-#pragma unroll
-            for (int j = 0; j < TN; ++j) {
-                if constexpr (TYPE == kTI8)
-                    acc[i][j] = matrix_step_i8(b[j], a[i & 1], acc[i][j]);
-                else if constexpr (SM == kNoScale)
-                    acc[i][j] = matrix_step<TYPE>(b[j], a[i & 1], acc[i][j]);
-                else
-                    t[i & 1][j] = matrix_step<TYPE>(b[j], a[i & 1], v4f{0.f, 0.f, 0.f, 0.f});
-            }
-            if constexpr (SM != kNoScale)
-                if (i > 0)
-                    add(i - 1);
-            // (after the first rows' matrix instructions are on their way)
-            if constexpr (!REG)
-                if (i == 0 && kt + (NS - 1) * WK < nk)
-                    stage(kt + (NS - 1) * WK);
-            if (i + 1 < TM)
-                __builtin_amdgcn_sched_group_barrier(0x100, AT ? 4 : 2, 0);   // LDS reads
-            if constexpr (SM != kNoScale) {
-#pragma unroll
-                for (int j = 0; j < TN * kMfmas; ++j) {
-                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);   // matrix
-                    __builtin_amdgcn_sched_group_barrier(0x002, kValus, 0);   // vector
-                }
-            }
-            __builtin_amdgcn_sched_barrier(0);
-        }
-        if constexpr (SM != kNoScale)
-            add(TM - 1);
-        if constexpr (REG) {
+    } else if constexpr (kAhead > 1) {
+        v4i held[2][GA + GB];
+        fetch(first + 1 < nk ? first + 1 : first, held[1]);
+        for (int kt = first; kt < nk; kt += 2) {
+            step(kt, held[0], held[1]);
             if (kt + 1 < nk)
-                put(kt + 1, held);
+                step(kt + 1, held[1], held[0]);
         }
+    } else {
+        v4i held[REG ? GA + GB : 1];
+        for (int kt = first + kg; kt - kg < nk; kt += WK)
+            if (!step(kt, held, held))
+                break;
     }
 
     // The groups' sums join in LDS, in the groups' order.
