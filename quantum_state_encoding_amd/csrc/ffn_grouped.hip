@@ -427,7 +427,7 @@ Choice cheapest_grouped(const GroupTile (&tiles)[N], const GroupCosts& w, const 
             s = s > 1 ? (w.steps + (w.steps + s - 1) / s - 1) / ((w.steps + s - 1) / s) : 1;
             const double sums = 2.0 * s * most * t.area * 4;
             const double shared =
-                both((double)((w.steps + s - 1) / s) * t.step + t.round) + 4.0 + sums / kSumBytes;
+                both((double)((w.steps + s - 1) / s) * t.step + t.round) + 6.0 + sums / kSumBytes;
             if (s > 1 && shared < cost) {
                 cost = shared;
                 splits = (int)s;
@@ -471,7 +471,8 @@ Choice choose(const GroupTile (&tiles)[N], const ProductArgs& p, const GroupArgs
         least);
 }
 
-// Strips: the weights' bytes for every 16 rows of a group, and some time to start.
+// Strips: the weights' bytes for every 16 rows of a group, or the steps that each of
+// a strip's eight waves takes (0.85 us each), and some time to start.
 // Groups of a row or two take them (about 26 experts of 2048 x 4096, bf16: 70 us and
 // 75 with 64 x 128 tiles, in two rounds; 18 experts of 496 x 3712: 16.8 and 23.9),
 // others are faster in tiles (64 experts of 2048 x 4096, 4 rows each in the mean,
@@ -482,7 +483,9 @@ double strips_cost(const ProductArgs& p, const GroupArgs& g, double rate)
     if (most_tiles(p.m, groups_of(g), 16) * ((p.n + 15) / 16) >= kFfnMaxTiles)
         return kNever;
     const double groups = groups_with_rows(p, g), avg = p.m / groups;
-    return 4.0 + groups * (avg > 1 ? 1 + avg / 16 : 1) * p.n * p.kbytes / rate;
+    const double bytes = groups * (avg > 1 ? 1 + avg / 16 : 1) * p.n * p.kbytes / rate;
+    const double steps = 0.85 * (double)p.kbytes / (8 * kStep);
+    return 4.0 + (bytes > steps ? bytes : steps);
 }
 
 template <int TYPE, int MT, int W, int U, bool ODD>

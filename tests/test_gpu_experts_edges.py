@@ -1,0 +1,334 @@
+"""Edges of the 8-bit integer products and of the products grouped by expert:
+padding that is not a number, many experts, tiles shared by two workgroups,
+strided gradients, two threads.  References and tolerances as in
+test_gpu_experts.py."""
+import ctypes
+import threading
+
+import pytest
+
+import quantum_state_encoding_amd as qse
+from quantum_state_encoding_amd import experts
+
+pytestmark = pytest.mark.gpu
+torch = pytest.importorskip("torch")
+
+from test_gpu_experts import (DT, cdiv, check_sums, codes, ends_of, gen, group_bounds,  # noqa: E402
+                              grouped_reference, int8_result, say, some_scales,
+                              spread_counts)
+
+
+def in_padding(t, rows=0):
+    """t in rows padded to 16 bytes, NaN around it (no row behind the last)."""
+    k = t.shape[-1]
+    pad = cdiv(k, 8) * 8 + 8
+    big = torch.full(t.shape[:-1] + (pad,), float("nan"), dtype=t.dtype, device="cuda")
+    view = big[..., :k]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("counts,rest,n,k", [
+    ([3, 0, 5, 1], 2, 70, 257), ([40, 1, 0, 33], 9, 129, 999), ([200, 0, 56], 0, 251, 61),
+    ([130, 129, 0, 1, 300], 77, 500, 71), ([700], 0, 1003, 205), ([600, 500], 0, 2051, 139),
+    ([1], 0, 5, 3), ([3000, 10, 1500, 0, 2000], 100, 3001, 267), ([300, 21], 5, 203, 9001),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_aligned_rows_with_padding_that_is_not_a_number(counts, rest, n, k, dtype):
+    say("padding", counts, rest, n, k, dtype)
+    g, dt = gen(n), DT[dtype]
+    m, e = sum(counts) + rest, len(counts)
+    x = torch.randn(m, k, generator=g, device="cuda").to(dt)
+    w = (torch.randn(e, n, k, generator=g, device="cuda") * k ** -0.5).to(dt)
+    dy = (torch.randn(m, n, generator=g, device="cuda") * 0.1).to(dt)
+    xs, ws, ds, ends = in_padding(x), in_padding(w), in_padding(dy), ends_of(counts)
+    used = m - rest
+    xs[used:] = float("nan")
+    ds[used:] = float("nan")
+    y = qse.grouped_matmul(xs, ws, ends)
+    want, mag = grouped_reference(x, w, counts, m)
+    check_sums(y, want, mag, k, dt)
+    dx, dw = qse.grouped_matmul_backward(xs, ws, ends, ds)
+    assert bool((dx[used:] == 0).all())
+    for i, lo, hi in group_bounds(counts):
+        if hi == lo:
+            assert bool((dw[i] == 0).all())
+            continue
+        gr, a, b = dy[lo:hi].double(), x[lo:hi].double(), w[i].double()
+        check_sums(dx[lo:hi], gr @ b, gr.abs() @ b.abs(), n, dt)
+        check_sums(dw[i], gr.t() @ a, gr.abs().t() @ a.abs(), hi - lo, dt)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "int8"])
+@pytest.mark.parametrize("where", ["x", "w"])
+def test_values_that_are_not_finite_stay_in_their_rows_and_columns(kind, where):
+    say("not finite", kind, where)
+    g = gen(7)
+    for counts, n, k in (([3, 2, 0, 4], 40, 130), ([300, 70, 0, 600], 520, 328)):
+        m, e = sum(counts), len(counts)
+        if kind == "int8":
+            x, w = codes(g, m, k), codes(g, e, n, k)
+            kw = dict(x_scales=some_scales(g, m), w_scales=some_scales(g, e, n))
+        else:
+            x = torch.randn(m, k, generator=g, device="cuda").bfloat16()
+            w = torch.randn(e, n, k, generator=g, device="cuda").bfloat16()
+            kw = {}
+        ends = ends_of(counts)
+        clean = qse.grouped_matmul(x, w, ends, **kw)
+        keep = torch.ones_like(clean, dtype=torch.bool)
+        if where == "x":
+            keep[counts[0]] = False                  # a row of the second expert
+            if kind == "int8":
+                kw["x_scales"][counts[0]] = float("nan")
+            else:
+                x[counts[0], k - 1] = float("inf")
+        else:
+            keep[sum(counts[:3]):, n - 1] = False    # the last expert's last column
+            if kind == "int8":
+                kw["w_scales"][3, n - 1] = float("inf")
+            else:
+                w[3, n - 1, 0] = float("nan")
+        y = qse.grouped_matmul(x, w, ends, **kw)
+        assert torch.equal(y[keep], clean[keep])
+        assert not bool(torch.isfinite(y[~keep]).any())
+
+
+@pytest.mark.parametrize("e", [63, 64, 65, 127, 128, 129, 1000, 5000])
+@pytest.mark.parametrize("m", [1, 50, 3000])
+def test_many_experts(e, m):
+    say("many experts", e, m)
+    g = gen(e + m)
+    n, k = 24, 32
+    counts = spread_counts(m, e, e)
+    x, w = codes(g, m + 3, k), codes(g, e, n, k)
+    sx, sw = some_scales(g, m + 3), some_scales(g, e, n)
+    y = qse.grouped_matmul(x, w, ends_of(counts), x_scales=sx, w_scales=sw)
+    owner = torch.repeat_interleave(torch.arange(e), torch.tensor(counts)).cuda()
+    sums = (x[:m].double()[:, None] * w[owner].double()).sum(2).float()
+    assert torch.equal(y[:m], (sums * sx[:m, None] * sw[owner]).bfloat16())
+    assert bool((y[m:] == 0).all())
+    xh = torch.randn(m + 3, k, generator=g, device="cuda").half()
+    wh = torch.randn(e, n, k, generator=g, device="cuda").half()
+    dy = torch.randn(m + 3, n, generator=g, device="cuda").half()
+    dx, dw = qse.grouped_matmul_backward(xh, wh, ends_of(counts), dy)
+    want = (dy[:m].double()[:, :, None] * wh[owner].double()).sum(1)
+    mag = (dy[:m].double()[:, :, None] * wh[owner].double()).abs().sum(1)
+    check_sums(dx[:m], want, mag, n, torch.float16)
+    assert bool((dx[m:] == 0).all())
+    each = dy[:m].double()[:, :, None] * xh[:m].double()[:, None]
+    want = torch.zeros(e, n, k, dtype=torch.float64, device="cuda").index_add_(0, owner, each)
+    mag = torch.zeros(e, n, k, dtype=torch.float64, device="cuda").index_add_(0, owner, each.abs())
+    check_sums(dw, want, mag, max(counts), torch.float16)
+
+
+@pytest.mark.parametrize("counts,n", [
+    # whole rounds of 256 tiles and a few more, which two workgroups share each:
+    # of more and of fewer than half a tile's rows, with rows of no expert
+    ([2049] * 4, 4096), ([2048 + 128] * 4, 4096), ([2048 + 129] * 4, 4096),
+    ([8192 + 1], 2048), ([2300, 1700, 4196], 2050), ([256] * 33, 2048), ([100] * 80, 2048),
+    ([4096 + 256], 4096),
+])
+@pytest.mark.parametrize("rest", [0, 700])
+def test_last_tiles_shared_by_two(counts, n, rest):
+    say("halves", counts[:4], len(counts), n, rest)
+    g = gen(len(counts) + n)
+    m, e, k = sum(counts) + rest, len(counts), 320
+    x, w = codes(g, m, k), codes(g, e, n, k)
+    sx, sw = some_scales(g, m), some_scales(g, e, n)
+    ends = ends_of(counts)
+    y = qse.grouped_matmul(x, w, ends, x_scales=sx, w_scales=sw)
+    for i, lo, hi in group_bounds(counts):
+        assert torch.equal(y[lo:hi], int8_result(x[lo:hi], sx[lo:hi], w[i], sw[i], torch.bfloat16))
+    assert bool((y[m - rest:] == 0).all())
+    out = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+    qse.grouped_matmul(x, w, ends, x_scales=sx, w_scales=sw, out=out)
+    assert torch.equal(out[:m - rest], y[:m - rest]) and bool((out[m - rest:] == 7.0).all())
+    xh = x.bfloat16()
+    wh = (w[:, :, :64] // 16).bfloat16()
+    z = qse.grouped_matmul(xh[:, :64], wh, ends)
+    for i, lo, hi in list(group_bounds(counts))[::7]:
+        a, b = xh[lo:hi, :64].double(), wh[i].double()
+        check_sums(z[lo:hi], a @ b.t(), a.abs() @ b.abs().t(), 64, torch.bfloat16)
+    assert bool((z[m - rest:] == 0).all())
+
+
+def test_strided_gradients_through_the_entry_point():
+    say("strided gradients")
+    L = experts._load()
+    g = gen(3)
+    stream = torch.cuda.current_stream().cuda_stream
+    for counts, rest, n, k in (([50, 0, 70], 9, 40, 72), ([600, 300, 0, 500], 30, 520, 264),
+                               ([50, 0, 70], 9, 41, 73)):
+        m, e = sum(counts) + rest, len(counts)
+        x = torch.randn(m, k, generator=g, device="cuda").bfloat16()
+        w = torch.randn(e, n, k, generator=g, device="cuda").bfloat16()
+        dy = torch.randn(m, n, generator=g, device="cuda").bfloat16()
+        ends = ends_of(counts)
+        want = qse.grouped_matmul_backward(x, w, ends, dy)
+        bx = torch.full((m, k + 13), 7.0, dtype=torch.bfloat16, device="cuda")
+        bw = torch.full((e, n + 2, k + 5), 7.0, dtype=torch.bfloat16, device="cuda")
+        dx, dw = bx[:, 5:5 + k], bw[:, 1:1 + n, 3:3 + k]
+
+        def call(dxp, dwp):
+            return L.fwt_grouped_matmul_backward(
+                x.data_ptr(), k, w.data_ptr(), k, n * k, ends.data_ptr(), e, dy.data_ptr(), n, 0,
+                m, n, k, dxp, k + 13, dwp, k + 5, (n + 2) * (k + 5), None, 0, stream)
+
+        assert call(dx.data_ptr(), None) == 0
+        check = torch.full_like(bw, 7.0)
+        assert torch.equal(bw, check)            # dw was not asked for
+        assert call(None, dw.data_ptr()) == 0
+        assert torch.equal(dx, want[0])
+        gr, a = dy.double(), x.double()
+        for i, lo, hi in group_bounds(counts):
+            check_sums(dw[i], gr[lo:hi].t() @ a[lo:hi], gr[lo:hi].abs().t() @ a[lo:hi].abs(),
+                       max(hi - lo, 1), torch.bfloat16)
+        dx.fill_(7.0)
+        dw.fill_(7.0)
+        assert bool((bx == 7.0).all()) and bool((bw == 7.0).all())
+
+
+def test_rows_of_no_expert_through_the_entry_point():
+    say("zero_rest")
+    L = experts._load()
+    g = gen(4)
+    m, n, k = 90, 33, 64
+    x = torch.randn(m, k, generator=g, device="cuda").bfloat16()
+    w = torch.randn(2, n, k, generator=g, device="cuda").bfloat16()
+    ends = ends_of([20, 30])
+    for zero in (0, 1):
+        y = torch.full((m, n), 7.0, dtype=torch.bfloat16, device="cuda")
+        assert L.fwt_grouped_matmul(x.data_ptr(), k, None, w.data_ptr(), k, n * k, None,
+                                    ends.data_ptr(), 2, 0, m, n, k, y.data_ptr(), 0, n, zero, None,
+                                    0, torch.cuda.current_stream().cuda_stream) == 0
+        assert bool((y[50:] == (0.0 if zero else 7.0)).all())
+
+
+def test_results_do_not_depend_on_where_a_group_lies():
+    # an expert's rows give the same bits in any group of the same call's sizes
+    say("place")
+    g = gen(9)
+    n, k = 300, 520
+    x = torch.randn(400, k, generator=g, device="cuda").bfloat16()
+    w = torch.randn(1, n, k, generator=g, device="cuda").bfloat16().expand(4, n, k).contiguous()
+    first = qse.grouped_matmul(x, w, ends_of([400, 0, 0, 0]))
+    for counts in ([0, 400, 0, 0], [100, 100, 100, 100], [1, 398, 0, 1], [33, 0, 367, 0]):
+        assert torch.equal(qse.grouped_matmul(x, w, ends_of(counts)), first)
+
+
+def test_two_threads_on_streams_of_their_own():
+    say("threads")
+    g = gen(5)
+    counts = [100, 0, 350, 50]
+    x = torch.randn(500, 2048, generator=g, device="cuda").bfloat16()
+    w = torch.randn(4, 256, 2048, generator=g, device="cuda").bfloat16()
+    dy = torch.randn(500, 256, generator=g, device="cuda").bfloat16()
+    ends = ends_of(counts)
+
+    def calls():
+        q, s = qse.rotate_quantize_int8(x, bits=11)
+        wq, ws = qse.rotate_quantize_int8(w.view(-1, 2048), bits=11)
+        return [qse.grouped_matmul(x, w, ends), *qse.grouped_matmul_backward(x, w, ends, dy), q, s,
+                qse.grouped_matmul(q, wq.view(4, 256, 2048), ends, x_scales=s,
+                                   w_scales=ws.view(4, 256)),
+                qse.int8_matmul(q[:300], s[:300], wq[:200], ws[:200])]
+
+    want = calls()
+    torch.cuda.synchronize()
+    bad = []
+
+    def work():
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = calls()
+                stream.synchronize()
+                if not all(torch.equal(a, b) for a, b in zip(got, want)):
+                    bad.append(1)
+
+    threads = [threading.Thread(target=work) for _ in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad
+
+
+def test_a_given_stream_keeps_the_operands():
+    # the operands' memory is not handed out again before the stream has passed
+    say("kept operands")
+    g = gen(6)
+    side = torch.cuda.Stream()
+    base = torch.randn(512, 4096, generator=g, device="cuda").bfloat16()
+    w = torch.randn(4, 512, 4096, generator=g, device="cuda").bfloat16()
+    ends = ends_of([100, 200, 12, 200])
+    want = qse.grouped_matmul(base, w, ends)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        x = base.clone()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            got = qse.grouped_matmul(x, w, ends, stream=side)
+        del x
+        junk = torch.full((512, 4096), 9.0, dtype=torch.bfloat16, device="cuda")
+        side.synchronize()
+        assert torch.equal(got, want)
+        del junk
+
+
+def test_outputs_count_as_written():
+    say("written")
+    x = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, 8, 16, dtype=torch.bfloat16, device="cuda")
+    out = torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda")
+    before = out._version
+    qse.grouped_matmul(x, w, ends_of([4]), out=out)
+    assert out._version > before
+    before = out._version
+    q, s = x.to(torch.int8), torch.ones(4, device="cuda")
+    qse.int8_matmul(q, s, q[:1].expand(8, 16).contiguous(), torch.ones(8, device="cuda"), out=out)
+    assert out._version > before
+
+
+def test_workspaces_are_enough_for_every_number_of_groups():
+    # the scratch that is asked for holds the sums whatever zero_rest is: what
+    # lies behind it stays as it was
+    say("workspace")
+    L = experts._load()
+    stream = torch.cuda.current_stream().cuda_stream
+    for e, m, n, k in ((1, 17, 64, 4096), (2, 100, 100, 16000), (7, 921, 300, 2048), (3, 400, 500, 3000),
+                       (5, 64, 128, 8192), (85, 85, 64, 2048), (1, 2000, 1000, 1000)):
+        size = ctypes.c_size_t()
+        for dtype, tdt in ((0, torch.bfloat16), (5, torch.int8)):
+            if dtype == 5 and k % 16:
+                continue
+            assert L.fwt_grouped_matmul_workspace(dtype, e, m, n, k, ctypes.byref(size)) == 0
+            ws = torch.full((size.value + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+            counts = spread_counts(m, e, m)
+            g = gen(m)
+            ends = ends_of(counts)
+            if dtype == 5:
+                x, w = codes(g, m, k), codes(g, e, n, k)
+                sx, sw = some_scales(g, m), some_scales(g, e, n)
+            else:
+                x = torch.randn(m, k, generator=g, device="cuda").to(tdt)
+                w = torch.randn(e, n, k, generator=g, device="cuda").to(tdt)
+                sx = sw = None
+            ys = []
+            for zero in (0, 1):
+                y = torch.empty(m, n, dtype=torch.bfloat16, device="cuda")
+                assert L.fwt_grouped_matmul(
+                    x.data_ptr(), k, sx.data_ptr() if dtype else None, w.data_ptr(), k, n * k,
+                    sw.data_ptr() if dtype else None, ends.data_ptr(), e, dtype, m, n, k,
+                    y.data_ptr(), 0, n, zero, ws.data_ptr() if size.value else None, size.value,
+                    stream) == 0
+                ys.append(y)
+            assert bool((ws[size.value:] == 0x5a).all())
+            assert torch.equal(ys[0], ys[1])
+            want, mag = (None, None) if dtype else grouped_reference(x, w, counts, m)
+            if not dtype:
+                check_sums(ys[0], want, mag, k, torch.bfloat16)
+            else:
+                for i, lo, hi in group_bounds(counts):
+                    assert torch.equal(ys[0][lo:hi], int8_result(x[lo:hi], sx[lo:hi], w[i], sw[i],
+                                                                 torch.bfloat16))
