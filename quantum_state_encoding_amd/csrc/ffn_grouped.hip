@@ -35,13 +35,14 @@ __device__ __forceinline__ int rows_of(const GroupArgs& g, int e, int& first)
 // columns: 64 groups at a time, one on each lane, whose tiles are summed across
 // the wave (every wave finds the same).  Each XCD gets a contiguous run of them.
 // HALVES: where the last round of tiles would leave half of the CUs without one,
-// two workgroups (of one XCD) take half of each tile's rows.
+// two workgroups (of one XCD) take half of each tile's rows.  Behind them all come
+// the tiles of the rows of no expert, which take no time to speak of.
 constexpr int kCus = 256;
 template <int BM, bool HALVES = false>
 __device__ __forceinline__ bool find_group(const GroupArgs& g, int w, int tiles_n, Group& at)
 {
     const int lane = threadIdx.x & 63;
-    const int groups = g.experts + (g.zero_rest ? 1 : 0);
+    const int groups = g.experts;
     const auto sum = [=](int base, int& first, int& rows, int& tiles) __attribute__((always_inline)) {
         const int e = base + lane;
         rows = e < groups ? rows_of(g, e, first) : 0;
@@ -62,16 +63,27 @@ __device__ __forceinline__ bool find_group(const GroupArgs& g, int w, int tiles_
         total += __builtin_amdgcn_readlane(sum(base, f, r, t), 63);
     }
     at.half = 0;
+    int items = total;
     if constexpr (HALVES) {
         const int last = total % kCus, whole = total - last;
-        if (last <= kCus / 2 && w >= whole) {
-            const int j = w - whole;
-            at.half = 1 + ((j >> 3) & 1);
-            w = whole + ((j >> 4) << 3) + (j & 7);
+        if (last <= kCus / 2) {
+            items = whole + ((last + 7) >> 3 << 4);
+            if (w >= whole && w < items) {
+                const int j = w - whole;
+                at.half = 1 + ((j >> 3) & 1);
+                w = whole + ((j >> 4) << 3) + (j & 7);
+                if (w >= total)
+                    return false;
+            }
         }
     }
-    if (w >= total)
-        return false;
+    if (w >= items) {
+        at.e = g.experts;
+        at.tile = w - items;
+        at.rows = g.zero_rest ? __builtin_amdgcn_readfirstlane(rows_of(g, g.experts, first)) : 0;
+        at.first = __builtin_amdgcn_readfirstlane(first);
+        return at.tile < (at.rows + BM - 1) / BM * tiles_n;
+    }
     const int t = place_of(w, total);
     int before = 0;
     for (int base = 0; base < groups; base += 64) {
@@ -156,7 +168,7 @@ grouped_kernel(ProductArgs p, const GroupArgs g)
     if (!find_group<BM, kPipe>(g, (int)blockIdx.x, p.tiles_n, at))
         return;
     if (at.e == g.experts) {
-        if (blockIdx.y == 0 && at.half < 2)
+        if (blockIdx.y == 0)
             zero_rows<BM, BN>(p, at, p.tiles_n);
         return;
     }
@@ -330,7 +342,7 @@ hipError_t run_grouped(ProductArgs p, const GroupArgs& g, int splits, hipStream_
     p.tiles_n = (int)((p.n + BN - 1) / BN);
     unsigned tiles = (unsigned)(most_tiles(p.m, groups_of(g), BM) * p.tiles_n);
     if (BM == 256 && !REG)
-        tiles += kCus / 2;               // (halves)
+        tiles += kCus / 2 + 8;           // (halves, and eights of them that are not whole)
     hipLaunchKernelGGL(k, dim3(tiles, (unsigned)splits), dim3(64 * WM * WN * WK), kLds, stream, p, g);
     e = hipGetLastError();
     if (splits == 1 || e != hipSuccess)
