@@ -5,6 +5,15 @@
 // the groups' ends, which only the device knows, and goes on as in a product of
 // that group alone.  The grid has a workgroup for each tile that there could be
 // (a last tile that is not whole for each group); those without one end.
+//
+// What bounds it.  Large groups: the card's power (bf16 steps of 256 x 256 tiles take
+// 1.45 us, 1.12 on operands of zeros) and the groups' last tiles, which are half
+// empty in the mean and take 0.7 of a whole one's time when at most half of their rows
+// exist; a round of tiles takes about 9 us beside its steps.  Few rows: the weights'
+// bytes.  Measured, groups uneven: bf16 m 16384 e 8 n 8192 k 4096 900-975 us by the
+// card, 1.13-1.22 PFLOP/s (library product 1.46), int8 e 32 n 4096 333-348; gradients
+// e 16 n 4096 k 4096 1080-1145 (both 550-590); bf16 one row for each of 32 experts'
+// places, e 64 n 2048 k 4096, 71-73 us, 5.5 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "ffn_product.h"

@@ -9,7 +9,7 @@
 // row of A and B (one k block of e4m3, 64 16-bit elements) into LDS, straight
 // from memory, while earlier ones feed the matrix instructions: 256 x 256
 // where the tiles fill the CUs, since a step's operands then feed most
-// instructions, smaller ones for fewer rows.
+// instructions, smaller ones for fewer rows.  The tile itself is in ffn_product.h.
 //
 // What bounds it: large products the matrix units and their clock (about
 // 1.9 GHz in such a kernel; busy 54-69 % of the CUs' cycles), then the
