@@ -192,8 +192,7 @@ grouped_kernel(ProductArgs p, const GroupArgs g)
         tm = 0;
     }
     enter<TYPE>(p, g, at);
-    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, false, BT,
-                 kPipe, true>(
+    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, false, BT, kPipe, true>(
         p, tm, tn, (int)blockIdx.y, EveryWorkgroup{});
 }
 
@@ -284,8 +283,8 @@ grouped_grad_kernel(ProductArgs p, const GroupArgs g)
         if ((int)blockIdx.y * ((steps + p.splits - 1) / p.splits) >= steps)
             return;
     }
-    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, true, true,
-                 BM == 256 && !REG, true>(
+    constexpr bool kPipe = BM == 256 && !REG;
+    product_body<TYPE, BM, BN, WM, WN, WK, NS, kEpStore, kNoScale, REG, true, true, kPipe, true>(
         p, where.tm, where.tn, (int)blockIdx.y, where);
 }
 
@@ -402,8 +401,9 @@ hipError_t run_grad(ProductArgs p, const GroupArgs& g, int splits, hipStream_t s
 // How the rows are spread is not known: a group is taken to have the average
 // number, and half a tile of rows more than it fills.  Over 53 sizes (4 to 64
 // experts, 0.5 to 2048 rows for each, unevenly) the choice takes 1.5 % longer than
-// the best tile in the mean, at most 16 %.  Where most of a round's slots are empty the workgroups of a
-// tile may share its steps, for a second launch and their sums' bytes.
+// the best tile in the mean, at most 16 %.  Where most of a round's slots are empty
+// the workgroups of a tile may share its steps, for a second launch and their sums'
+// bytes.
 struct GroupTile {
     int bm, bn, slots;
     float step, round;
