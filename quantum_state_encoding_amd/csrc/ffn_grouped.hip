@@ -492,8 +492,9 @@ Choice choose(const GroupTile (&tiles)[N], const ProductArgs& p, const GroupArgs
         least);
 }
 
-// Strips: the weights' bytes for every 16 rows of a group, or the steps that each of
-// a strip's eight waves takes (0.85 us each), and some time to start.
+// Strips: the weights' bytes for every 16 rows of a group, and some time to start, or
+// rounds of two strips on a CU, each the time to start and the steps that its eight
+// waves take in turn (0.85 us each).
 // Groups of a row or two take them (about 26 experts of 2048 x 4096, bf16: 70 us and
 // 75 with 64 x 128 tiles, in two rounds; 18 experts of 496 x 3712: 16.8 and 23.9),
 // others are faster in tiles (64 experts of 2048 x 4096, 4 rows each in the mean,
@@ -504,9 +505,12 @@ double strips_cost(const ProductArgs& p, const GroupArgs& g, double rate)
     if (most_tiles(p.m, groups_of(g), 16) * ((p.n + 15) / 16) >= kFfnMaxTiles)
         return kNever;
     const double groups = groups_with_rows(p, g), avg = p.m / groups;
-    const double bytes = groups * (avg > 1 ? 1 + avg / 16 : 1) * p.n * p.kbytes / rate;
-    const double steps = 0.85 * (double)p.kbytes / (8 * kStep);
-    return 4.0 + (bytes > steps ? bytes : steps);
+    const double each = groups * (avg > 1 ? 1 + avg / 16 : 1);
+    const double bytes = 4.0 + each * p.n * p.kbytes / rate;
+    const double full = each * ((p.n + 15) / 16) / (2 * kCus);
+    const double steps = 4.0 + 0.85 * (double)p.kbytes / (8 * kStep);
+    const double rounds = full > 1 ? full * steps : steps;
+    return bytes > rounds ? bytes : rounds;
 }
 
 template <int TYPE, int MT, int W, int U, bool ODD>
