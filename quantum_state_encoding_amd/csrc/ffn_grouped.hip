@@ -397,7 +397,8 @@ hipError_t run_grad(ProductArgs p, const GroupArgs& g, int splits, hipStream_t s
 //   64 x 128                     256    .42  4      .68  6     .42  4
 //   64 x 128, three on a CU      768                1.4   6
 //   8 bits, 64 x 64, deeper      256                           .26  3
-// and the bytes at 6.5 TB/s, at any address 2.5, 2.7 and 3.8.
+// and the bytes at 6.5 TB/s, at any address 2.5, 2.7 and 3.8 (at multiples of four bytes
+// 3.7, 4.6 and 5.0, and steps of 1.85, 1.1, 0.62 and 1.3).
 // How the rows are spread is not known: a group is taken to have the average
 // number, and half a tile of rows more than it fills.  Over 53 sizes (4 to 64
 // experts, 0.5 to 2048 rows for each, unevenly) the choice takes 1.5 % longer than
@@ -494,12 +495,13 @@ Choice choose(const GroupTile (&tiles)[N], const ProductArgs& p, const GroupArgs
 
 // Strips: the weights' bytes for every 16 rows of a group, and some time to start, or
 // rounds of two strips on a CU, each the time to start and the steps that its eight
-// waves take in turn (0.85 us each).
+// waves take in turn (0.85 us each).  Rates in bytes a microsecond, 16-bit rows at
+// multiples of 16 and of 4 bytes and at others, and of 8-bit integers.
 // Groups of a row or two take them (about 26 experts of 2048 x 4096, bf16: 70 us and
 // 75 with 64 x 128 tiles, in two rounds; 18 experts of 496 x 3712: 16.8 and 23.9),
 // others are faster in tiles (64 experts of 2048 x 4096, 4 rows each in the mean,
 // unevenly: 212 us and 169).
-constexpr double kStrip16 = 5.7e6, kStripOdd = 3.0e6, kStrip8 = 4.6e6;   // bytes a microsecond
+constexpr double kStrip16 = 5.7e6, kStrip4 = 3.7e6, kStripOdd = 3.0e6, kStrip8 = 4.6e6;
 double strips_cost(const ProductArgs& p, const GroupArgs& g, double rate)
 {
     if (most_tiles(p.m, groups_of(g), 16) * ((p.n + 15) / 16) >= kFfnMaxTiles)
@@ -540,16 +542,24 @@ hipError_t grouped16(const ProductArgs& p, const GroupArgs& g, size_t* query, hi
                                    {128, 128, 512, 1.06f, 6.f, 0},
                                    {128, 128, 256, .62f, 5.f, 128 * 128},
                                    {64, 128, 256, .42f, 4.f, 64 * 128}};
-    double cost_any, cost;
-    const Choice ca = choose(any, p, g, cost_any), c = choose(tiles, p, g, cost);
+    // (multiples of four bytes)
+    constexpr GroupTile fours[] = {{256, 256, 256, 1.85f, 11.f, 0, 3.7e6f},
+                                   {128, 128, 512, 1.1f, 7.f, 0, 4.6e6f},
+                                   {64, 128, 768, 1.3f, 6.f, 64 * 128, 5.0e6f},
+                                   {64, 128, 256, .62f, 6.f, 0, 5.0e6f}};
+    double cost_odd, cost_four, cost_tile;
+    const Choice co = choose(any, p, g, cost_odd), cf = choose(fours, p, g, cost_four),
+                 c = choose(tiles, p, g, cost_tile);
     if (query) {
-        *query = ca.bytes > c.bytes ? ca.bytes : c.bytes;
+        *query = co.bytes > c.bytes ? co.bytes : c.bytes;
+        *query = *query > cf.bytes ? *query : cf.bytes;
         return hipSuccess;
     }
-    const bool anywhere = any_address(p, g, 15);
+    const bool anywhere = any_address(p, g, 15), odd = any_address(p, g, 3);
+    const Choice ca = odd ? co : cf;
+    const double cost = odd ? cost_odd : anywhere ? cost_four : cost_tile;
     if constexpr (!BT) {
-        const bool odd = any_address(p, g, 3);
-        if (strips_cost(p, g, odd ? kStripOdd : kStrip16) < (anywhere ? cost_any : cost))
+        if (strips_cost(p, g, odd ? kStripOdd : anywhere ? kStrip4 : kStrip16) < cost)
             return odd ? run_strips<TYPE, 1, 8, 4, true>(p, g, stream)
                        : run_strips<TYPE, 1, 8, 4, false>(p, g, stream);
     }

@@ -59,6 +59,52 @@ def test_aligned_rows_with_padding_that_is_not_a_number(counts, rest, n, k, dtyp
         check_sums(dw[i], gr.t() @ a, gr.abs().t() @ a.abs(), hi - lo, dt)
 
 
+def at_four_bytes(t):
+    """t inside NaN, rows at multiples of 4 bytes, not all of 16."""
+    k = t.shape[-1]
+    ld = cdiv(k, 2) * 2 + 4
+    ld += 2 if ld % 8 == 0 else 0
+    big = torch.full(t.shape[:-1] + (ld,), float("nan"), dtype=t.dtype, device="cuda")
+    view = big[..., 2:2 + k]
+    view.copy_(t)
+    return view
+
+
+@pytest.mark.parametrize("counts,rest,n,k", [
+    ([1], 0, 1, 1), ([2, 1], 1, 3, 2), ([3, 0, 5, 1], 2, 70, 257), ([9, 8], 1, 15, 7),
+    ([40, 1, 0, 33], 9, 129, 998), ([200, 0, 56], 0, 250, 61), ([130, 129, 0, 1, 300], 77, 500, 70),
+    ([700], 0, 1003, 206), ([600, 500], 0, 2050, 138), ([3000, 10, 1500, 0, 2000], 100, 3001, 266),
+    ([300, 21], 5, 202, 9002), ([1] * 70, 3, 34, 130), ([257, 255, 2049], 3, 2046, 126),
+    ([50, 100], 0, 6, 2002), ([50, 100], 0, 2002, 6), ([64], 0, 100, 16002), ([2600], 0, 66, 62),
+])
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+def test_rows_at_multiples_of_four_bytes(counts, rest, n, k, dtype):
+    say("four bytes", counts[:5], rest, n, k, dtype)
+    g, dt = gen(n + k), DT[dtype]
+    m, e = sum(counts) + rest, len(counts)
+    x = torch.randn(m, k, generator=g, device="cuda").to(dt)
+    w = (torch.randn(e, n, k, generator=g, device="cuda") * k ** -0.5).to(dt)
+    dy = (torch.randn(m, n, generator=g, device="cuda") * 0.1).to(dt)
+    xs, ws, ds, ends = at_four_bytes(x), at_four_bytes(w), at_four_bytes(dy), ends_of(counts)
+    for t in (xs, ws, ds):
+        assert t.data_ptr() % 4 == 0 and all(s % 2 == 0 for s in t.stride()[:-1])
+    used = m - rest
+    xs[used:] = float("nan")
+    ds[used:] = float("nan")
+    y = qse.grouped_matmul(xs, ws, ends)
+    want, mag = grouped_reference(x, w, counts, m)
+    check_sums(y, want, mag, k, dt)
+    dx, dw = qse.grouped_matmul_backward(xs, ws, ends, ds)
+    assert bool((dx[used:] == 0).all())
+    for i, lo, hi in group_bounds(counts):
+        if hi == lo:
+            assert bool((dw[i] == 0).all())
+            continue
+        gr, a, b = dy[lo:hi].double(), x[lo:hi].double(), w[i].double()
+        check_sums(dx[lo:hi], gr @ b, gr.abs() @ b.abs(), n, dt)
+        check_sums(dw[i], gr.t() @ a, gr.abs().t() @ a.abs(), hi - lo, dt)
+
+
 @pytest.mark.parametrize("kind", ["bf16", "int8"])
 @pytest.mark.parametrize("where", ["x", "w"])
 def test_values_that_are_not_finite_stay_in_their_rows_and_columns(kind, where):
