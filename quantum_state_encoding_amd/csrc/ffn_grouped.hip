@@ -47,6 +47,9 @@ __device__ __forceinline__ int rows_of(const GroupArgs& g, int e, int& first)
 // two workgroups (of one XCD) take half of each tile's rows.  Behind them all come
 // the tiles of the rows of no expert, which take no time to speak of.
 constexpr int kCus = 256;
+// 64 groups have at most 2^28 tiles, all groups fewer than the grid, unless ends fall:
+// their sum is cut, so that it stays in 32 bits and the tiles found are tiles of theirs.
+constexpr int kTotal = 1 << 29;
 template <int BM, bool HALVES = false>
 __device__ __forceinline__ bool find_group(const GroupArgs& g, int w, int tiles_n, Group& at)
 {
@@ -70,6 +73,7 @@ __device__ __forceinline__ bool find_group(const GroupArgs& g, int w, int tiles_
     for (int base = 64; base < groups; base += 64) {
         int f, r, t;
         total += __builtin_amdgcn_readlane(sum(base, f, r, t), 63);
+        total = total < kTotal ? total : kTotal;
     }
     at.half = 0;
     int items = total;

@@ -167,6 +167,29 @@ def test_many_experts(e, m):
     check_sums(dw, want, mag, max(counts), torch.float16)
 
 
+def test_falling_ends_of_very_many_experts():
+    # every second of 2^16 experts claims all rows: 2^15 times 2^16 tiles of 128 x 128
+    # and more, which 32 bits do not hold.  The rows are unspecified; nothing around
+    # them is written, and rows of the weights that all experts share are what is read.
+    e, m, n, k = 1 << 16, 1 << 20, 1040, 8
+    tiles = (m // 128) * cdiv(n, 128)
+    assert e // 2 * tiles > 2 ** 31
+    say("falling ends", e, m, n, k)
+    ends = torch.zeros(e, dtype=torch.int32, device="cuda")
+    ends[::2] = m
+    x = torch.ones(m, k, dtype=torch.bfloat16, device="cuda")
+    w = torch.ones(e, n, k, dtype=torch.bfloat16, device="cuda")
+    around = torch.full((m + 16, n), -1.0, dtype=torch.bfloat16, device="cuda")
+    qse.grouped_matmul(x, w, ends, out=around[8:m + 8])
+    torch.cuda.synchronize()
+    assert bool((around[:8] == -1).all()) and bool((around[m + 8:] == -1).all())
+    rows = around[8:m + 8]
+    assert bool(((rows == -1) | (rows == k)).all())
+    # and the next call is right
+    y = qse.grouped_matmul(x[:100], w[:3], ends_of([40, 0, 60]))
+    assert bool((y == k).all())
+
+
 @pytest.mark.parametrize("counts,n", [
     # whole rounds of 256 tiles and a few more, which two workgroups share each:
     # of more and of fewer than half a tile's rows, with rows of no expert
