@@ -94,8 +94,11 @@ int fwt_int8_matmul(const void* a, int64_t lda, const float* a_scales, const voi
  *  zero_rest   the rows of y that belong to no expert: 0 leaves them as they
  *              were, otherwise they become 0.
  *  ws          scratch of fwt_grouped_matmul_workspace bytes (0 for most
- *              sizes), as for fwt_int8_matmul.  NULL: a long contraction is not
- *              shared, which takes longer and adds fp32 sums in another order.
+ *              sizes), as for fwt_int8_matmul, and for copies of 16-bit operands
+ *              (up to 1 GiB) where k is no multiple of 8 and a large call on
+ *              aligned rows takes less time with the copying.  NULL: nothing is
+ *              shared or copied, which takes longer and may add fp32 sums in
+ *              another order.
  * Which kernel runs, and so the order of fp32 sums, goes by the sizes, the
  * addresses' alignment and ws, not by where the groups end.
  * More than 2^22 tiles of 128 x 64 results (every expert may have one row of

@@ -69,6 +69,120 @@ bool too_many_weights(int64_t experts, int64_t n, int64_t k)
     return too_many(n, k) || tiles * experts >= qse::kFfnMaxTiles;
 }
 
+// Copies of operands into rows of multiples of 16 bytes, in scratch behind the sums:
+// where those rows' products and the copies take less time.  Rows of fewer than 64
+// elements or of 2^20 and more, and operands of more than 1 GiB together, are left as
+// they are, and those of calls of less than 60 us, where the model is too coarse for
+// what there is to gain (gradients, bf16: m 2523 e 3 n 846 k 627 38.7 us, 41.9 with
+// copies; m 8000 e 4 n 2001 k 2001 276 and 215; m 16000 e 8 n 4001 k 4095, forward, 731
+// and 649).
+constexpr int64_t kMinCopied = 64, kMaxCopied = (int64_t)1 << 20, kMaxCopies = (int64_t)1 << 30;
+
+bool worth_copies(int64_t bytes, double now, double without)
+{
+    return without > 60.0 && now + qse::row_copies_cost(bytes) < without;
+}
+
+bool may_copy(int64_t cols) { return cols >= kMinCopied && cols < kMaxCopied; }
+
+size_t aligned256(size_t n) { return (n + 255) & ~(size_t)255; }
+
+// Bytes of a copy, 0 for rows that need none.
+int64_t copy_bytes(int64_t rows, int64_t cols)
+{
+    return cols % 8 == 0 ? 0 : rows * qse::padded_row(cols);
+}
+
+// How an operand lies: 0 at multiples of 16 bytes, 1 of 4, 2 others.
+int level_of(const void* p, int64_t ld, int64_t stride)
+{
+    const uintptr_t a = (uintptr_t)p | (uintptr_t)(2 * ld) | (uintptr_t)(2 * stride);
+    return (a & 15) == 0 ? 0 : (a & 3) == 0 ? 1 : 2;
+}
+
+int larger(int a, int b) { return a > b ? a : b; }
+
+// dx and dw of the sizes, at these levels.
+double backward_cost(int64_t experts, int64_t m, int64_t n, int64_t k, int dx, int dw)
+{
+    GroupArgs g = groups(nullptr, experts, m);
+    double cost = 0;
+    if (dx >= 0) {
+        ProductArgs p = sizes(m, k, 2 * n);
+        p.may_split = 1;
+        cost += qse::grouped_cost(p, g, true, dx);
+    }
+    if (dw >= 0) {
+        ProductArgs p = sizes(n, k, 2 * m);
+        p.may_split = 1;
+        cost += qse::grouped_t_cost(p, g, dw);
+    }
+    return cost;
+}
+double forward_cost(int64_t experts, int64_t m, int64_t n, int64_t k, int level)
+{
+    ProductArgs p = sizes(m, n, 2 * k);
+    p.may_split = 1;
+    return qse::grouped_cost(p, groups(nullptr, experts, m), false, level);
+}
+
+// Bytes of scratch for copies, 0 where none are made.
+int64_t forward_copies(int64_t experts, int64_t m, int64_t n, int64_t k)
+{
+    const int64_t bytes = copy_bytes(m, k) + copy_bytes(experts * n, k);
+    return may_copy(k) && bytes && bytes <= kMaxCopies &&
+                   worth_copies(bytes, forward_cost(experts, m, n, k, 0),
+                                forward_cost(experts, m, n, k, 2))
+               ? bytes
+               : 0;
+}
+int64_t backward_copies(int64_t experts, int64_t m, int64_t n, int64_t k)
+{
+    const int64_t bytes = copy_bytes(m + experts * n, k) + copy_bytes(m, n);
+    return may_copy(k) && may_copy(n) && bytes && bytes <= kMaxCopies &&
+                   worth_copies(bytes, backward_cost(experts, m, n, k, 0, 0),
+                                backward_cost(experts, m, n, k, 2, 2))
+               ? bytes
+               : 0;
+}
+
+// The copies of a call.
+struct Copies {
+    qse::RowCopy at[3];
+    int count = 0;
+    int64_t bytes = 0;
+    bool room = true;        // for each that is wanted
+    // a misaligned operand of `rows` (`each` of an expert) by cols: its number, or -1
+    int want(int level, int64_t rows, int64_t cols, int64_t each, const void* src, int64_t ld,
+             int64_t stride)
+    {
+        if (level == 0)
+            return -1;
+        room = room && copy_bytes(rows, cols);
+        at[count] = qse::RowCopy{src, nullptr, 2 * ld, 2 * stride, rows, cols, each};
+        bytes += copy_bytes(rows, cols);
+        return count++;
+    }
+    // that operand's copy, its rows' and its experts' strides in elements
+    void use(int i, const void*& src, int64_t& ld, int64_t& stride) const
+    {
+        if (i < 0)
+            return;
+        src = at[i].dst;
+        ld = qse::padded_row(at[i].cols) / 2;
+        stride = at[i].each * ld;
+    }
+    hipError_t make(void* ws, const GroupArgs& g, hipStream_t stream)
+    {
+        char* next = (char*)ws;
+        for (int i = 0; i < count; ++i) {
+            at[i].dst = next;
+            next += copy_bytes(at[i].rows, at[i].cols);
+        }
+        return qse::launch_row_copies(at, count, g, stream);
+    }
+};
+
 // dx = dy w_e (contraction over n) and dw_e = dy^T x (over the rows).
 size_t backward_need(int64_t experts, int64_t m, int64_t n, int64_t k)
 {
@@ -189,6 +303,9 @@ int fwt_grouped_matmul_workspace(int dtype, int64_t experts, int64_t m, int64_t 
     GroupArgs g = groups(nullptr, experts, m);
     g.zero_rest = 1;
     *bytes = qse::grouped_workspace(sizes(m, n, k * size_of(dtype)), g, dtype, false);
+    const int64_t copies = is16(dtype) ? forward_copies(experts, m, n, k) : 0;
+    if (copies)
+        *bytes = aligned256(*bytes) + copies;
     return FWT_OK;
 }
 
@@ -236,6 +353,25 @@ int fwt_grouped_matmul(const void* x, int64_t ldx, const float* x_scales, const 
     const int rc = check_call(arrays, stream);
     if (rc != FWT_OK)
         return rc;
+    GroupArgs g = groups(ends, experts, m);
+    const int64_t room = need && !i8 ? forward_copies(experts, m, n, k) : 0;
+    if (room) {
+        int64_t none = 0, between = experts > 1 ? stride_w : 0;
+        const int lx = level_of(x, ldx, 0), lw = level_of(w, ldw, between);
+        Copies c;
+        const int ix = c.want(lx, m, k, 0, x, ldx, 0);
+        const int iw = c.want(lw, experts * n, k, n, w, ldw, between);
+        if (c.count && c.room &&
+            worth_copies(c.bytes, forward_cost(experts, m, n, k, 0),
+                         forward_cost(experts, m, n, k, larger(lx, lw)))) {
+            const hipError_t e = c.make((char*)ws + (need - room), g, stream);
+            if (e != hipSuccess)
+                return status(e);
+            c.use(ix, x, ldx, none);
+            c.use(iw, w, ldw, between);
+            stride_w = between;
+        }
+    }
     ProductArgs p = sizes(m, n, k * sz);
     p.a = x;
     p.lda = ldx * sz;
@@ -248,7 +384,6 @@ int fwt_grouped_matmul(const void* x, int64_t ldx, const float* x_scales, const 
     p.ctype = (int)ytype;
     p.may_split = need != 0;
     p.partial = ws;
-    GroupArgs g = groups(ends, experts, m);
     g.stride_b = experts > 1 ? stride_w * sz : 0;
     g.zero_rest = zero_rest != 0;
     return status(qse::launch_grouped(p, g, dtype, false, stream));
@@ -264,6 +399,8 @@ int fwt_grouped_matmul_backward_workspace(int64_t experts, int64_t m, int64_t n,
         too_many_weights(experts, n, k))
         return FWT_OK;                   // (no sums, or refused)
     *bytes = backward_need(experts, m, n, k);
+    if (const int64_t copies = backward_copies(experts, m, n, k))
+        *bytes = aligned256(*bytes) + copies;
     return FWT_OK;
 }
 
@@ -312,6 +449,30 @@ int fwt_grouped_matmul_backward(const void* x, int64_t ldx, const void* w, int64
         return rc;
     GroupArgs g = groups(ends, experts, m);
     hipError_t e = hipSuccess;
+    const int64_t room = need && sums ? backward_copies(experts, m, n, k) : 0;
+    if (room) {
+        int64_t none = 0, between = experts > 1 ? stride_w : 0;
+        const int lx = weights ? level_of(x, ldx, 0) : 0;
+        const int lw = rows ? level_of(w, ldw, between) : 0;
+        const int ld = level_of(dy, lddy, 0);
+        Copies c;
+        const int id = c.want(ld, m, n, 0, dy, lddy, 0);
+        const int ix = c.want(lx, m, k, 0, x, ldx, 0);
+        const int iw = c.want(lw, experts * n, k, n, w, ldw, between);
+        const int to = rows ? 0 : -1, too = weights ? 0 : -1;
+        if (c.count && c.room &&
+            worth_copies(c.bytes, backward_cost(experts, m, n, k, to, too),
+                         backward_cost(experts, m, n, k, rows ? larger(ld, lw) : -1,
+                                       weights ? larger(ld, lx) : -1))) {
+            e = c.make((char*)ws + (need - room), g, stream);
+            if (e != hipSuccess)
+                return status(e);
+            c.use(id, dy, lddy, none);
+            c.use(ix, x, ldx, none);
+            c.use(iw, w, ldw, between);
+            stride_w = between;
+        }
+    }
     if (rows && !sums) {
         e = qse::launch_zero16(dx, lddx, m, k, stream);
     } else if (rows) {

@@ -535,25 +535,26 @@ bool any_address(const ProductArgs& p, const GroupArgs& g, uintptr_t mask)
              (uintptr_t)g.stride_b) & mask) != 0;
 }
 
+constexpr GroupTile kTilesAny[] = {{256, 256, 256, 1.9f, 11.f, 0, 2.5e6f},
+                                   {128, 128, 512, 1.2f, 7.f, 0, 2.7e6f},
+                                   {64, 128, 768, 1.4f, 6.f, 64 * 128, 3.8e6f},
+                                   {64, 128, 256, .68f, 6.f, 0, 3.8e6f}};
+constexpr GroupTile kTiles16[] = {{256, 256, 256, 1.45f, 9.f, 0},
+                                  {128, 128, 512, 1.06f, 6.f, 0},
+                                  {128, 128, 256, .62f, 5.f, 128 * 128},
+                                  {64, 128, 256, .42f, 4.f, 64 * 128}};
+// (multiples of four bytes)
+constexpr GroupTile kTilesFour[] = {{256, 256, 256, 1.85f, 11.f, 0, 3.7e6f},
+                                    {128, 128, 512, 1.1f, 7.f, 0, 4.6e6f},
+                                    {64, 128, 768, 1.3f, 6.f, 64 * 128, 5.0e6f},
+                                    {64, 128, 256, .62f, 6.f, 0, 5.0e6f}};
+
 template <int TYPE, bool BT>
 hipError_t grouped16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipStream_t stream)
 {
-    constexpr GroupTile any[] = {{256, 256, 256, 1.9f, 11.f, 0, 2.5e6f},
-                                 {128, 128, 512, 1.2f, 7.f, 0, 2.7e6f},
-                                 {64, 128, 768, 1.4f, 6.f, 64 * 128, 3.8e6f},
-                                 {64, 128, 256, .68f, 6.f, 0, 3.8e6f}};
-    constexpr GroupTile tiles[] = {{256, 256, 256, 1.45f, 9.f, 0},
-                                   {128, 128, 512, 1.06f, 6.f, 0},
-                                   {128, 128, 256, .62f, 5.f, 128 * 128},
-                                   {64, 128, 256, .42f, 4.f, 64 * 128}};
-    // (multiples of four bytes)
-    constexpr GroupTile fours[] = {{256, 256, 256, 1.85f, 11.f, 0, 3.7e6f},
-                                   {128, 128, 512, 1.1f, 7.f, 0, 4.6e6f},
-                                   {64, 128, 768, 1.3f, 6.f, 64 * 128, 5.0e6f},
-                                   {64, 128, 256, .62f, 6.f, 0, 5.0e6f}};
     double cost_odd, cost_four, cost_tile;
-    const Choice co = choose(any, p, g, cost_odd), cf = choose(fours, p, g, cost_four),
-                 c = choose(tiles, p, g, cost_tile);
+    const Choice co = choose(kTilesAny, p, g, cost_odd), cf = choose(kTilesFour, p, g, cost_four),
+                 c = choose(kTiles16, p, g, cost_tile);
     if (query) {
         *query = co.bytes > c.bytes ? co.bytes : c.bytes;
         *query = *query > cf.bytes ? *query : cf.bytes;
@@ -619,14 +620,15 @@ hipError_t grouped8(const ProductArgs& p, const GroupArgs& g, size_t* query, hip
 // Gradients of weights: an expert's tiles have its own rows as their steps; the
 // average's count, twice as many where they may be shared (the expert with the most
 // rows ends last).
-template <int TYPE>
-hipError_t grad16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipStream_t stream)
+constexpr GroupTile kGradAny[] = {{256, 256, 256, 1.9f, 11.f, 0},
+                                  {128, 128, 512, 1.2f, 7.f, 128 * 128}};
+constexpr GroupTile kGrad16[] = {{256, 256, 256, 1.6f, 9.f, 0},
+                                 {128, 128, 512, 1.06f, 6.f, 0},
+                                 {128, 128, 256, .62f, 5.f, 128 * 128}};
+template <int N>
+Choice choose_grad(const GroupTile (&tiles)[N], const ProductArgs& p, const GroupArgs& g,
+                   double& least)
 {
-    constexpr GroupTile any[] = {{256, 256, 256, 1.9f, 11.f, 0},
-                                 {128, 128, 512, 1.2f, 7.f, 128 * 128}};
-    constexpr GroupTile tiles[] = {{256, 256, 256, 1.6f, 9.f, 0},
-                                   {128, 128, 512, 1.06f, 6.f, 0},
-                                   {128, 128, 256, .62f, 5.f, 128 * 128}};
     const auto count = [&](const GroupTile& t, int64_t& most) {
         most = ((p.m + t.bm - 1) / t.bm) * ((p.n + t.bn - 1) / t.bn) * g.experts;
         return (double)most;
@@ -636,8 +638,14 @@ hipError_t grad16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipSt
     const int64_t few = (rows * 2 + kStep - 1) / kStep;
     const GroupCosts w{g.experts > 1 && p.may_split ? 2 * few : few, bytes,
                        p.may_split != 0, true};
+    return cheapest_grouped(tiles, w, count, least);
+}
+
+template <int TYPE>
+hipError_t grad16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipStream_t stream)
+{
     double cost;
-    const Choice ca = cheapest_grouped(any, w, count, cost), c = cheapest_grouped(tiles, w, count, cost);
+    const Choice ca = choose_grad(kGradAny, p, g, cost), c = choose_grad(kGrad16, p, g, cost);
     if (query) {
         *query = ca.bytes > c.bytes ? ca.bytes : c.bytes;
         return hipSuccess;
@@ -658,7 +666,105 @@ hipError_t grad16(const ProductArgs& p, const GroupArgs& g, size_t* query, hipSt
     return run_grad<TYPE, 128, 128, 2, 2, 1, 4>(p, g, c.splits, stream);
 }
 
+// Copies of operands in rows that are no multiples of 16 bytes (RowCopy): a wave for
+// every four rows at a time, a chunk of 16 bytes of each on a lane, so that short rows
+// have their loads in flight too (bf16 m 16000 e 8 n 4001 k 4095, both operands: 145 us,
+// 5.5 TB/s read and written).
+struct RowCopies {
+    RowCopy at[3];
+};
+__global__ __launch_bounds__(256) void row_copy_kernel(const RowCopies c, const GroupArgs g)
+{
+    constexpr int R = 4;
+    const RowCopy p = c.at[blockIdx.y];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane((int)threadIdx.x >> 6);
+    const int64_t len = p.cols * 2, ldd = (len + 15) & ~(int64_t)15;
+    const int each = (int)p.each;
+    int rows = (int)p.rows;
+    if (!each) {                         // up to the largest end
+        int most = 0;
+        for (int e = lane; e < g.experts; e += 64)
+            most = g.ends[e] > most ? g.ends[e] : most;
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+            const int o = __shfl_xor(most, d);
+            most = most > o ? most : o;
+        }
+        most = __builtin_amdgcn_readfirstlane(most);
+        rows = most < rows ? most : rows;
+    }
+    for (int row = ((int)blockIdx.x * 4 + wave) * R; row < rows; row += (int)gridDim.x * 4 * R) {
+        const char* src[R];
+        bool live[R];
+#pragma unroll
+        for (int i = 0; i < R; ++i) {
+            const int r = row + i < rows ? row + i : rows - 1;
+            live[i] = row + i < rows;
+            src[i] = (const char*)p.src + r * p.ld;
+            if (each) {
+                const int e = r / each;
+                int first;
+                live[i] = live[i] && rows_of(g, e, first) != 0;
+                src[i] = (const char*)p.src + e * p.stride + (r - e * each) * p.ld;
+            }
+        }
+        char* const dst = (char*)p.dst + row * ldd;
+        for (int64_t at = lane * 16; at < ldd; at += 1024) {
+            v4i v[R];
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (live[i])
+                    v[i] = load16_tail<kTBf16>(src[i], at, len);
+#pragma unroll
+            for (int i = 0; i < R; ++i)
+                if (live[i])
+                    *(v4i*)(dst + i * ldd + at) = v[i];
+        }
+    }
+}
+
 }  // namespace
+
+// A launch, and the bytes of the copies' writes, at the rate of both.
+constexpr double kCopyBytes = 2.7e6;
+double row_copies_cost(int64_t bytes) { return 4.0 + (double)bytes / kCopyBytes; }
+
+hipError_t launch_row_copies(const RowCopy* copies, int count, const GroupArgs& g,
+                             hipStream_t stream)
+{
+    RowCopies c{};
+    int64_t most = 0;
+    for (int i = 0; i < count; ++i) {
+        c.at[i] = copies[i];
+        most = copies[i].rows > most ? copies[i].rows : most;
+    }
+    const int64_t groups = (most + 15) / 16;
+    hipLaunchKernelGGL(row_copy_kernel,
+                       dim3((unsigned)(groups < 8 * kCus ? groups : 8 * kCus), (unsigned)count),
+                       dim3(256), 0, stream, c, g);
+    return hipGetLastError();
+}
+
+double grouped_cost(const ProductArgs& p, const GroupArgs& g, bool bt, int level)
+{
+    double cost;
+    (void)(level == 0   ? choose(kTiles16, p, g, cost)
+           : level == 1 ? choose(kTilesFour, p, g, cost)
+                        : choose(kTilesAny, p, g, cost));
+    if (bt)
+        return cost;
+    const double strips =
+        strips_cost(p, g, level == 0 ? kStrip16 : level == 1 ? kStrip4 : kStripOdd);
+    return strips < cost ? strips : cost;
+}
+
+double grouped_t_cost(const ProductArgs& p, const GroupArgs& g, int level)
+{
+    double cost;
+    (void)(level ? choose_grad(kGradAny, p, g, cost) : choose_grad(kGrad16, p, g, cost));
+    return cost;
+}
 
 hipError_t launch_grouped(const ProductArgs& p, const GroupArgs& g, int type, bool bt,
                           hipStream_t stream)

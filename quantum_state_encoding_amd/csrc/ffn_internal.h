@@ -108,6 +108,25 @@ hipError_t launch_grouped_t(const ProductArgs& p, const GroupArgs& g, int type,
 size_t grouped_workspace(ProductArgs p, const GroupArgs& g, int type, bool bt);
 size_t grouped_t_workspace(ProductArgs p, const GroupArgs& g, int type);
 
+// What these are expected to take, microseconds (16 bits): level 0 for operands whose
+// addresses and strides are multiples of 16 bytes, 1 of 4, 2 others.
+double grouped_cost(const ProductArgs& p, const GroupArgs& g, bool bt, int level);
+double grouped_t_cost(const ProductArgs& p, const GroupArgs& g, int level);
+
+// A copy of an operand of 16 bits in rows of padded_row bytes, zeros behind each.
+struct RowCopy {
+    const void* src;
+    void* dst;              // 16-byte aligned
+    int64_t ld, stride;     // bytes between src's rows, and its experts
+    int64_t rows, cols;     // rows of all
+    int64_t each;           // of an expert, 0: rows that the groups share
+};
+inline int64_t padded_row(int64_t cols) { return (cols * 2 + 15) & ~(int64_t)15; }
+// Experts without rows and rows of no expert are not read.
+hipError_t launch_row_copies(const RowCopy* copies, int count, const GroupArgs& g,
+                             hipStream_t stream);
+double row_copies_cost(int64_t bytes);
+
 // A product of 8-bit integers with a scale for each row of A and of B.
 hipError_t launch_int8(const ProductArgs& p, hipStream_t stream);
 size_t int8_workspace(ProductArgs p);

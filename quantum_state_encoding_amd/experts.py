@@ -215,7 +215,7 @@ def grouped_matmul(x, w, ends, x_scales=None, w_scales=None, out_dtype=None, out
             raise ValueError("the output has the operands' dtype")
     _no_graph("grouped_matmul", x, w, x_scales, w_scales, out)
     need = 0
-    if _ffn._may_share(m, n, k):
+    if _ffn._may_share(m, n, k) or (k % 8 and x.dtype is not _i8):
         size = ctypes.c_size_t(0)
         _ffn._raise(lib.fwt_grouped_matmul_workspace(_types[x.dtype], experts, m, n, k,
                                                      ctypes.byref(size)),

@@ -167,6 +167,135 @@ def test_many_experts(e, m):
     check_sums(dw, want, mag, max(counts), torch.float16)
 
 
+# sizes whose misaligned operands are copied into aligned rows first
+COPIED = [([3089, 0, 415], 100, 1019, 3373), ([2500, 2200, 1], 0, 1510, 1001),
+          ([1200] * 4, 7, 2001, 2004), ([4000], 333, 1999, 2000)]
+
+
+def copied_operands(case, dt):
+    counts, rest, n, k = COPIED[case]
+    g = gen(case)
+    m, e = sum(counts) + rest, len(counts)
+    x = torch.randn(m, k, generator=g, device="cuda").to(dt)
+    w = (torch.randn(e, n, k, generator=g, device="cuda") * k ** -0.5).to(dt)
+    dy = (torch.randn(m, n, generator=g, device="cuda") * 0.1).to(dt)
+    x[m - rest:] = float("nan")
+    dy[m - rest:] = float("nan")
+    for i, c in enumerate(counts):
+        if c == 0:
+            w[i] = float("nan")
+    return counts, rest, n, k, x, w, dy
+
+
+def check_copied(counts, rest, n, k, x, w, dy, y, dx, dw):
+    dt, used = x.dtype, x.shape[0] - rest
+    assert bool((y[used:] == 0).all()) and bool((dx[used:] == 0).all())
+    for i, lo, hi in group_bounds(counts):
+        if hi == lo:
+            assert bool((dw[i] == 0).all())
+            continue
+        a, b, gr = x[lo:hi].double(), w[i].double(), dy[lo:hi].double()
+        check_sums(y[lo:hi], a @ b.t(), a.abs() @ b.abs().t(), k, dt)
+        check_sums(dx[lo:hi], gr @ b, gr.abs() @ b.abs(), n, dt)
+        check_sums(dw[i], gr.t() @ a, gr.abs().t() @ a.abs(), hi - lo, dt)
+
+
+@pytest.mark.parametrize("case", range(len(COPIED)))
+@pytest.mark.parametrize("dtype", ["bf16", "f16"])
+@pytest.mark.parametrize("strided", [0, 1])
+def test_copied_operands(case, dtype, strided):
+    say("copied", case, dtype, strided)
+    counts, rest, n, k, x, w, dy = copied_operands(case, DT[dtype])
+    ends = ends_of(counts)
+
+    def lay(t):      # rows of an odd stride from an odd place, NaN around them
+        if not strided:
+            return t
+        big = torch.full(t.shape[:-1] + (t.shape[-1] + 3 + t.shape[-1] % 2,), float("nan"),
+                         dtype=t.dtype, device="cuda")
+        view = big[..., 1:1 + t.shape[-1]]
+        view.copy_(t)
+        return view
+
+    xs, ws, ds = lay(x), lay(w), lay(dy)
+    y = qse.grouped_matmul(xs, ws, ends)
+    dx, dw = qse.grouped_matmul_backward(xs, ws, ends, ds)
+    check_copied(counts, rest, n, k, x, w, dy, y, dx, dw)
+    assert torch.equal(qse.grouped_matmul(xs, ws, ends), y)
+    again = qse.grouped_matmul_backward(xs, ws, ends, ds)
+    assert torch.equal(again[0], dx) and torch.equal(again[1], dw)
+
+
+def test_copied_operands_scratch_and_parts():
+    # scratch of the size that is asked for holds the sums and the copies; dx or dw
+    # alone; no scratch
+    L = experts._load()
+    stream = torch.cuda.current_stream().cuda_stream
+    asked = 0
+    for case in range(len(COPIED)):
+        say("copied scratch", case)
+        counts, rest, n, k, x, w, dy = copied_operands(case, torch.bfloat16)
+        m, e, ends = x.shape[0], len(counts), ends_of(counts)
+        size = ctypes.c_size_t()
+        for parts in (3, 1, 2, 0):
+            assert L.fwt_grouped_matmul_workspace(0, e, m, n, k, ctypes.byref(size)) == 0
+            need = size.value
+            assert L.fwt_grouped_matmul_backward_workspace(e, m, n, k, ctypes.byref(size)) == 0
+            need = max(need, size.value)
+            asked = max(asked, need)
+            ws = torch.full((need + 4096,), 0x5a, dtype=torch.uint8, device="cuda")
+            at, room = (ws.data_ptr(), need) if parts else (None, 0)
+            y = torch.empty(m, n, dtype=x.dtype, device="cuda")
+            dx, dw = torch.full_like(x, 3.0), torch.full_like(w, 3.0)
+            assert L.fwt_grouped_matmul(x.data_ptr(), k, None, w.data_ptr(), k, n * k, None,
+                                        ends.data_ptr(), e, 0, m, n, k, y.data_ptr(), 0, n, 1,
+                                        at, room, stream) == 0
+            for which in ((3,) if parts in (0, 3) else (parts, 3 - parts)):
+                assert L.fwt_grouped_matmul_backward(
+                    x.data_ptr(), k, w.data_ptr(), k, n * k, ends.data_ptr(), e, dy.data_ptr(),
+                    n, 0, m, n, k, dx.data_ptr() if which & 1 else None, k,
+                    dw.data_ptr() if which & 2 else None, k, n * k, at, room, stream) == 0
+            check_copied(counts, rest, n, k, x, w, dy, y, dx, dw)
+            assert bool((ws[need:] == 0x5a).all())
+    assert asked > 16 << 20          # (copies are among them)
+
+
+def test_copied_operands_that_begin_at_one_place():
+    # x and grad are views of one buffer, of different widths
+    say("copied, one place")
+    counts, rest, n, k, _, w, _ = copied_operands(1, torch.bfloat16)
+    big = torch.randn(sum(counts), 1511, generator=gen(9), device="cuda").bfloat16()
+    x, dy = big[:, :k], big[:, :n]
+    y = qse.grouped_matmul(x, w, ends_of(counts))
+    dx, dw = qse.grouped_matmul_backward(x, w, ends_of(counts), dy)
+    check_copied(counts, rest, n, k, x, w, dy, y, dx, dw)
+
+
+def test_copied_operands_replayed():
+    say("copied, replayed")
+    counts, rest, n, k, x, w, dy = copied_operands(2, torch.float16)
+    x[sum(counts):], dy[sum(counts):] = 1.0, 1.0
+    ends = ends_of(counts)
+    call = lambda: ((qse.grouped_matmul(x, w, ends),)                     # noqa: E731
+                    + qse.grouped_matmul_backward(x, w, ends, dy))
+    call()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = call()
+    for turn in range(4):
+        x.copy_(torch.randn(x.shape, generator=gen(turn), device="cuda"))
+        new = ends_of([[1200, 1200, 1200, 1200], [0, 4000, 10, 0], [4807, 0, 0, 0],
+                       [1, 1, 1, 1]][turn])
+        ends.copy_(new)
+        graph.replay()
+        torch.cuda.synchronize()
+        want = call()
+        torch.cuda.synchronize()
+        for a, b in zip(got, want):
+            assert torch.equal(a, b)
+
+
 def test_falling_ends_of_very_many_experts():
     # every second of 2^16 experts claims all rows: 2^15 times 2^16 tiles of 128 x 128
     # and more, which 32 bits do not hold.  The rows are unspecified; nothing around
