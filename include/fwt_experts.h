@@ -16,10 +16,10 @@
  * has the rows from ends[e - 1] (from 0 for the first) up to ends[e], so equal
  * numbers are an expert without rows.  The device reads them when the call
  * runs; the host does not wait for them.  They are 0 .. m and do not fall;
- * numbers outside 0 .. m are cut to it, and where they fall the results of the
- * rows that they contradict each other about are unspecified (nothing outside the
- * arrays is read or written).  Rows from ends[experts - 1] on belong to no
- * expert: they are not read.
+ * numbers outside 0 .. m are cut to it.  Rows from ends[experts - 1] on belong to
+ * no expert: they are not read.  Where ends fall, the results of rows that two
+ * experts claim, or an expert and the rows of none, are unspecified, and dw of those
+ * experts (nothing outside the arrays is read or written); all others hold.
  *
  * Conventions are fwt_ffn.h's: status codes, device buffers that the caller
  * owns, all arguments checked on the host before anything is enqueued, nothing

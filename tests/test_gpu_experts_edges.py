@@ -319,6 +319,97 @@ def test_falling_ends_of_very_many_experts():
     assert bool((y == k).all())
 
 
+def falling_ends(m, kind):
+    """Ends that fall, and for each row the experts that claim it."""
+    half = m // 2
+    if kind == "last":          # the rows of the second half are the last expert's alone
+        ends = [half, 0] * 40 + [half, m]
+    elif kind == "none":        # ... are no expert's
+        ends = [half, 0] * 40
+    elif kind == "middle":      # a part is a middle expert's alone, of the second 64
+        ends = [half - 5, 0] * 45 + [half - 5, half + 7] + [half + 7] * 3 + [m, half + 9] * 3 + [m]
+    else:
+        g = torch.Generator()
+        g.manual_seed(kind)
+        ends = (torch.randint(-m // 8, m * 9 // 8, (7 + 30 * kind,), generator=g)).tolist()
+        ends[3:3] = [m // 3] * 2
+    cut = [0] + [min(max(v, 0), m) for v in ends]
+    claims = [[] for _ in range(m)]
+    for e, (lo, hi) in enumerate(zip(cut, cut[1:])):
+        for r in range(lo, hi):
+            claims[r].append(e)
+    return ends, claims, cut[-1]
+
+
+@pytest.mark.parametrize("m,n,k", [(40, 64, 64), (300, 200, 512), (1000, 200, 60), (2000, 1000, 61),
+                                   (4096, 2048, 64), (300, 130, 4096)])
+@pytest.mark.parametrize("kind", ["last", "none", "middle", 1, 2, 3])
+@pytest.mark.parametrize("dtype", ["bf16", "int8"])
+def test_falling_ends_leave_the_other_rows(m, n, k, kind, dtype):
+    # rows that one expert alone claims are that expert's, rows that none does are
+    # zeros, however often the other ends fall.  Small integers: sums are exact.
+    if dtype == "int8" and k % 16:
+        k = cdiv(k, 16) * 16
+    say("falling ends, other rows", m, n, k, kind, dtype)
+    L = experts._load()
+    g = gen(n)
+    stream = torch.cuda.current_stream().cuda_stream
+    ends, claims, last = falling_ends(m, kind)
+    e = len(ends)
+    one = [r for r in range(m) if len(claims[r]) == 1 and r < last]
+    none = [r for r in range(m) if not claims[r]]
+    assert one or none or isinstance(kind, int)
+    sparse = lambda *shape: (torch.rand(*shape, generator=g, device="cuda") < 32 / shape[-1]).float() \
+        * torch.randint(-1, 2, shape, generator=g, device="cuda")                    # noqa: E731
+    dt = torch.int8 if dtype == "int8" else torch.bfloat16
+    x, w, dy = sparse(m, k), sparse(e, n, k), sparse(m, n)
+    dev = torch.tensor(ends, dtype=torch.int32, device="cuda")
+    rows = torch.tensor(one, dtype=torch.int64, device="cuda")
+    whose = torch.tensor([claims[r][0] for r in one], dtype=torch.int64, device="cuda")
+    empty = torch.tensor(none, dtype=torch.int64, device="cuda")
+    x8, w8 = x.to(dt), w.to(dt)
+    sx, sw = torch.ones(m, device="cuda"), torch.ones(e, n, device="cuda")
+    y = torch.full((m, n), float("nan"), dtype=torch.bfloat16, device="cuda")
+    assert L.fwt_grouped_matmul(
+        x8.data_ptr(), k, sx.data_ptr() if dtype == "int8" else None, w8.data_ptr(), k, n * k,
+        sw.data_ptr() if dtype == "int8" else None, dev.data_ptr(), e, 5 if dtype == "int8" else 0,
+        m, n, k, y.data_ptr(), 0, n, 1, None, 0, stream) == 0
+
+    def check(got, a, b):
+        assert bool((got[empty] == 0).all())
+        for i in whose.unique().tolist():
+            mine = rows[whose == i]
+            assert torch.equal(got[mine].float(), a[mine] @ b(i))
+        assert not bool(torch.isnan(got.float()).any())       # every row is written
+
+    check(y, x, lambda i: w[i].t().contiguous())
+    if dtype == "int8":
+        return
+    dx = torch.full((m, k), float("nan"), dtype=torch.bfloat16, device="cuda")
+    d8 = dy.to(dt)
+    dw = torch.full((e, n, k), float("nan"), dtype=torch.bfloat16, device="cuda")
+    assert L.fwt_grouped_matmul_backward(
+        x8.data_ptr(), k, w8.data_ptr(), k, n * k, dev.data_ptr(), e, d8.data_ptr(), n, 0, m, n, k,
+        dx.data_ptr(), k, dw.data_ptr(), k, n * k, None, 0, stream) == 0
+    check(dx, dy, lambda i: w[i])
+    assert not bool(torch.isnan(dw.float()).any())
+
+
+def test_falling_ends_with_copied_operands():
+    # the last expert's rows are its own, in sizes whose operands are copied first
+    say("falling ends, copied")
+    counts, rest, n, k, x, w, dy = copied_operands(0, torch.bfloat16)
+    used = sum(counts)
+    ends = torch.tensor([1500, 0, used], dtype=torch.int32, device="cuda")
+    y = qse.grouped_matmul(x, w, ends)
+    dx, dw = qse.grouped_matmul_backward(x, w, ends, dy)
+    assert bool((y[used:] == 0).all()) and bool((dx[used:] == 0).all())
+    a, b, gr = x[1500:used].double(), w[2].double(), dy[1500:used].double()
+    check_sums(y[1500:used], a @ b.t(), a.abs() @ b.abs().t(), k, torch.bfloat16)
+    check_sums(dx[1500:used], gr @ b, gr.abs() @ b.abs(), n, torch.bfloat16)
+    assert bool(torch.isfinite(y.float()).all()) and bool(torch.isfinite(dx.float()).all())
+
+
 @pytest.mark.parametrize("counts,n", [
     # whole rounds of 256 tiles and a few more, which two workgroups share each:
     # of more and of fewer than half a tile's rows, with rows of no expert
