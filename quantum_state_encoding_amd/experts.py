@@ -6,9 +6,10 @@ integers (a scale for each row), the product of two such operands, and the
 products of rows that are sorted by expert, with their gradients.  Arguments,
 streams and scratch are as in ``ffn``: outputs are torch allocations on the
 call's stream, nothing waits, the operands' memory is kept until a given stream
-has passed the call, and in grad mode operands that require gradients are
-refused, since the calls record no graph (grouped_matmul_backward takes them;
-its results are not differentiable themselves).
+has passed the call, and operands with a forward-mode tangent are refused, and in
+grad mode those that require gradients, since the calls record no graph
+(grouped_matmul_backward takes both; its results are not differentiable
+themselves).
 
 Example (the down projection of a served model's experts, 8-bit)::
 
@@ -109,6 +110,7 @@ def _check_ends(ends, dev, experts):
 
 
 def _no_graph(what, *tensors):
+    _ffn._no_tangents(what, tensors)
     if _ffn._grad_mode():
         for t in tensors:
             if t is not None and t.requires_grad:

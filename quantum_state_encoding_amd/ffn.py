@@ -6,9 +6,9 @@ the rest of the package they only marshal arguments; outputs and scratch are
 torch allocations on the call's stream.  ``stream`` (the current one by
 default) is one of the current device; it is not made to wait for the operands,
 nor another stream for the results, but the operands' memory is kept until it
-has passed the call.  The calls record nothing for autograd: in
-grad mode operands that require gradients are refused (gated_ffn_backward takes
-them; its results are not differentiable themselves).
+has passed the call.  The calls record nothing for autograd: operands with a
+forward-mode tangent are refused, and in grad mode those that require gradients
+(gated_ffn_backward takes both; its results are not differentiable themselves).
 
 Example (one feed-forward block of a served model; weights prepared once)::
 
@@ -39,11 +39,13 @@ _ACTS = {"silu": 0, "gelu": 1}
 _lib = None
 # of torch, set by _load
 _types = _f32 = _f8 = _floats = _halves = _gated = _raw_stream = _device = _grad_mode = None
+_forward = None           # torch.autograd.forward_ad
 _here = contextlib.nullcontext()
 
 
 def _load():
     global _lib, _types, _f32, _f8, _floats, _halves, _gated, _raw_stream, _device, _grad_mode
+    global _forward
     if _lib is None:
         import torch
         lib = _qse.load_library()
@@ -68,7 +70,7 @@ def _load():
         _halves = (torch.bfloat16, torch.float16)
         _floats, _gated = _halves + (_f32,), _halves + (_f8,)
         _raw_stream = torch._C._cuda_getCurrentRawStream   # the handle alone: no Stream object
-        _grad_mode = torch.is_grad_enabled
+        _grad_mode, _forward = torch.is_grad_enabled, torch.autograd.forward_ad
         _lib = lib
     return _lib
 
@@ -139,9 +141,20 @@ def _out_dtype(out_dtype, out):
     return dtype
 
 
+def _no_tangents(what, tensors):
+    """Refuses operands with a tangent, in any grad mode: the results would have
+    none."""
+    # (outside a level, asking each tensor would take 0.4 us)
+    if getattr(_forward, "_current_level", 0) >= 0:
+        for t in tensors:
+            if t is not None and _forward.unpack_dual(t).tangent is not None:
+                raise ValueError("%s hands no tangents on: call it with detached tensors" % what)
+
+
 def _no_graph(what, *tensors):
     """Refuses operands whose gradients would be lost: the calls record
     nothing for autograd."""
+    _no_tangents(what, tensors)
     if _grad_mode():
         for t in tensors:
             if t is not None and t.requires_grad:

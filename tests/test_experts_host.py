@@ -191,3 +191,18 @@ def test_host_tensors_are_refused(L):
             qse.rotate_quantize_int8(x, bits=bits)
     with pytest.raises(TypeError):
         qse.rotate_quantize_int8(x, bits=2.5)
+
+
+def test_tangents_are_not_dropped(L):
+    import torch
+    from torch.autograd import forward_ad
+    from quantum_state_encoding_amd import ffn
+    x = torch.zeros(4, 8)
+    for check in (ffn._no_graph, experts._no_graph):
+        with forward_ad.dual_level():
+            dual = forward_ad.make_dual(x, torch.ones(4, 8))
+            for mode in (torch.enable_grad(), torch.no_grad()):     # (both keep tangents)
+                with mode, pytest.raises(ValueError, match="tangent"):
+                    check("call", x, None, dual)
+            check("call", x, None, dual.detach())
+        check("call", x, None)

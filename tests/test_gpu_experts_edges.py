@@ -579,6 +579,31 @@ def test_outputs_count_as_written():
     assert out._version > before
 
 
+def test_operands_with_tangents_are_refused():
+    say("tangents")
+    from torch.autograd import forward_ad
+    x = torch.zeros(4, 16, dtype=torch.bfloat16, device="cuda")
+    w = torch.zeros(1, 8, 16, dtype=torch.bfloat16, device="cuda")
+    q, s, ws = x.to(torch.int8), torch.ones(4, device="cuda"), torch.ones(1, 8, device="cuda")
+    ends = ends_of([4])
+    wq, e4, es = w.to(torch.int8), x.to(torch.float8_e4m3fn), torch.ones(1, 4, device="cuda")
+    with forward_ad.dual_level():
+        dual = lambda t: forward_ad.make_dual(t, torch.ones_like(t))               # noqa: E731
+        for call in (lambda: qse.rotate_quantize_int8(dual(x)), lambda: qse.rotate_quantize(dual(x)),
+                     lambda: qse.grouped_matmul(dual(x), w, ends),
+                     lambda: qse.grouped_matmul(x, dual(w), ends),
+                     lambda: qse.grouped_matmul(x, w, ends, out=dual(x[:, :8].clone())),
+                     lambda: qse.grouped_matmul(q, wq, ends, x_scales=dual(s), w_scales=ws),
+                     lambda: qse.int8_matmul(q, dual(s), q, s),
+                     lambda: qse.scaled_matmul(e4, dual(es), e4, es),
+                     lambda: qse.gated_ffn(x, dual(w[0]), w[0])):
+            with pytest.raises(ValueError, match="tangent"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="tangent"):
+                call()
+        qse.grouped_matmul(dual(x).detach(), w, ends)
+
+
 def test_workspaces_are_enough_for_every_number_of_groups():
     # the scratch that is asked for holds the sums whatever zero_rest is: what
     # lies behind it stays as it was
