@@ -93,18 +93,24 @@ int fwt_int8_matmul(const void* a, int64_t lda, const float* a_scales, const voi
  *              strides 16-byte aligned, row strides below 2^23.
  *  zero_rest   the rows of y that belong to no expert: 0 leaves them as they
  *              were, otherwise they become 0.
- *  ws          scratch of fwt_grouped_matmul_workspace bytes (0 for most
+ *  ws          scratch of fwt_grouped_matmul_workspace_for bytes (0 for most
  *              sizes), as for fwt_int8_matmul, and for copies of 16-bit operands
- *              (up to 1 GiB) where k is no multiple of 8 and a large call on
- *              aligned rows takes less time with the copying.  NULL: nothing is
- *              shared or copied, which takes longer and may add fp32 sums in
- *              another order.
+ *              that are misaligned (up to 1 GiB) where k is no multiple of 8 and a
+ *              large call on aligned rows takes less time with the copying.  NULL:
+ *              nothing is shared or copied, which takes longer and may add fp32 sums
+ *              in another order.
+ *              fwt_grouped_matmul_workspace: enough for any operands of the sizes;
+ *              .._for: of x and w, of which the addresses and strides count and
+ *              nothing is read.
  * Which kernel runs, and so the order of fp32 sums, goes by the sizes, the
  * addresses' alignment and ws, not by where the groups end.
  * More than 2^22 tiles of 128 x 64 results (every expert may have one row of
  * tiles that is not whole), or more than 2^16 experts, are FWT_EUNSUPPORTED. */
 int fwt_grouped_matmul_workspace(int dtype, int64_t experts, int64_t m, int64_t n, int64_t k,
                                  size_t* bytes);
+int fwt_grouped_matmul_workspace_for(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                     int64_t stride_w, int64_t experts, int dtype, int64_t m,
+                                     int64_t n, int64_t k, size_t* bytes);
 int fwt_grouped_matmul(const void* x, int64_t ldx, const float* x_scales, const void* w,
                        int64_t ldw, int64_t stride_w, const float* w_scales,
                        const int32_t* ends, int64_t experts, int dtype, int64_t m, int64_t n,
@@ -117,10 +123,14 @@ int fwt_grouped_matmul(const void* x, int64_t ldx, const float* x_scales, const 
  * dx m x k, dw experts x n x k (lddw between rows, stride_dw between experts).
  * Sums are in fp32 and only the results are rounded.  All arrays have the dtype,
  * any alignment, row strides below 2^22.  dx or dw may be NULL: that gradient is
- * not computed.  ws: scratch of fwt_grouped_matmul_backward_workspace bytes, as
- * above. */
+ * not computed.  ws: scratch of fwt_grouped_matmul_backward_workspace_for bytes
+ * (dx, dw: not 0 for a gradient that is wanted), or of .._workspace, as above. */
 int fwt_grouped_matmul_backward_workspace(int64_t experts, int64_t m, int64_t n, int64_t k,
                                           size_t* bytes);
+int fwt_grouped_matmul_backward_workspace_for(const void* x, int64_t ldx, const void* w,
+                                              int64_t ldw, int64_t stride_w, int64_t experts,
+                                              const void* dy, int64_t lddy, int64_t m, int64_t n,
+                                              int64_t k, int dx, int dw, size_t* bytes);
 int fwt_grouped_matmul_backward(const void* x, int64_t ldx, const void* w, int64_t ldw,
                                 int64_t stride_w, const int32_t* ends, int64_t experts,
                                 const void* dy, int64_t lddy, fwt_ffn_dtype dtype, int64_t m,

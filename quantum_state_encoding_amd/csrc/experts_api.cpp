@@ -87,16 +87,19 @@ bool may_copy(int64_t cols) { return cols >= kMinCopied && cols < kMaxCopied; }
 
 size_t aligned256(size_t n) { return (n + 255) & ~(size_t)255; }
 
-// Bytes of a copy, 0 for rows that need none.
+// Bytes of a copy, 0 for rows that need none, more than kMaxCopies for any more than that.
 int64_t copy_bytes(int64_t rows, int64_t cols)
 {
-    return cols % 8 == 0 ? 0 : rows * qse::padded_row(cols);
+    if (cols % 8 == 0)
+        return 0;
+    const int64_t row = qse::padded_row(cols);
+    return rows > kMaxCopies / row ? kMaxCopies + 1 : rows * row;
 }
 
 // How an operand lies: 0 at multiples of 16 bytes, 1 of 4, 2 others.
 int level_of(const void* p, int64_t ld, int64_t stride)
 {
-    const uintptr_t a = (uintptr_t)p | (uintptr_t)(2 * ld) | (uintptr_t)(2 * stride);
+    const uintptr_t a = (uintptr_t)p | 2 * (uintptr_t)ld | 2 * (uintptr_t)stride;
     return (a & 15) == 0 ? 0 : (a & 3) == 0 ? 1 : 2;
 }
 
@@ -159,14 +162,20 @@ struct Copies {
         if (level == 0)
             return -1;
         room = room && copy_bytes(rows, cols);
-        at[count] = qse::RowCopy{src, nullptr, 2 * ld, 2 * stride, rows, cols, each};
+        at[count] = qse::RowCopy{src,  nullptr, (int64_t)(2 * (uint64_t)ld), (int64_t)(2 * (uint64_t)stride),
+                                 rows, cols,    each};
         bytes += copy_bytes(rows, cols);
         return count++;
+    }
+    void none()
+    {
+        count = 0;
+        bytes = 0;
     }
     // that operand's copy, its rows' and its experts' strides in elements
     void use(int i, const void*& src, int64_t& ld, int64_t& stride) const
     {
-        if (i < 0)
+        if (i < 0 || !count)
             return;
         src = at[i].dst;
         ld = qse::padded_row(at[i].cols) / 2;
@@ -183,6 +192,60 @@ struct Copies {
     }
 };
 
+// What of these operands is copied, if anything; stride_w 0 for one expert.
+struct ForwardCopies : Copies {
+    int x, w;
+    ForwardCopies(const void* px, int64_t ldx, const void* pw, int64_t ldw, int64_t stride_w,
+                  int64_t experts, int64_t m, int64_t n, int64_t k)
+    {
+        const int lx = level_of(px, ldx, 0), lw = level_of(pw, ldw, stride_w);
+        x = want(lx, m, k, 0, px, ldx, 0);
+        w = want(lw, experts * n, k, n, pw, ldw, stride_w);
+        if (!count || !room || !forward_copies(experts, m, n, k) ||
+            !worth_copies(bytes, forward_cost(experts, m, n, k, 0),
+                          forward_cost(experts, m, n, k, larger(lx, lw))))
+            none();
+    }
+};
+struct BackwardCopies : Copies {
+    int dy, x, w;
+    BackwardCopies(const void* px, int64_t ldx, const void* pw, int64_t ldw, int64_t stride_w,
+                   const void* pdy, int64_t lddy, int64_t experts, int64_t m, int64_t n, int64_t k,
+                   bool rows, bool weights)
+    {
+        const int lx = weights ? level_of(px, ldx, 0) : 0;
+        const int lw = rows ? level_of(pw, ldw, stride_w) : 0;
+        const int ld = level_of(pdy, lddy, 0);
+        dy = want(ld, m, n, 0, pdy, lddy, 0);
+        x = want(lx, m, k, 0, px, ldx, 0);
+        w = want(lw, experts * n, k, n, pw, ldw, stride_w);
+        if (!count || !room || !backward_copies(experts, m, n, k) ||
+            !worth_copies(bytes,
+                          backward_cost(experts, m, n, k, rows ? 0 : -1, weights ? 0 : -1),
+                          backward_cost(experts, m, n, k, rows ? larger(ld, lw) : -1,
+                                        weights ? larger(ld, lx) : -1)))
+            none();
+    }
+};
+
+// Scratch: the sums, then the copies.
+size_t with_copies(size_t sums, int64_t copies)
+{
+    return copies ? aligned256(sums) + copies : sums;
+}
+
+// Sums of the forward call; whether there is work that is not refused.
+bool forward_runs(int64_t experts, int64_t m, int64_t n)
+{
+    return m != 0 && n != 0 && experts <= kMaxExperts && !too_many_grouped(m, n, experts + 1);
+}
+size_t forward_need(int dtype, int64_t experts, int64_t m, int64_t n, int64_t k)
+{
+    GroupArgs g = groups(nullptr, experts, m);
+    g.zero_rest = 1;
+    return qse::grouped_workspace(sizes(m, n, k * size_of(dtype)), g, dtype, false);
+}
+
 // dx = dy w_e (contraction over n) and dw_e = dy^T x (over the rows).
 size_t backward_need(int64_t experts, int64_t m, int64_t n, int64_t k)
 {
@@ -191,6 +254,11 @@ size_t backward_need(int64_t experts, int64_t m, int64_t n, int64_t k)
     g.zero_rest = 1;
     const size_t dx = qse::grouped_workspace(sizes(m, k, 2 * n), g, FWT_BF16, true);
     return dx > dw ? dx : dw;
+}
+bool backward_runs(int64_t experts, int64_t m, int64_t n, int64_t k)
+{
+    return m != 0 && n != 0 && experts <= kMaxExperts && !too_many_grouped(m, k, experts + 1) &&
+           !too_many_weights(experts, n, k);
 }
 
 }  // namespace
@@ -298,14 +366,27 @@ int fwt_grouped_matmul_workspace(int dtype, int64_t experts, int64_t m, int64_t 
         (!is16(dtype) && dtype != FWT_INT8))
         return FWT_EINVAL;
     *bytes = 0;
-    if (m == 0 || n == 0 || experts > kMaxExperts || too_many_grouped(m, n, experts + 1))
-        return FWT_OK;                   // (no work, or refused)
-    GroupArgs g = groups(nullptr, experts, m);
-    g.zero_rest = 1;
-    *bytes = qse::grouped_workspace(sizes(m, n, k * size_of(dtype)), g, dtype, false);
-    const int64_t copies = is16(dtype) ? forward_copies(experts, m, n, k) : 0;
-    if (copies)
-        *bytes = aligned256(*bytes) + copies;
+    if (forward_runs(experts, m, n))
+        *bytes = with_copies(forward_need(dtype, experts, m, n, k),
+                             is16(dtype) ? forward_copies(experts, m, n, k) : 0);
+    return FWT_OK;
+}
+
+int fwt_grouped_matmul_workspace_for(const void* x, int64_t ldx, const void* w, int64_t ldw,
+                                     int64_t stride_w, int64_t experts, int dtype, int64_t m,
+                                     int64_t n, int64_t k, size_t* bytes)
+{
+    if (!bytes || !dims_ok(m, n, k) || experts < 1 ||
+        (!is16(dtype) && dtype != FWT_INT8))
+        return FWT_EINVAL;
+    *bytes = 0;
+    if (!forward_runs(experts, m, n))
+        return FWT_OK;
+    *bytes = forward_need(dtype, experts, m, n, k);
+    if (is16(dtype))
+        *bytes = with_copies(*bytes, ForwardCopies(x, ldx, w, ldw, experts > 1 ? stride_w : 0,
+                                                   experts, m, n, k)
+                                         .bytes);
     return FWT_OK;
 }
 
@@ -316,7 +397,8 @@ int fwt_grouped_matmul(const void* x, int64_t ldx, const float* x_scales, const 
                        void* ws, size_t ws_bytes, hipStream_t stream)
 {
     size_t need = 0;
-    const int rc0 = fwt_grouped_matmul_workspace(dtype, experts, m, n, k, &need);
+    const int rc0 = fwt_grouped_matmul_workspace_for(x, ldx, w, ldw, stride_w, experts, dtype, m, n,
+                                                     k, &need);
     if (rc0 != FWT_OK)
         return rc0;
     const bool i8 = dtype == FWT_INT8;
@@ -354,21 +436,15 @@ int fwt_grouped_matmul(const void* x, int64_t ldx, const float* x_scales, const 
     if (rc != FWT_OK)
         return rc;
     GroupArgs g = groups(ends, experts, m);
-    const int64_t room = need && !i8 ? forward_copies(experts, m, n, k) : 0;
-    if (room) {
+    if (need && !i8) {
         int64_t none = 0, between = experts > 1 ? stride_w : 0;
-        const int lx = level_of(x, ldx, 0), lw = level_of(w, ldw, between);
-        Copies c;
-        const int ix = c.want(lx, m, k, 0, x, ldx, 0);
-        const int iw = c.want(lw, experts * n, k, n, w, ldw, between);
-        if (c.count && c.room &&
-            worth_copies(c.bytes, forward_cost(experts, m, n, k, 0),
-                         forward_cost(experts, m, n, k, larger(lx, lw)))) {
-            const hipError_t e = c.make((char*)ws + (need - room), g, stream);
+        ForwardCopies c(x, ldx, w, ldw, between, experts, m, n, k);
+        if (c.count) {
+            const hipError_t e = c.make((char*)ws + (need - c.bytes), g, stream);
             if (e != hipSuccess)
                 return status(e);
-            c.use(ix, x, ldx, none);
-            c.use(iw, w, ldw, between);
+            c.use(c.x, x, ldx, none);
+            c.use(c.w, w, ldw, between);
             stride_w = between;
         }
     }
@@ -395,12 +471,24 @@ int fwt_grouped_matmul_backward_workspace(int64_t experts, int64_t m, int64_t n,
     if (!bytes || !dims_ok(m, n, k) || experts < 1)
         return FWT_EINVAL;
     *bytes = 0;
-    if (m == 0 || n == 0 || experts > kMaxExperts || too_many_grouped(m, k, experts + 1) ||
-        too_many_weights(experts, n, k))
-        return FWT_OK;                   // (no sums, or refused)
-    *bytes = backward_need(experts, m, n, k);
-    if (const int64_t copies = backward_copies(experts, m, n, k))
-        *bytes = aligned256(*bytes) + copies;
+    if (backward_runs(experts, m, n, k))
+        *bytes = with_copies(backward_need(experts, m, n, k), backward_copies(experts, m, n, k));
+    return FWT_OK;
+}
+
+int fwt_grouped_matmul_backward_workspace_for(const void* x, int64_t ldx, const void* w,
+                                              int64_t ldw, int64_t stride_w, int64_t experts,
+                                              const void* dy, int64_t lddy, int64_t m, int64_t n,
+                                              int64_t k, int dx, int dw, size_t* bytes)
+{
+    if (!bytes || !dims_ok(m, n, k) || experts < 1)
+        return FWT_EINVAL;
+    *bytes = 0;
+    if (backward_runs(experts, m, n, k) && (dx || dw))
+        *bytes = with_copies(backward_need(experts, m, n, k),
+                             BackwardCopies(x, ldx, w, ldw, experts > 1 ? stride_w : 0, dy, lddy,
+                                            experts, m, n, k, dx != 0, dw != 0)
+                                 .bytes);
     return FWT_OK;
 }
 
@@ -412,7 +500,8 @@ int fwt_grouped_matmul_backward(const void* x, int64_t ldx, const void* w, int64
                                 hipStream_t stream)
 {
     size_t need = 0;
-    const int rc0 = fwt_grouped_matmul_backward_workspace(experts, m, n, k, &need);
+    const int rc0 = fwt_grouped_matmul_backward_workspace_for(
+        x, ldx, w, ldw, stride_w, experts, dy, lddy, m, n, k, dx != nullptr, dw != nullptr, &need);
     if (rc0 != FWT_OK)
         return rc0;
     if (!is16(dtype))
@@ -449,27 +538,16 @@ int fwt_grouped_matmul_backward(const void* x, int64_t ldx, const void* w, int64
         return rc;
     GroupArgs g = groups(ends, experts, m);
     hipError_t e = hipSuccess;
-    const int64_t room = need && sums ? backward_copies(experts, m, n, k) : 0;
-    if (room) {
+    if (need && sums) {
         int64_t none = 0, between = experts > 1 ? stride_w : 0;
-        const int lx = weights ? level_of(x, ldx, 0) : 0;
-        const int lw = rows ? level_of(w, ldw, between) : 0;
-        const int ld = level_of(dy, lddy, 0);
-        Copies c;
-        const int id = c.want(ld, m, n, 0, dy, lddy, 0);
-        const int ix = c.want(lx, m, k, 0, x, ldx, 0);
-        const int iw = c.want(lw, experts * n, k, n, w, ldw, between);
-        const int to = rows ? 0 : -1, too = weights ? 0 : -1;
-        if (c.count && c.room &&
-            worth_copies(c.bytes, backward_cost(experts, m, n, k, to, too),
-                         backward_cost(experts, m, n, k, rows ? larger(ld, lw) : -1,
-                                       weights ? larger(ld, lx) : -1))) {
-            e = c.make((char*)ws + (need - room), g, stream);
+        BackwardCopies c(x, ldx, w, ldw, between, dy, lddy, experts, m, n, k, rows, weights);
+        if (c.count) {
+            e = c.make((char*)ws + (need - c.bytes), g, stream);
             if (e != hipSuccess)
                 return status(e);
-            c.use(id, dy, lddy, none);
-            c.use(ix, x, ldx, none);
-            c.use(iw, w, ldw, between);
+            c.use(c.dy, dy, lddy, none);
+            c.use(c.x, x, ldx, none);
+            c.use(c.w, w, ldw, between);
             stride_w = between;
         }
     }

@@ -32,8 +32,9 @@ INT8 = 5                  # FWT_INT8
 
 # Every symbol include/fwt_experts.h declares.
 EXPERTS_SYMBOLS = ("fwt_rotate_quantize_int8", "fwt_int8_matmul_workspace", "fwt_int8_matmul",
-                   "fwt_grouped_matmul_workspace", "fwt_grouped_matmul",
-                   "fwt_grouped_matmul_backward_workspace", "fwt_grouped_matmul_backward")
+                   "fwt_grouped_matmul_workspace", "fwt_grouped_matmul_workspace_for",
+                   "fwt_grouped_matmul", "fwt_grouped_matmul_backward_workspace",
+                   "fwt_grouped_matmul_backward_workspace_for", "fwt_grouped_matmul_backward")
 
 _lib = None
 # of torch, set by _load
@@ -52,9 +53,13 @@ def _load():
         lib.fwt_int8_matmul.argtypes = [vp, i64, vp, vp, i64, vp, i64, i64, i64, vp, i32, i64, vp,
                                         sz, vp]
         lib.fwt_grouped_matmul_workspace.argtypes = [i32, i64, i64, i64, i64, psz]
+        lib.fwt_grouped_matmul_workspace_for.argtypes = [vp, i64, vp, i64, i64, i64, i32, i64, i64,
+                                                         i64, psz]
         lib.fwt_grouped_matmul.argtypes = [vp, i64, vp, vp, i64, i64, vp, vp, i64, i32, i64, i64,
                                            i64, vp, i32, i64, i32, vp, sz, vp]
         lib.fwt_grouped_matmul_backward_workspace.argtypes = [i64, i64, i64, i64, psz]
+        lib.fwt_grouped_matmul_backward_workspace_for.argtypes = [
+            vp, i64, vp, i64, i64, i64, vp, i64, i64, i64, i64, i32, i32, psz]
         lib.fwt_grouped_matmul_backward.argtypes = [vp, i64, vp, i64, i64, vp, i64, vp, i64, i32,
                                                     i64, i64, i64, vp, i64, vp, i64, i64, vp, sz,
                                                     vp]
@@ -222,6 +227,10 @@ def grouped_matmul(x, w, ends, x_scales=None, w_scales=None, out_dtype=None, out
         _ffn._raise(lib.fwt_grouped_matmul_workspace(_types[x.dtype], experts, m, n, k,
                                                      ctypes.byref(size)),
                     "fwt_grouped_matmul_workspace")
+        if k % 8 and size.value >= 2 * (m + experts * n) * k:      # (copies may be in it)
+            _ffn._raise(lib.fwt_grouped_matmul_workspace_for(
+                x.data_ptr(), ldx, w.data_ptr(), ldw, between, experts, _types[x.dtype], m, n, k,
+                ctypes.byref(size)), "fwt_grouped_matmul_workspace_for")
         need = size.value
     handle, where = _ffn._on(stream, dev, x, w, ends, x_scales, w_scales, out)
     with where:
@@ -250,6 +259,11 @@ def grouped_matmul_backward(x, w, ends, grad, stream=None):
     size = ctypes.c_size_t(0)
     _ffn._raise(lib.fwt_grouped_matmul_backward_workspace(experts, m, n, k, ctypes.byref(size)),
                 "fwt_grouped_matmul_backward_workspace")
+    copies = (2 * (m + experts * n) * k if k % 8 else 0) + (2 * m * n if n % 8 else 0)
+    if copies and size.value >= copies:                  # (they may be in it)
+        _ffn._raise(lib.fwt_grouped_matmul_backward_workspace_for(
+            x.data_ptr(), ldx, w.data_ptr(), ldw, between, experts, grad.data_ptr(), ldd, m, n, k,
+            1, 1, ctypes.byref(size)), "fwt_grouped_matmul_backward_workspace_for")
     handle, where = _ffn._on(stream, dev, x, w, ends, grad)
     with where:
         dx = x.new_empty((m, k))

@@ -174,6 +174,62 @@ def test_backward_refusals(L):
         assert backward(L, **bad) == EUNSUPPORTED, bad
 
 
+def test_scratch_for_copies_is_that_of_misaligned_operands(L):
+    gm, gf = L.fwt_grouped_matmul_workspace, L.fwt_grouped_matmul_workspace_for
+    bm, bf = L.fwt_grouped_matmul_backward_workspace, L.fwt_grouped_matmul_backward_workspace_for
+    e, m, n, k = 8, 16000, 4001, 4095
+    row = lambda cols: 2 * (-(-cols // 8) * 8)                                    # noqa: E731
+    pad, odd, A, O = 4096, 4095, 1 << 32, (1 << 32) + 2
+    all_x, all_w, all_dy = m * row(k), e * n * row(k), m * row(n)
+
+    def fwd(x=A, ldx=pad, w=A, ldw=pad, sw=n * pad, dtype=BF16):
+        st, b = size(gf, x, ldx, w, ldw, sw, e, dtype, m, n, k)
+        assert st == OK
+        return b
+
+    assert size(gm, BF16, e, m, n, k) == (OK, all_x + all_w)
+    assert fwd() == 0 and fwd(x=None, w=None) == 0
+    assert fwd(dtype=INT8) == 0
+    assert fwd(ldx=odd) == all_x and fwd(x=O) == all_x
+    assert fwd(ldw=odd, sw=n * odd) == all_w and fwd(w=O) == all_w and fwd(sw=n * pad + 1) == all_w
+    assert fwd(ldx=odd, w=O) == all_x + all_w
+
+    def bwd(x=A, ldx=pad, w=A, ldw=pad, sw=n * pad, dy=A, lddy=4008, dx=1, dw=1):
+        st, b = size(bf, x, ldx, w, ldw, sw, e, dy, lddy, m, n, k, dx, dw)
+        assert st == OK
+        return b
+
+    up = lambda b: -(-b // 256) * 256                                               # noqa: E731
+    assert size(bm, e, m, n, k) == (OK, all_x + all_w + all_dy)
+    assert bwd() == 0 and bwd(dx=0, dw=0, dy=O) == 0
+    assert bwd(x=O, w=O, dy=O) == all_x + all_w + all_dy
+    assert bwd(x=O) == all_x and bwd(x=O, dw=0) == 0 and bwd(w=O, dx=0) == 0
+    assert bwd(dy=O) == all_dy and bwd(dy=O, x=O, dx=0) == all_dy + all_x
+    # with one expert the stride between experts does not count
+    assert size(gf, A, pad, A, pad, 7, 1, BF16, m, n, k) == (OK, 0)
+    # never more than for any operands; sums are shared whatever lies where
+    for e, m, n, k in ((2, 100, 100, 16000), (3, 3604, 1019, 3373), (1, 300, 200, 9001),
+                       (4, 8000, 2001, 2001), (1, 16384, 64, 64), (32, 4000, 2001, 1501)):
+        most, most_b = size(gm, BF16, e, m, n, k)[1], size(bm, e, m, n, k)[1]
+        for x in (A, A + 4, O):
+            for w in (A, A + 4, O):
+                b = size(gf, x, k, w, k, n * k, e, BF16, m, n, k)
+                assert b[0] == OK and b[1] <= most
+                for dy in (A, O):
+                    for want in (1, 2, 3):
+                        b = size(bf, x, k, w, k, n * k, e, dy, n, m, n, k, want & 1, want & 2)
+                        assert b[0] == OK and b[1] <= most_b
+    # sizes past what there is
+    assert size(gm, BF16, 1 << 16, 1 << 6, 1 << 20, (1 << 20) - 1)[0] == OK
+    for bad in (dict(e=0), dict(m=-1), dict(k=0), dict(dtype=F32)):
+        a = dict(dict(e=2, m=4, n=8, k=64, dtype=BF16), **bad)
+        assert size(gf, A, 64, A, 64, 512, a["e"], a["dtype"], a["m"], a["n"], a["k"])[0] == EINVAL
+        if "dtype" not in bad:
+            assert size(bf, A, 64, A, 64, 512, a["e"], A, 8, a["m"], a["n"], a["k"], 1, 1)[0] == EINVAL
+    assert gf(A, 64, A, 64, 512, 2, BF16, 4, 8, 64, None) == EINVAL
+    assert bf(A, 64, A, 64, 512, 2, A, 8, 4, 8, 64, 1, 1, None) == EINVAL
+
+
 def test_host_tensors_are_refused(L):
     import torch
     x = torch.zeros(4, 64, dtype=torch.bfloat16)

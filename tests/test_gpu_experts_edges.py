@@ -260,6 +260,36 @@ def test_copied_operands_scratch_and_parts():
     assert asked > 16 << 20          # (copies are among them)
 
 
+def test_aligned_rows_take_no_scratch_for_copies():
+    # sizes whose misaligned operands are copied, here in rows of multiples of 16 bytes:
+    # a call allocates its results; one misaligned operand, room for that one more
+    say("no scratch for copies")
+    counts, rest, n, k = COPIED[0]
+    m, e = sum(counts) + rest, len(counts)
+    x, w = torch.randn(m, k, device="cuda").bfloat16(), torch.randn(e, n, k, device="cuda").bfloat16()
+    dy = torch.randn(m, n, device="cuda").bfloat16()
+    xs, ws, ds, ends = in_padding(x), in_padding(w), in_padding(dy), ends_of(counts)
+
+    def peak(call):
+        call()
+        torch.cuda.synchronize()
+        before = torch.cuda.memory_allocated()
+        torch.cuda.reset_peak_memory_stats()
+        out = call()
+        del out
+        return torch.cuda.max_memory_allocated() - before
+
+    results = 2 * m * n
+    some = 1 << 20                    # (of the allocator's)
+    assert peak(lambda: qse.grouped_matmul(xs, ws, ends)) <= results + some
+    with_x = peak(lambda: qse.grouped_matmul(x, ws, ends))
+    with_both = peak(lambda: qse.grouped_matmul(x, w, ends))
+    copy = 2 * m * cdiv(k, 8) * 8
+    assert with_x <= results + copy + some and with_both > results + copy + some
+    grads = 2 * (m + e * n) * k
+    assert peak(lambda: qse.grouped_matmul_backward(xs, ws, ends, ds)) <= grads + 2 * some
+
+
 def test_copied_operands_that_begin_at_one_place():
     # x and grad are views of one buffer, of different widths
     say("copied, one place")
