@@ -131,6 +131,17 @@ def _out_dtype(out_dtype, out):
     return dtype
 
 
+def _may_share(m, n, k, dtype):
+    """Whether a grouped product could want scratch for shares of its steps.  Up to 16
+    rows run in strips until these take longer than the second launch that shares need
+    (calls, microseconds without and with: bf16 m 1 e 1 n 64 k 16384 20.0 and 15.4, m 2
+    e 2 n 256 k 8192 12.0 and 15.4; kernels: int8 m 12 e 1 n 213 k 32608 21.3 and 10.3,
+    m 3 e 29 n 346 k 11328 8.0 and 10.9)."""
+    if m > 16:
+        return _ffn._may_share(m, n, k)
+    return k >= (28672 if dtype is _i8 else 14336) and m * n <= 1 << 21
+
+
 def rotate_quantize_int8(x, bits=0, stream=None):
     """8-bit integers and scales of ``x (I (x) H_bits) 2^(-bits/2)``.
 
@@ -222,7 +233,7 @@ def grouped_matmul(x, w, ends, x_scales=None, w_scales=None, out_dtype=None, out
             raise ValueError("the output has the operands' dtype")
     _no_graph("grouped_matmul", x, w, x_scales, w_scales, out)
     need = 0
-    if _ffn._may_share(m, n, k) or (k % 8 and x.dtype is not _i8):
+    if _may_share(m, n, k, x.dtype) or (k % 8 and x.dtype is not _i8):
         size = ctypes.c_size_t(0)
         _ffn._raise(lib.fwt_grouped_matmul_workspace(_types[x.dtype], experts, m, n, k,
                                                      ctypes.byref(size)),

@@ -609,6 +609,51 @@ def test_outputs_count_as_written():
     assert out._version > before
 
 
+@pytest.mark.parametrize("dtype,counts,n,k", [
+    ("bf16", [8], 512, 16384), ("f16", [16], 128, 16384), ("bf16", [3, 0, 6, 1], 48, 18448),
+    ("bf16", [1], 40, 30000), ("int8", [12], 213, 32608), ("int8", [4, 0, 9], 92, 28672),
+    ("bf16", [2, 3], 100, 12345),
+])
+def test_few_rows_share_a_long_contraction(dtype, counts, n, k):
+    # the binding offers the scratch that the library wants for up to 16 rows too, so its
+    # results are the bits of a call through the entry point that has it
+    say("few rows, long contraction", dtype, counts, n, k)
+    L = experts._load()
+    m, e, g = sum(counts), len(counts), gen(n)
+    kw = {}
+    if dtype == "int8":
+        x, w = codes(g, m, k), codes(g, e, n, k)
+        kw = dict(x_scales=some_scales(g, m), w_scales=some_scales(g, e, n))
+    else:
+        x = torch.randn(m, k, generator=g, device="cuda").to(DT[dtype])
+        w = (torch.randn(e, n, k, generator=g, device="cuda") * k ** -0.5).to(DT[dtype])
+    ends, size, code = ends_of(counts), ctypes.c_size_t(), {"bf16": 0, "f16": 1, "int8": 5}[dtype]
+    assert L.fwt_grouped_matmul_workspace(code, e, m, n, k, ctypes.byref(size)) == 0
+    assert size.value > 1 << 19
+    ws = torch.empty(size.value, dtype=torch.uint8, device="cuda")
+    out = 1 if dtype == "f16" else 0
+    want = torch.empty(m, n, dtype=DT["f16" if out else "bf16"], device="cuda")
+    ptr = lambda t: None if t is None else t.data_ptr()                             # noqa: E731
+    assert L.fwt_grouped_matmul(
+        x.data_ptr(), k, ptr(kw.get("x_scales")), w.data_ptr(), k, n * k, ptr(kw.get("w_scales")),
+        ends.data_ptr(), e, code, m, n, k, want.data_ptr(), out, n, 1, ws.data_ptr(), size.value,
+        torch.cuda.current_stream().cuda_stream) == 0
+    del ws
+    torch.cuda.synchronize()
+    before = torch.cuda.memory_allocated()
+    torch.cuda.reset_peak_memory_stats()
+    y = qse.grouped_matmul(x, w, ends, **kw)
+    assert torch.cuda.max_memory_allocated() - before >= size.value
+    assert torch.equal(y, want)
+    for i, lo, hi in group_bounds(counts):
+        if hi > lo and dtype == "int8":
+            assert torch.equal(y[lo:hi], int8_result(x[lo:hi], kw["x_scales"][lo:hi], w[i],
+                                                     kw["w_scales"][i], torch.bfloat16))
+        elif hi > lo:
+            a, b = x[lo:hi].double(), w[i].double()
+            check_sums(y[lo:hi], a @ b.t(), a.abs() @ b.abs().t(), k, x.dtype)
+
+
 def test_operands_with_tangents_are_refused():
     say("tangents")
     from torch.autograd import forward_ad
