@@ -392,7 +392,7 @@ hipError_t run_grouped(ProductArgs p, const GroupArgs& g, int splits, hipStream_
     e = hipGetLastError();
     if (splits == 1 || e != hipSuccess)
         return e;
-    if constexpr (BM <= 128 && BN <= 128)
+    if constexpr (may_split<TYPE, BM, BN>())
         hipLaunchKernelGGL((grouped_join_kernel<TYPE, BM, BN, WM, WN>),
                            dim3(tiles, BM / WM / 16, BN / WN / 16), dim3(64 * WM * WN), 0, stream, p,
                            g);

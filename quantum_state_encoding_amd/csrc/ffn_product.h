@@ -945,6 +945,13 @@ __global__ __launch_bounds__(64 * WM * WN) void join_kernel(const ProductArgs p)
     join_body<TYPE, BM, BN, WM, WN, EP, AT, WIDE>(p, EveryWorkgroup{});
 }
 
+// Tiles whose steps the choices below share: none of 256, of 8-bit integers the smallest.
+template <int TYPE, int BM, int BN>
+constexpr bool may_split()
+{
+    return TYPE == kTI8 ? BM == 64 && BN == 64 : BM <= 128 && BN <= 128;
+}
+
 template <int TYPE, int BM, int BN, int WM, int WN, int WK, int NS, int EP, int SM, int REG = kAligned,
           bool AT = false, bool BT = false, bool PIPE = false, bool WIDE = PIPE>
 hipError_t run(ProductArgs p, int splits, hipStream_t stream)
@@ -978,7 +985,7 @@ hipError_t run(ProductArgs p, int splits, hipStream_t stream)
     }
     if (splits == 1 || e != hipSuccess)
         return e;
-    if constexpr (BM <= 128 && BN <= 128) {      // (larger tiles are never split)
+    if constexpr (may_split<TYPE, BM, BN>()) {
         const dim3 grid(tiles, BM / WM / 16, BNO / WN / 16);
         hipLaunchKernelGGL((join_kernel<TYPE, BM, BN, WM, WN, EP, AT, WIDE>), grid, dim3(64 * WM * WN), 0,
                            stream, p);

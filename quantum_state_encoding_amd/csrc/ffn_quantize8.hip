@@ -220,6 +220,7 @@ template <int TYPE, int BITS, bool ONE, bool TWICE>
 __global__ __launch_bounds__(ONE ? 1024 : 256) void quantize8_kernel(const Quantize8Args p,
                                                                      float norm, int shift)
 {
+    static_assert(ONE || (BITS >= 5 && BITS <= 11), "a wave's row, in 32 neighbours of a lane");
     extern __shared__ __align__(16) float lds[];
     __shared__ unsigned tops[16];
     const int t = threadIdx.x, lane = t & 63;
@@ -315,10 +316,12 @@ hipError_t run(const Quantize8Args& p, float norm, hipStream_t stream)
 {
     const dim3 grid((unsigned)quantize8_groups(p.m, p.k));
     constexpr size_t kLds = BITS > 5 ? (size_t)kWaveRow * 4 : 0;    // of a wave
-    if (p.k <= kWaveRow) {
-        hipLaunchKernelGGL((quantize8_kernel<TYPE, BITS, false, false>), grid, dim3(256), 4 * kLds,
-                           stream, p, norm, shift_of(p.k));
-        return hipGetLastError();
+    if constexpr (BITS >= 5 && BITS <= 11) {     // (2^12 and more are longer, BITS 4 is for those)
+        if (p.k <= kWaveRow) {
+            hipLaunchKernelGGL((quantize8_kernel<TYPE, BITS, false, false>), grid, dim3(256),
+                               4 * kLds, stream, p, norm, shift_of(p.k));
+            return hipGetLastError();
+        }
     }
     const bool twice = p.k > kRowMax;
     const int waves = twice ? 16 : (int)((p.k + kWaveRow - 1) / kWaveRow);

@@ -230,6 +230,22 @@ def test_scratch_for_copies_is_that_of_misaligned_operands(L):
     assert bf(A, 64, A, 64, 512, 2, A, 8, 4, 8, 64, 1, 1, None) == EINVAL
 
 
+def test_kernels_are_those_that_calls_reach(lib):
+    # rows of up to 2048 elements take rotations of up to 2^11, which 32 neighbours of a
+    # lane hold from the start; the layout for shorter rotations is one of long rows
+    built = open(qse.library_path(), "rb").read()
+    names = set(re.findall(rb"quantize8_kernelILi(\d)ELi(\d+)ELb([01])ELb([01])E", built))
+    short = {int(bits) for _, bits, one, _ in names if one == b"0"}
+    assert short == set(range(5, 12))
+    for twice in (b"0", b"1"):
+        assert {int(bits) for _, bits, one, two in names
+                if one == b"1" and two == twice} == set(range(4, 15))
+    assert len(names) == 3 * (7 + 11 + 11)
+    # of 8-bit integers, shares of the smallest tiles alone are joined
+    for kernel in (rb"\d\djoin_kernel", rb"grouped_join_kernel"):
+        assert set(re.findall(kernel + rb"ILi5ELi(\d+)ELi(\d+)E", built)) == {(b"64", b"64")}
+
+
 def test_host_tensors_are_refused(L):
     import torch
     x = torch.zeros(4, 64, dtype=torch.bfloat16)
