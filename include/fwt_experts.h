@@ -2,7 +2,7 @@
  * fwt_experts.h - 8-bit integer products and products grouped by expert,
  * around the Walsh-Hadamard rotation, on MI355X (gfx950).
  *
- * The feed-forward block of fwt_ffn.h for models with experts, and for 8-bit
+ * Products of fwt_ffn.h's feed-forward block for models with experts, and for 8-bit
  * integers with one scale for a whole row (a token of activations, a channel
  * of weights), which leaves the sums of a product exact.  Four operators:
  *

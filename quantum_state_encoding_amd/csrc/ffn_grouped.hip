@@ -10,10 +10,10 @@
 // 1.45 us, 1.12 on operands of zeros) and the groups' last tiles, which are half
 // empty in the mean and take 0.7 of a whole one's time when at most half of their rows
 // exist; a round of tiles takes about 9 us beside its steps.  Few rows: the weights'
-// bytes.  Measured, groups uneven: bf16 m 16384 e 8 n 8192 k 4096 900-975 us by the
-// card, 1.13-1.22 PFLOP/s (library product 1.46), int8 e 32 n 4096 333-348; gradients
-// e 16 n 4096 k 4096 1080-1145 (both 550-590); bf16 one row for each of 32 experts'
-// places, e 64 n 2048 k 4096, 71-73 us, 5.5 TB/s.
+// bytes.  Measured by the card, groups uneven: bf16 m 16384 e 8 n 8192 k 4096 895-960 us,
+// 1.15-1.23 PFLOP/s (library product 1.46), int8 e 32 n 4096 330-356; gradients
+// e 16 n 4096 k 4096 1069-1145 (dx 528-554, dw 557-587); bf16 one row for each of 32
+// experts' places, e 64 n 2048 k 4096, 66-73 us, 5.8 TB/s.
 #include <hip/hip_runtime.h>
 
 #include "ffn_product.h"
@@ -437,11 +437,12 @@ hipError_t run_grad(ProductArgs p, const GroupArgs& g, int splits, hipStream_t s
 // and the bytes at 6.5 TB/s, at any address 2.5, 2.7 and 3.8 (at multiples of four bytes
 // 3.7, 4.6 and 5.0, and steps of 1.85, 1.1, 0.62 and 1.3).
 // How the rows are spread is not known: a group is taken to have the average
-// number, and half a tile of rows more than it fills.  Over 53 sizes (4 to 64
-// experts, 0.5 to 2048 rows for each, unevenly) the choice takes 1.5 % longer than
-// the best tile in the mean, at most 16 %.  Where most of a round's slots are empty
-// the workgroups of a tile may share its steps, for a second launch and their sums'
-// bytes.
+// number, and half a tile of rows more than it fills.  Over 60 sizes (4 to 64
+// experts, half a row to 2048 rows for each, unevenly; forward, gradients and 8 bits) the
+// choice takes 4.4 % longer than the best tile in the mean, at most 31 % (dx of rows at
+// odd addresses, m 7231 e 23 n 2327 k 3109: 244 us, 186 with 256 x 256).  Where most of
+// a round's slots are empty the workgroups of a tile may share its steps, for a second
+// launch and their sums' bytes.
 struct GroupTile {
     int bm, bn, slots;
     float step, round;

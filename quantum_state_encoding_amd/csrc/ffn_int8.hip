@@ -3,10 +3,11 @@
 // ffn_strip.hip's strips.  The sums are 32-bit integers, exact, so neither the
 // tile nor the number of shares changes a result; the scales are the epilogue.
 //
-// Measured: m 8192 n 4096 k 16384 400-425 us by the card, 2.6-2.7 P operations/s
-// (the library's 8192^3 on one of them: 2.16), the matrix units busy 67 % of the
+// Measured: m 8192 n 4096 k 16384 401-431 us by the card, 2.55-2.74 P operations/s
+// (the library's 8192^3 on one of them: 2.16), the matrix units busy 65 % of the
 // cycles; m 333 n 4100 k 2056 11.9 us, one tile's first loads, 17 steps and stores;
-// one token, n 16384 k 4096, 12.2 us, the weights' bytes (5.5 TB/s).
+// one token, n 16384 k 4096, 12.2 us where the weights are in the caches (5.5 TB/s),
+// 18.6 where they are not.
 #include <hip/hip_runtime.h>
 
 #include "ffn_product.h"
@@ -51,7 +52,13 @@ hipError_t tiles_int8(const ProductArgs& p, size_t* query, hipStream_t stream)
     return run_int8<64, 64, 2, 2, 2, 4>(p, c.splits, stream);
 }
 
-// Few rows of A.
+// Few rows of A, unless the tiles fill the CUs.  Microseconds in strips and in tiles, of 1,
+// 16 and 32 rows, weights from memory: n 1024 k 4096 4.9 7.5, 6.4 7.5, 8.3 7.6; n 4096
+// k 4096 6.3 10.6, 8.1 10.6, 9.5 10.7; n 8192 k 8192 15.2 22.1, 21.2 22.2, 26.4 22.7; and
+// where tiles are taken, n 16384 k 4096 15.5 18.6, 21.1 19.2, 26.0 19.6; n 32768 k 4096
+// 27.9 35.1, 36.4 36.5, 47.6 36.8; n 65536 k 2048 32.0 29.3, 38.5 30.7, 47.8 31.6.  (The
+// number of rows has a say too, which the rule leaves out: up to a quarter, for one row of
+// n 32768.)
 bool strips(const ProductArgs& p) { return p.m <= kStripRows && (p.n + 63) / 64 < 256; }
 
 template <int MT, int W, int U>

@@ -58,7 +58,9 @@ __device__ __forceinline__ void tile_of(int w, int tiles_m, int tiles_n, int& tm
 // 32 bytes each, so those 32-byte units are spread over the banks by k.
 __device__ __forceinline__ int unit_mask(int k) { return (k & 3) | ((k >> 3) & 1) << 2; }
 
-// WIDE: the block's rows are every second four of 32 (wide_row).
+// WIDE: the block's rows are every second four of 32 (wide_row).  A lane then takes eight
+// bytes of every sixteen of two units, so the masks m and m ^ 1 of two k send them to the
+// same banks: two ways, 6 to 7 % of the cycles of grouped gradients (none without WIDE).
 template <int BR, bool WIDE = false>
 __device__ __forceinline__ v4i read_t_half(const unsigned char* tile, int block, int lane, int h)
 {

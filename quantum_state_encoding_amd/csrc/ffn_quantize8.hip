@@ -7,13 +7,13 @@
 //
 // The scale needs all of a row before its first code, so a row's rotated values
 // stay in registers, 32 a lane, a wave for every 2048, until its waves have
-// joined their maxima: one pass over memory, which bounds it up to 2^5; beyond that
-// vector instructions come close (2^14: 96 % of the CUs' cycles).  Kernel times, and
-// at a large copy's rate (4.95 TB/s): fp32 4100 x 5000, 2^3 20.8 us (20.7); bf16
-// 8192 x 4096, 2^0 19, 2^5 22, 2^7 26, 2^10 27, 2^12 33 (20.3); bf16 8192 x 16384,
-// 2^14 90-95 (81), fp32 139 (136).  Rows above 32768 elements (1024 lanes) are
-// rotated twice, for the maximum and for the codes (bf16 1024 x 65536, 2^10: 90 us,
-// 41 at that rate).
+// joined their maxima: one pass over memory, which bounds short rotations; from 2^5 on
+// vector instructions do, 18 to 22 an element (2^5, 2^10 and 2^12 of 8192 x 4096: 94 to
+// 100 % of the CUs' cycles, 2^14 96 %).  Kernel times, and at a large copy's rate
+// (4.95 TB/s): fp32 4100 x 5000, 2^3 17-20 us (20.7); bf16 8192 x 4096, 2^0 18, 2^5 22,
+// 2^7 22, 2^10 23, 2^12 23 (20.3), 2048 x 16384, 2^12 26; bf16 8192 x 16384, 2^14 89-95
+// (81), fp32 119-139 (136).  Rows above 32768 elements (1024 lanes) are rotated twice,
+// for the maximum and for the codes (bf16 1024 x 65536, 2^10: 85-90 us, 41 at that rate).
 // The rotations run in ffn_rotate.hip's layouts:
 //   b <= 4        twice 16 neighbours of a lane (rows of up to 2048 elements, and
 //                 b = 5: 32 neighbours), register stages
